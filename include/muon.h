@@ -261,6 +261,21 @@ muon_status muon_plan_set_weights(muon_plan* plan, const muon_weight* w, int32_t
 muon_status muon_plan_step_apply(muon_plan* plan, const muon_config* cfg, const muon_apply* ap,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- gradient factor in device memory -----------------------------------
+ *
+ * Attaches a factor to a plan (NULL detaches it): every later step of the
+ * plan (muon_plan_step, _step_noalloc, _step_apply) reads *scale when it runs
+ * and uses G' = G * *scale in place of G, a float32 product that is not
+ * rounded to the set's dtype (buf' = mu * buf + G' still is, once). With
+ * `scale` of a muon_clip_result (muon_clip.h) this is the Muon step on
+ * gradients clipped by their global norm, without a pass that writes them.
+ * A factor of one gives the results of a plan without one, bit for bit.
+ * `grad` is only read. *scale must stay valid while attached and be written
+ * before the step on the step's stream (or ordered before it); a captured
+ * graph keeps the pointer it was captured with. MUON_E_ALIGN if scale is
+ * not 4-byte aligned. muon_step and muon_orthogonalize have no factor. */
+muon_status muon_plan_set_grad_scale(muon_plan* plan, const float* scale);
+
 /* ---- introspection (tests, benchmarks, profiling) ---------------------- */
 
 /* Kernels of one step, in launch order: momentum, normalise, then per

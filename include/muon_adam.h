@@ -78,6 +78,17 @@ muon_status muon_adam_plan_create(const muon_adam_tensor* ts, int32_t n, muon_dt
  * kernel launch). */
 muon_status muon_adam_plan_step(muon_adam_plan* plan, const muon_adam_config* cfg, void* stream);
 
+/* Attaches a gradient factor in device memory (NULL detaches it): every
+ * later muon_adam_plan_step reads *scale when it runs and uses g * *scale
+ * (a float32 product, before any other arithmetic) for each gradient, so a
+ * list clipped by its global norm (`scale` of a muon_clip_result,
+ * muon_clip.h) needs no pass that writes clipped gradients. A factor of one
+ * gives the results of a plan without one, bit for bit. *scale must stay
+ * valid while attached and be written before the step on the step's stream
+ * (or ordered before it); a captured graph keeps the pointer it was captured
+ * with. MUON_E_ALIGN if scale is not 4-byte aligned. */
+muon_status muon_adam_plan_set_grad_scale(muon_adam_plan* plan, const float* scale);
+
 /* Frees a plan after waiting for the device (NULL is a no-op). */
 void muon_adam_plan_destroy(muon_adam_plan* plan);
 

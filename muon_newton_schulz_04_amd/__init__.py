@@ -25,6 +25,10 @@ __all__ = [
     "muon_plan_step_noalloc", "MUON_SCRATCH_BYTES",
     "MuonAdamTensor", "MuonAdamConfig", "AdamPlan", "muon_adam_plan_create",
     "muon_adam_plan_step", "muon_adam_plan_destroy", "muon_adam_work_items",
+    "muon_plan_set_grad_scale", "muon_adam_plan_set_grad_scale",
+    "MuonClipTensor", "MuonClipConfig", "ClipPlan", "muon_clip_plan_create",
+    "muon_clip_plan_norm", "muon_clip_plan_step", "muon_clip_plan_destroy",
+    "muon_clip_workspace_bytes",
     "MUON_F32", "MUON_BF16", "MUON_PRECISION_DEFAULT",
 ]
 
@@ -75,6 +79,16 @@ class MuonAdamConfig(ctypes.Structure):
                 ("eps", ctypes.c_float), ("wd", ctypes.c_float), ("step", ctypes.c_int32)]
 
 
+class MuonClipTensor(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("out_ld", ctypes.c_int64), ("grad", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MuonClipConfig(ctypes.Structure):
+    _fields_ = [("max_norm", ctypes.c_float), ("eps", ctypes.c_float), ("grad_mul", ctypes.c_float)]
+
+
 class MuonBufferInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("m", "n", "mp", "np", "x_lo", "x_op0", "x_op1", "gram", "poly", "x0_scale")]
@@ -117,6 +131,13 @@ def load_library(path: str = LIB_PATH):
         "muon_adam_plan_create": (i32, [P(MuonAdamTensor), i32, i32, P(vp)]),
         "muon_adam_plan_step": (i32, [vp, P(MuonAdamConfig), vp]),
         "muon_adam_plan_destroy": (None, [vp]),
+        "muon_plan_set_grad_scale": (i32, [vp, vp]),
+        "muon_adam_plan_set_grad_scale": (i32, [vp, vp]),
+        "muon_clip_workspace_bytes": (i32, [P(MuonClipTensor), i32, P(sz)]),
+        "muon_clip_plan_create": (i32, [P(MuonClipTensor), i32, P(vp)]),
+        "muon_clip_plan_norm": (i32, [vp, P(MuonClipConfig), vp, vp, vp, sz, vp]),
+        "muon_clip_plan_step": (i32, [vp, P(MuonClipConfig), vp, vp, vp, sz, vp]),
+        "muon_clip_plan_destroy": (None, [vp]),
         "muon_adam_work_items": (i32, [P(MuonAdamTensor), i32, i32, P(i64)]),
     }
     for name, (res, args) in sig.items():
@@ -228,6 +249,15 @@ def _workspace(nbytes: int, device, workspace):
     return workspace
 
 
+def _scale_ptr(t, device) -> Optional[int]:
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != 1 or not t.is_cuda or device not in (None, t.device):
+        raise ValueError("the gradient scale is one float32 element on the plan's device")
+    return t.data_ptr()
+
+
 # ---------------------------------------------------------------- entry points
 
 def muon_workspace_bytes(mats, dtype: Optional[int] = None) -> int:
@@ -320,6 +350,14 @@ class MuonPlan:
                "muon_plan_step_apply")
         return ws
 
+    def set_grad_scale(self, scale):
+        """Later steps use grad * scale, ``scale`` a one-element float32 tensor on the
+        plan's device that is read when the step runs (e.g. ``ClipPlan.scale``);
+        None detaches it."""
+        p = _scale_ptr(scale, self.device)
+        _check(load_library().muon_plan_set_grad_scale(self.handle, p), "muon_plan_set_grad_scale")
+        self._grad_scale = scale
+
     def set_timing(self, mode):
         """0 / False: off; 1 / True: each kernel over the whole set in its own
         timed launch; 2: the step's own launches timed as they run."""
@@ -399,6 +437,10 @@ def muon_plan_step_apply(plan: MuonPlan, cfg: MuonConfig, lr: float, wd: float, 
 
 def muon_plan_step_noalloc(plan: MuonPlan, cfg: MuonConfig, stream=None):
     return plan.step_noalloc(cfg, stream)
+
+
+def muon_plan_set_grad_scale(plan: MuonPlan, scale):
+    plan.set_grad_scale(scale)
 
 
 def muon_plan_set_timing(plan: MuonPlan, mode):
@@ -507,6 +549,13 @@ class AdamPlan:
         _check(lib.muon_adam_plan_create(arr, n, dt, ctypes.byref(h)), "muon_adam_plan_create")
         self.handle = h
 
+    def set_grad_scale(self, scale):
+        """Later steps use grad * scale (see ``MuonPlan.set_grad_scale``)."""
+        p = _scale_ptr(scale, self._keep[0][0].device if self._keep[0] else None)
+        _check(load_library().muon_adam_plan_set_grad_scale(self.handle, p),
+               "muon_adam_plan_set_grad_scale")
+        self._grad_scale = scale
+
     def step(self, lr: float, beta1: float, beta2: float, eps: float, wd: float, step: int,
              stream=None):
         cfg = MuonAdamConfig(float(lr), float(beta1), float(beta2), float(eps), float(wd), int(step))
@@ -534,4 +583,169 @@ def muon_adam_plan_step(plan: AdamPlan, lr, beta1, beta2, eps, wd, step, stream=
 
 
 def muon_adam_plan_destroy(plan: AdamPlan):
+    plan.destroy()
+
+
+def muon_adam_plan_set_grad_scale(plan: AdamPlan, scale):
+    plan.set_grad_scale(scale)
+
+
+# ------------------------------------------- global gradient norm and clipping
+
+def _row_layout(t):
+    """(rows, cols, ld, order of the dimensions) of a tensor whose elements lie in
+    rows of consecutive elements at one stride: any dense tensor (also a permuted
+    one) is one row, a 2-D view with a unit stride has its own rows."""
+    dims = sorted((d for d in range(t.dim()) if t.shape[d] != 1), key=lambda d: t.stride(d))
+    cols, ld, rows = 1, None, 1
+    for d in dims:
+        n, st = t.shape[d], t.stride(d)
+        if ld is None and st == cols:
+            cols *= n
+        elif ld is None and st > cols:
+            ld, rows = st, n
+        elif ld is not None and st == ld * rows:
+            rows *= n
+        else:
+            raise ValueError("a gradient must be rows of consecutive elements at one row stride")
+    return rows, cols, cols if ld is None else ld, dims
+
+
+def _clip_tensors(grads, outs):
+    """muon_clip_tensor array from lists of torch tensors (``outs`` None: in place;
+    an entry None: the norm only)."""
+    n = len(grads)
+    outs = list(grads) if outs is None else list(outs)
+    if len(outs) != n:
+        raise ValueError("grads and outs must have the same length")
+    arr = (MuonClipTensor * max(n, 1))()
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        dt = _dtype_code(g)
+        if g.device != grads[0].device or (o is not None and o.device != g.device):
+            raise ValueError("all tensors of a list must be on one device")
+        if o is not None and (o.dtype != g.dtype or o.shape != g.shape):
+            raise ValueError("an out must match its grad's shape and dtype")
+        if g.numel() == 0:
+            arr[i] = MuonClipTensor(0, 0, 0, 0, None, None, dt, 0)
+            continue
+        rows, cols, ld, dims = _row_layout(g)
+        old = ld
+        if o is not None:
+            # the two are walked side by side: rows of the same length, the dimensions in the same order
+            r2, c2, old, dims2 = _row_layout(o)
+            if dims2 != dims:
+                raise ValueError("an out must order its dimensions as its grad does")
+            if (r2, c2) != (rows, cols):
+                if c2 == rows * cols:       # out is dense, grad has rows
+                    old = cols
+                elif cols == r2 * c2:       # grad is dense, out has rows
+                    rows, cols, ld = r2, c2, c2
+                else:
+                    raise ValueError("grad and out must split into the same rows")
+        arr[i] = MuonClipTensor(rows, cols, ld, old, _ptr(g), _ptr(o), dt, 0)
+    return arr, n
+
+
+def muon_clip_workspace_bytes(grads, outs=None) -> int:
+    arr, n = _clip_tensors(grads, outs)
+    out = ctypes.c_size_t(0)
+    _check(load_library().muon_clip_workspace_bytes(arr, n, ctypes.byref(out)),
+           "muon_clip_workspace_bytes")
+    return out.value
+
+
+class ClipPlan:
+    """Global norm of a fixed list of gradients (bf16 and float32 may be mixed) and
+    clipping by it. ``outs`` None clips in place; a list of tensors receives the
+    clipped gradients (an entry None: that gradient only counts in the norm).
+
+    ``result`` holds {norm, scale} of the last call on the device, ``scale`` is a view of
+    its second element (what ``set_grad_scale`` of the optimizer plans takes)."""
+
+    def __init__(self, grads, outs=None):
+        import torch
+        lib = load_library()
+        grads = list(grads)
+        self._keep = (grads, None if outs is None else list(outs))
+        arr, n = _clip_tensors(grads, outs)
+        self.n = n
+        self.device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        if self.device.type != "cuda":
+            raise ValueError("gradients must be in device memory")
+        self.handle = ctypes.c_void_p(None)
+        ws = ctypes.c_size_t(0)
+        _check(lib.muon_clip_workspace_bytes(arr, n, ctypes.byref(ws)), "muon_clip_workspace_bytes")
+        self.workspace_bytes = ws.value
+        h = ctypes.c_void_p(None)
+        with torch.cuda.device(self.device):
+            _check(lib.muon_clip_plan_create(arr, n, ctypes.byref(h)), "muon_clip_plan_create")
+        self.handle = h
+        self.result = torch.zeros(2, dtype=torch.float32, device=self.device)
+        self.scale = self.result[1:2]
+
+    def _run(self, entry, max_norm, eps, grad_mul, norms, result, workspace, stream):
+        import torch
+        result = self.result if result is None else result
+        for t, k in ((result, 2), (norms, self.n)):
+            if t is not None and (t.dtype != torch.float32 or t.numel() != k or not t.is_contiguous()
+                                  or t.device != self.device):
+                raise ValueError(f"result and norms are contiguous float32 tensors of 2 and {self.n} "
+                                 f"elements on {self.device}")
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        if workspace is None:
+            # allocated and, once dropped, reused in the order of the stream that uses it
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), self.device)
+            with torch.cuda.stream(s):
+                workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+        cfg = MuonClipConfig(float(max_norm), float(eps), float(grad_mul))
+        args = (self.handle, ctypes.byref(cfg), result.data_ptr(), _ptr(norms), workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), _stream_handle(stream))
+        fn = getattr(load_library(), entry)
+        if torch.cuda.current_device() == self.device.index:
+            _check(fn(*args), entry)
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn(*args), entry)
+        return result
+
+    def norm(self, max_norm: float = float("inf"), eps: float = 1e-6, grad_mul: float = 1.0, norms=None,
+             result=None, workspace=None, stream=None):
+        """Writes {norm, scale} into ``result`` (the plan's own unless given) and each
+        tensor's norm into ``norms`` (float32, one per tensor); gradients are only read.
+        Returns ``result``; nothing waits for the device."""
+        return self._run("muon_clip_plan_norm", max_norm, eps, grad_mul, norms, result, workspace, stream)
+
+    def step(self, max_norm: float, eps: float = 1e-6, grad_mul: float = 1.0, norms=None, result=None,
+             workspace=None, stream=None):
+        """``norm``, then every gradient times the scale into its out (in place without outs)."""
+        return self._run("muon_clip_plan_step", max_norm, eps, grad_mul, norms, result, workspace, stream)
+
+    def destroy(self):
+        if self.handle:
+            load_library().muon_clip_plan_destroy(self.handle)
+            self.handle = ctypes.c_void_p(None)
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def muon_clip_plan_create(grads, outs=None) -> ClipPlan:
+    return ClipPlan(grads, outs)
+
+
+def muon_clip_plan_norm(plan: ClipPlan, max_norm=float("inf"), eps=1e-6, grad_mul=1.0, norms=None, result=None,
+                        workspace=None, stream=None):
+    return plan.norm(max_norm, eps, grad_mul, norms, result, workspace, stream)
+
+
+def muon_clip_plan_step(plan: ClipPlan, max_norm, eps=1e-6, grad_mul=1.0, norms=None, result=None, workspace=None,
+                        stream=None):
+    return plan.step(max_norm, eps, grad_mul, norms, result, workspace, stream)
+
+
+def muon_clip_plan_destroy(plan: ClipPlan):
     plan.destroy()

@@ -7,6 +7,8 @@
 // parameters off the Muon path), per element, in fp32:
 //   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
 //   p = p (1 - lr' wd') - (lr' / bc1) m / (sqrt(v) / sqrt(bc2) + eps)
+// g times the plan's gradient factor where it has one (a clipped gradient, read
+// from device memory: no pass of its own over the gradients), and
 // with lr' = lr lr_mul, wd' = wd wd_mul, bc_i = 1 - beta_i^t (the bias-
 // corrected form m/bc1 / (sqrt(v/bc2) + eps), rearranged so that the per-call
 // factors 1/bc1 and 1/sqrt(bc2) are computed once on the host).
@@ -53,6 +55,7 @@ struct Args {
   const Item* items;
   float lr, b1, b2, eps, wd;
   float inv_bc1, inv_sqrt_bc2;  // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+  const float* gscale;          // gradients are multiplied by *gscale (nullptr: by one)
 };
 
 __device__ __forceinline__ float bf2f(uint16_t h) { return __uint_as_float(uint32_t(h) << 16); }
@@ -78,10 +81,12 @@ template <> struct PElem<uint16_t> {
 
 struct Consts {
   float b1, c1, b2, c2, eps, keep, step, isb2;
+  float gs;  // the gradient's factor
 };
 
 // One element: updates m, v in place and returns the new parameter value.
 __device__ __forceinline__ float adam_elem(float p, float g, float& m, float& v, const Consts& k) {
+  g *= k.gs;  // exact for a factor of one
   m = __fmaf_rn(k.b1, m, k.c1 * g);
   v = __fmaf_rn(k.b2, v, k.c2 * (g * g));
   const float denom = __fsqrt_rn(v) * k.isb2 + k.eps;
@@ -193,6 +198,7 @@ __global__ __launch_bounds__(kThreads) void adam_kernel(Args A) {
   k.keep = 1.f - lr_e * (A.wd * t.wd_mul);
   k.step = lr_e * A.inv_bc1;
   k.isb2 = A.inv_sqrt_bc2;
+  k.gs = A.gscale ? *A.gscale : 1.f;
   const int64_t base = int64_t(it.chunk) * kChunk;
   const int64_t end = base + kChunk < t.numel ? base + kChunk : t.numel;
   // two vectors per thread per pass, both loaded before either is updated
@@ -275,6 +281,7 @@ struct muon_adam_plan_s {
   const muon_adam::Tensor* d_ts = nullptr;
   const muon_adam::Item* d_items = nullptr;
   int64_t nitems = 0;
+  const float* gscale = nullptr;  // muon_adam_plan_set_grad_scale
 };
 
 extern "C" {
@@ -349,6 +356,7 @@ muon_status muon_adam_plan_step(muon_adam_plan* plan, const muon_adam_config* cf
   a.b2 = cfg->beta2;
   a.eps = cfg->eps;
   a.wd = cfg->wd;
+  a.gscale = plan->gscale;
   a.inv_bc1 = static_cast<float>(1.0 / (1.0 - std::pow(double(cfg->beta1), double(cfg->step))));
   a.inv_sqrt_bc2 =
       static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(double(cfg->beta2), double(cfg->step))));
@@ -359,6 +367,13 @@ muon_status muon_adam_plan_step(muon_adam_plan* plan, const muon_adam_config* cf
   else
     hipLaunchKernelGGL(muon_adam::adam_kernel<uint16_t>, grid, block, 0, s, a);
   return hipGetLastError() == hipSuccess ? MUON_OK : MUON_E_LAUNCH;
+}
+
+muon_status muon_adam_plan_set_grad_scale(muon_adam_plan* plan, const float* scale) {
+  if (plan == nullptr) return MUON_E_INVALID;
+  if (reinterpret_cast<uintptr_t>(scale) % 4 != 0) return MUON_E_ALIGN;
+  plan->gscale = scale;
+  return MUON_OK;
 }
 
 void muon_adam_plan_destroy(muon_adam_plan* plan) {

@@ -50,6 +50,7 @@ struct muon_plan_s {
   int64_t acc_n[MUON_K_COUNT + 1] = {};
   bool has_weights = false;                   // muon_plan_set_weights succeeded
   void* scratch = nullptr;                    // this device's fixed scratch array
+  const float* gscale = nullptr;              // muon_plan_set_grad_scale
 };
 
 namespace {
@@ -202,6 +203,7 @@ muon_status step_impl(muon_plan_s* p, const muon_config* cfg, void* ws, size_t w
   a.tmax_off = H.tmax_off;
   a.x0s_off = H.x0s_off;
   a.hint = p->d_hint;
+  a.gscale = orthogonalize_only ? nullptr : p->gscale;
   // the chained schedule (not under per-kernel timing, which times each
   // kernel's own launch)
   const bool chain = fused && H.chained && p->chain_ok && p->chain_on && !(p->timing == 1 && allow_timing);
@@ -518,6 +520,13 @@ muon_status muon_plan_step_apply(muon_plan* plan, const muon_config* cfg, const 
   if (st != MUON_OK) return st;
   if (!plan->has_weights) return MUON_E_INVALID;
   return step_impl(plan, cfg, workspace, workspace_bytes, stream, false, ap);
+}
+
+muon_status muon_plan_set_grad_scale(muon_plan* plan, const float* scale) {
+  if (plan == nullptr) return MUON_E_INVALID;
+  if (reinterpret_cast<uintptr_t>(scale) % 4 != 0) return MUON_E_ALIGN;
+  plan->gscale = scale;
+  return MUON_OK;
 }
 
 void muon_plan_destroy(muon_plan* plan) { release(plan); }

@@ -1,0 +1,539 @@
+// Global gradient norm and clipping (include/muon_clip.h): the kernels, the
+// plan (validated list split into work items in device memory) and the C ABI.
+//
+//   N = c sqrt(sum of squares of every element of every tensor)
+//   factor = c min(1, max_norm / (N + eps));  out = g factor
+//
+// The norm reads every gradient once (2 or 4 bytes an element, two flops) and
+// is bound by HBM, or by the launches for small lists. One wave takes one
+// work item, a run of consecutive elements (or of rows of a strided tensor)
+// of one tensor; squares are summed in float64, where a bf16 or fp32 square
+// neither over- nor underflows, so no scaling by a maximum is needed.
+// Partial sums go to fixed slots of the workspace and are added in a fixed
+// order: no atomics, equal inputs give equal bits.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "../../include/muon_clip.h"
+
+namespace muon_clip {
+
+constexpr int kWaves = 4;                 // work items (one per wave) of a block
+constexpr int kThreads = 64 * kWaves;
+constexpr int64_t kMinBytes = 4096;       // smallest work item
+constexpr int64_t kMaxBytes = 1 << 28;    // largest (its element count fits an int32)
+constexpr int64_t kTargetItems = 8192;    // 32 waves on each of the 256 CUs
+constexpr int kReduced = 1024;            // partials of a long list are first added up to this many
+
+// One wave's work: `rows` rows of `n` consecutive elements.
+struct Item {
+  const char* g;
+  char* o;
+  int64_t ld, out_ld;  // elements
+  int32_t n, rows;
+  int32_t dtype;       // muon_dtype
+  int32_t pad_;
+};
+
+struct Range {
+  int32_t beg, end;  // work items of a tensor
+};
+
+struct Args {
+  const Item* items;
+  int32_t n_items;
+  int32_t n_part;      // block sums in `part`
+  double* part;        // one sum per block of the norm kernel
+  double* isum;        // one sum per item (nullptr: not wanted)
+  const Range* ranges; // items of each tensor
+  int32_t n_tensors;
+  float* norms;        // nullptr: not wanted
+  muon_clip_result* res;
+  float max_norm, eps, mul;
+};
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// 16-byte accesses at an element's alignment (the hardware takes any)
+typedef f32x4 f32x4_u __attribute__((aligned(4)));
+typedef u32x4 u32x4_u __attribute__((aligned(2)));
+
+// Element types: V elements to a 16-byte vector.
+struct F32 {
+  typedef float T;
+  typedef f32x4 Vec;
+  typedef f32x4_u VecU;
+  static constexpr int V = 4;
+  static __device__ __forceinline__ float get(const Vec& x, int e) { return x[e]; }
+  static __device__ __forceinline__ float load(const T* p) { return *p; }
+  static __device__ __forceinline__ void store(T* p, float x) { *p = x; }
+  static __device__ __forceinline__ Vec scale(const Vec& x, float s) { return x * s; }
+};
+struct Bf16 {
+  typedef uint16_t T;
+  typedef u32x4 Vec;
+  typedef u32x4_u VecU;
+  static constexpr int V = 8;
+  static __device__ __forceinline__ float get(const Vec& x, int e) {
+    return __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
+  }
+  static __device__ __forceinline__ float load(const T* p) { return __uint_as_float(uint32_t(*p) << 16); }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {  // round to nearest even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+  }
+  static __device__ __forceinline__ void store(T* p, float x) { *p = static_cast<T>(pack(x, 0.f)); }
+  static __device__ __forceinline__ Vec scale(const Vec& x, float s) {
+    Vec y;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) y[q] = pack(get(x, 2 * q) * s, get(x, 2 * q + 1) * s);
+    return y;
+  }
+};
+
+__device__ __forceinline__ double sq(float x) { return double(x) * double(x); }
+
+// Elements before the first 16-byte boundary at or after p, at most n.
+template <typename E>
+__device__ __forceinline__ int head_of(const typename E::T* p, int n) {
+  const int h = static_cast<int>(-reinterpret_cast<uintptr_t>(p) & 15) / static_cast<int>(sizeof(typename E::T));
+  return h < n ? h : n;
+}
+
+// A lane's share of the sum of squares of n consecutive elements.
+template <typename E>
+__device__ __forceinline__ double ssq_run(const typename E::T* p, int n, int lane) {
+  double a = 0.0, b = 0.0;
+  const int head = head_of<E>(p, n);
+  if (lane < head) a = sq(E::load(p + lane));
+  p += head;
+  n -= head;
+  const int nv = n / E::V;
+  const typename E::Vec* v = reinterpret_cast<const typename E::Vec*>(p);
+  constexpr int U = 8;
+  int k = lane;
+  for (; k + 64 * (U - 1) < nv; k += 64 * U) {
+    typename E::Vec x[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) x[j] = v[k + 64 * j];
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int e = 0; e < E::V; e += 2) {
+        a += sq(E::get(x[j], e));
+        b += sq(E::get(x[j], e + 1));
+      }
+  }
+  for (; k < nv; k += 64) {
+    const typename E::Vec x = v[k];
+#pragma unroll
+    for (int e = 0; e < E::V; e += 2) {
+      a += sq(E::get(x, e));
+      b += sq(E::get(x, e + 1));
+    }
+  }
+  const int t = nv * E::V + lane;
+  if (t < n) b += sq(E::load(p + t));
+  return a + b;
+}
+
+template <typename E>
+__device__ __forceinline__ double ssq_item(const Item& it, int lane) {
+  typedef typename E::T T;
+  const T* g = reinterpret_cast<const T*>(it.g);
+  if (it.rows > 1 && it.n < 64 * E::V) {  // short rows: one element a lane, rows one after the other
+    double a = 0.0;
+    const uint32_t all = static_cast<uint32_t>(it.rows) * static_cast<uint32_t>(it.n);
+    for (uint32_t e = lane; e < all; e += 64) {
+      const uint32_t r = e / static_cast<uint32_t>(it.n), c = e - r * static_cast<uint32_t>(it.n);
+      a += sq(E::load(g + int64_t(r) * it.ld + c));
+    }
+    return a;
+  }
+  double a = 0.0;
+  for (int r = 0; r < it.rows; ++r) a += ssq_run<E>(g + int64_t(r) * it.ld, it.n, lane);
+  return a;
+}
+
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+  return x;
+}
+
+__device__ __forceinline__ double block_sum(double x, double* red) {
+  x = wave_sum(x);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) s += red[w];
+  return s;
+}
+
+// Sum of n partials, the same for every thread of the block.
+__device__ __forceinline__ double sum_partials(const double* part, int n, double* red) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) s += part[i];
+  return block_sum(s, red);
+}
+
+__device__ __forceinline__ muon_clip_result result_of(double total, const Args& A) {
+  const double n = sqrt(total) * double(A.mul), d = n + double(A.eps);
+  const double c = d <= double(A.max_norm) ? 1.0 : double(A.max_norm) / d;  // NaN stays NaN
+  return {static_cast<float>(n), static_cast<float>(c * double(A.mul))};
+}
+
+// Sums of squares: block b takes items 4 b .. 4 b + 3, a wave each.
+__global__ __launch_bounds__(kThreads) void clip_norm_kernel(Args A) {
+  __shared__ double red[kWaves];
+  const int lane = threadIdx.x & 63;
+  const int i = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
+  double s = 0.0;
+  if (i < A.n_items) {
+    const Item it = A.items[i];
+    s = wave_sum(it.dtype == MUON_F32 ? ssq_item<F32>(it, lane) : ssq_item<Bf16>(it, lane));
+    if (A.isum != nullptr && lane == 0) A.isum[i] = s;
+  }
+  if (lane == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) t += red[w];
+    A.part[blockIdx.x] = t;
+  }
+}
+
+// Long lists: block b adds up a run of consecutive partials.
+__global__ __launch_bounds__(kThreads) void clip_reduce_kernel(const double* part, double* out, int n, int each) {
+  __shared__ double red[kWaves];
+  const int64_t beg = int64_t(blockIdx.x) * each;
+  const int64_t m = beg < n ? (n - beg < each ? n - beg : each) : 0;
+  const double s = sum_partials(part + beg, static_cast<int>(m), red);
+  if (threadIdx.x == 0) out[blockIdx.x] = s;
+}
+
+// Block 0: the norm and the factor. The others: tensor norms, a wave each.
+__global__ __launch_bounds__(kThreads) void clip_finish_kernel(Args A) {
+  __shared__ double red[kWaves];
+  if (blockIdx.x == 0) {
+    const double s = sum_partials(A.part, A.n_part, red);
+    if (threadIdx.x == 0) *A.res = result_of(s, A);
+    return;
+  }
+  const int64_t t = int64_t(blockIdx.x - 1) * kWaves + (threadIdx.x >> 6);
+  if (t >= A.n_tensors) return;
+  const int lane = threadIdx.x & 63;
+  const Range r = A.ranges[t];
+  double s = 0.0;
+  for (int i = r.beg + lane; i < r.end; i += 64) s += A.isum[i];
+  s = wave_sum(s);
+  if (lane == 0) A.norms[t] = static_cast<float>(sqrt(s) * double(A.mul));
+}
+
+// o = g s for n consecutive elements, aligned on the output.
+template <typename E>
+__device__ __forceinline__ void scale_run(const typename E::T* g, typename E::T* o, int n, float s, int lane) {
+  const int head = head_of<E>(o, n);
+  if (lane < head) E::store(o + lane, E::load(g + lane) * s);
+  g += head;
+  o += head;
+  n -= head;
+  const int nv = n / E::V;
+  const typename E::VecU* v = reinterpret_cast<const typename E::VecU*>(g);
+  typename E::Vec* w = reinterpret_cast<typename E::Vec*>(o);
+  constexpr int U = 4;
+  int k = lane;
+  for (; k + 64 * (U - 1) < nv; k += 64 * U) {
+    typename E::Vec x[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) x[j] = v[k + 64 * j];
+#pragma unroll
+    for (int j = 0; j < U; ++j) w[k + 64 * j] = E::scale(x[j], s);
+  }
+  for (; k < nv; k += 64) {
+    const typename E::Vec x = v[k];
+    w[k] = E::scale(x, s);
+  }
+  const int t = nv * E::V + lane;
+  if (t < n) E::store(o + t, E::load(g + t) * s);
+}
+
+template <typename E>
+__device__ __forceinline__ void scale_item(const Item& it, float s, int lane) {
+  typedef typename E::T T;
+  const T* g = reinterpret_cast<const T*>(it.g);
+  T* o = reinterpret_cast<T*>(it.o);
+  if (it.rows > 1 && it.n < 64 * E::V) {
+    const uint32_t all = static_cast<uint32_t>(it.rows) * static_cast<uint32_t>(it.n);
+    for (uint32_t e = lane; e < all; e += 64) {
+      const uint32_t r = e / static_cast<uint32_t>(it.n), c = e - r * static_cast<uint32_t>(it.n);
+      E::store(o + int64_t(r) * it.out_ld + c, E::load(g + int64_t(r) * it.ld + c) * s);
+    }
+    return;
+  }
+  for (int r = 0; r < it.rows; ++r)
+    scale_run<E>(g + int64_t(r) * it.ld, o + int64_t(r) * it.out_ld, it.n, s, lane);
+}
+
+// out = g factor, an item a wave. In place with a factor of one there is
+// nothing to do.
+__global__ __launch_bounds__(kThreads) void clip_scale_kernel(Args A) {
+  const int i = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
+  if (i >= A.n_items) return;
+  const Item it = A.items[i];
+  const float s = A.res->scale;
+  if (it.g == it.o && s == 1.f) return;
+  const int lane = threadIdx.x & 63;
+  if (it.dtype == MUON_F32) scale_item<F32>(it, s, lane);
+  else scale_item<Bf16>(it, s, lane);
+}
+
+// ------------------------------------------------------------------ host
+
+struct Interval {
+  uintptr_t lo, hi;
+  bool write;
+};
+
+struct Host {
+  std::vector<Item> items;
+  std::vector<Range> ranges;
+  bool all_out = true;  // every non-empty tensor has an out
+};
+
+int64_t size_of(int32_t dtype) { return dtype == MUON_F32 ? 4 : 2; }
+
+muon_status build(const muon_clip_tensor* ts, int32_t n, Host* H) {
+  if (n < 0 || n > MUON_CLIP_MAX_TENSORS) return MUON_E_SHAPE;
+  if (n > 0 && ts == nullptr) return MUON_E_INVALID;
+  std::vector<Interval> iv;
+  double total = 0.0;  // bytes
+  int64_t elems = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const muon_clip_tensor& T = ts[i];
+    if (T.dtype != MUON_F32 && T.dtype != MUON_BF16) return MUON_E_DTYPE;
+    if (T.reserved != 0) return MUON_E_INVALID;
+    if (T.rows < 0 || T.cols < 0 || T.rows > MUON_CLIP_MAX_NUMEL || T.cols > MUON_CLIP_MAX_NUMEL) return MUON_E_SHAPE;
+    if (T.rows == 0 || T.cols == 0) continue;
+    if (T.rows > MUON_CLIP_MAX_NUMEL / T.cols) return MUON_E_SHAPE;
+    if (T.ld < T.cols || T.ld > MUON_CLIP_MAX_NUMEL || T.rows - 1 > MUON_CLIP_MAX_NUMEL / T.ld) return MUON_E_SHAPE;
+    if (T.grad == nullptr) return MUON_E_INVALID;
+    const uintptr_t es = static_cast<uintptr_t>(size_of(T.dtype));
+    const uintptr_t g = reinterpret_cast<uintptr_t>(T.grad), o = reinterpret_cast<uintptr_t>(T.out);
+    if (g % es != 0 || o % es != 0) return MUON_E_ALIGN;
+    const uintptr_t span = static_cast<uintptr_t>((T.rows - 1) * T.ld + T.cols) * es;
+    if (g > UINTPTR_MAX - span) return MUON_E_SHAPE;
+    if (o != 0) {
+      if (T.out_ld < T.cols || T.out_ld > MUON_CLIP_MAX_NUMEL || T.rows - 1 > MUON_CLIP_MAX_NUMEL / T.out_ld)
+        return MUON_E_SHAPE;
+      const uintptr_t ospan = static_cast<uintptr_t>((T.rows - 1) * T.out_ld + T.cols) * es;
+      if (o > UINTPTR_MAX - ospan) return MUON_E_SHAPE;
+      if (g == o && T.rows > 1 && T.ld != T.out_ld) return MUON_E_INVALID;
+      iv.push_back({o, o + ospan, true});
+    } else {
+      H->all_out = false;
+    }
+    if (g != o) iv.push_back({g, g + span, false});
+    total += double(T.rows) * double(T.cols) * double(es);
+    elems += T.rows * T.cols;
+    if (elems > MUON_CLIP_MAX_NUMEL) return MUON_E_SHAPE;
+  }
+  std::sort(iv.begin(), iv.end(), [](const Interval& x, const Interval& y) { return x.lo < y.lo; });
+  uintptr_t max_hi_any = 0, max_hi_w = 0;
+  for (const Interval& x : iv) {
+    if (x.lo < max_hi_w || (x.write && x.lo < max_hi_any)) return MUON_E_INVALID;
+    max_hi_any = std::max(max_hi_any, x.hi);
+    if (x.write) max_hi_w = std::max(max_hi_w, x.hi);
+  }
+
+  // Items of about equal bytes: at most twice kTargetItems of them (twice
+  // 2^42 / kMaxBytes for the longest list) and one more per tensor.
+  const double want = std::ceil(total / double(kTargetItems) / double(kMinBytes)) * double(kMinBytes);
+  const int64_t bytes = static_cast<int64_t>(std::min(double(kMaxBytes), std::max(double(kMinBytes), want)));
+  H->ranges.resize(static_cast<size_t>(n));
+  for (int32_t i = 0; i < n; ++i) {
+    const muon_clip_tensor& T = ts[i];
+    Range& R = H->ranges[i];
+    R.beg = static_cast<int32_t>(H->items.size());
+    const int64_t es = size_of(T.dtype), chunk = bytes / es;
+    int64_t rows = T.rows, cols = T.cols;
+    if (rows > 0 && cols > 0) {
+      const char* g = static_cast<const char*>(T.grad);
+      char* o = static_cast<char*>(T.out);
+      const bool flat = rows == 1 || (T.ld == cols && (o == nullptr || T.out_ld == cols));
+      if (flat) {
+        cols *= rows;
+        rows = 1;
+      }
+      if (cols >= chunk) {  // pieces of rows
+        for (int64_t r = 0; r < rows; ++r)
+          for (int64_t c = 0; c < cols; c += chunk)
+            H->items.push_back({g + (r * T.ld + c) * es, o ? o + (r * T.out_ld + c) * es : nullptr, 0, 0,
+                                static_cast<int32_t>(std::min(chunk, cols - c)), 1, T.dtype, 0});
+      } else {              // whole rows, at most about one item's bytes
+        const int64_t each = std::max<int64_t>(1, chunk / cols);
+        for (int64_t r = 0; r < rows; r += each)
+          H->items.push_back({g + r * T.ld * es, o ? o + r * T.out_ld * es : nullptr, T.ld, T.out_ld,
+                              static_cast<int32_t>(cols), static_cast<int32_t>(std::min(each, rows - r)), T.dtype, 0});
+      }
+    }
+    R.end = static_cast<int32_t>(H->items.size());
+  }
+  return MUON_OK;
+}
+
+int32_t blocks_of(size_t items) { return static_cast<int32_t>((items + kWaves - 1) / kWaves); }
+
+// Workspace: item sums, block sums, reduced sums (float64 each).
+size_t workspace_of(size_t items) { return 8 * (items + size_t(blocks_of(items)) + kReduced); }
+
+}  // namespace muon_clip
+
+struct muon_clip_plan_s {
+  int device = -1;
+  void* dmem = nullptr;
+  const muon_clip::Item* d_items = nullptr;
+  const muon_clip::Range* d_ranges = nullptr;
+  int32_t n_items = 0, n_tensors = 0;
+  bool all_out = true;
+  size_t ws_bytes = 0;
+};
+
+namespace {
+
+muon_status enqueue(muon_clip_plan* plan, const muon_clip_config* cfg, muon_clip_result* result, float* norms,
+                    void* ws, size_t ws_bytes, void* stream, bool scale) {
+  using namespace muon_clip;
+  if (plan == nullptr || cfg == nullptr || result == nullptr) return MUON_E_INVALID;
+  if (!(cfg->max_norm >= 0.f) || !std::isfinite(cfg->eps) || cfg->eps < 0.f || !std::isfinite(cfg->grad_mul) ||
+      !(cfg->grad_mul > 0.f))
+    return MUON_E_INVALID;
+  if (scale && !plan->all_out) return MUON_E_INVALID;
+  if (reinterpret_cast<uintptr_t>(result) % 4 != 0 || reinterpret_cast<uintptr_t>(norms) % 4 != 0) return MUON_E_ALIGN;
+  if (ws == nullptr || ws_bytes < plan->ws_bytes || reinterpret_cast<uintptr_t>(ws) % 256 != 0)
+    return MUON_E_WORKSPACE;
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess || dev != plan->device) return MUON_E_DEVICE;
+  const int32_t blocks = blocks_of(static_cast<size_t>(plan->n_items));
+  Args a{};
+  a.items = plan->d_items;
+  a.n_items = plan->n_items;
+  a.isum = norms ? static_cast<double*>(ws) : nullptr;
+  a.part = static_cast<double*>(ws) + plan->n_items;
+  a.n_part = blocks;
+  a.ranges = plan->d_ranges;
+  a.n_tensors = plan->n_tensors;
+  a.norms = norms;
+  a.res = result;
+  a.max_norm = cfg->max_norm;
+  a.eps = cfg->eps;
+  a.mul = cfg->grad_mul;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const dim3 block(kThreads);
+  if (blocks > 0) {
+    hipLaunchKernelGGL(clip_norm_kernel, dim3(unsigned(blocks)), block, 0, s, a);
+    if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
+  }
+  if (blocks > 4 * kReduced) {
+    const int32_t each = (blocks + kReduced - 1) / kReduced;
+    hipLaunchKernelGGL(clip_reduce_kernel, dim3(kReduced), block, 0, s, a.part, a.part + blocks, blocks, each);
+    if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
+    a.part += blocks;
+    a.n_part = kReduced;
+  }
+  const unsigned fin = 1u + (norms ? unsigned((plan->n_tensors + kWaves - 1) / kWaves) : 0u);
+  hipLaunchKernelGGL(clip_finish_kernel, dim3(fin), block, 0, s, a);
+  if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
+  if (scale && blocks > 0) {
+    hipLaunchKernelGGL(clip_scale_kernel, dim3(unsigned(blocks)), block, 0, s, a);
+    if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
+  }
+  return MUON_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_clip_workspace_bytes(const muon_clip_tensor* ts, int32_t n, size_t* bytes) {
+  if (bytes == nullptr) return MUON_E_INVALID;
+  try {
+    muon_clip::Host H;
+    const muon_status st = muon_clip::build(ts, n, &H);
+    if (st == MUON_OK) *bytes = muon_clip::workspace_of(H.items.size());
+    return st;
+  } catch (...) {
+    return MUON_E_ALLOC;
+  }
+}
+
+muon_status muon_clip_plan_create(const muon_clip_tensor* ts, int32_t n, muon_clip_plan** plan) {
+  if (plan == nullptr) return MUON_E_INVALID;
+  *plan = nullptr;
+  try {
+    muon_clip::Host H;
+    const muon_status st = muon_clip::build(ts, n, &H);
+    if (st != MUON_OK) return st;
+    int dev = 0;
+    hipDeviceProp_t prop;
+    if (hipGetDevice(&dev) != hipSuccess || hipGetDeviceProperties(&prop, dev) != hipSuccess ||
+        std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
+      return MUON_E_DEVICE;
+    const size_t ib = (sizeof(muon_clip::Item) * H.items.size() + 255) / 256 * 256;
+    std::vector<char> h(std::max<size_t>(256, ib + sizeof(muon_clip::Range) * H.ranges.size()), 0);
+    if (!H.items.empty()) std::memcpy(h.data(), H.items.data(), sizeof(muon_clip::Item) * H.items.size());
+    if (!H.ranges.empty()) std::memcpy(h.data() + ib, H.ranges.data(), sizeof(muon_clip::Range) * H.ranges.size());
+    muon_clip_plan_s* p = new (std::nothrow) muon_clip_plan_s();
+    if (!p) return MUON_E_ALLOC;
+    p->device = dev;
+    p->n_items = static_cast<int32_t>(H.items.size());
+    p->n_tensors = n;
+    p->all_out = H.all_out;
+    p->ws_bytes = muon_clip::workspace_of(H.items.size());
+    if (hipMalloc(&p->dmem, h.size()) != hipSuccess) {
+      (void)hipGetLastError();
+      delete p;
+      return MUON_E_ALLOC;
+    }
+    if (hipMemcpy(p->dmem, h.data(), h.size(), hipMemcpyHostToDevice) != hipSuccess) {
+      (void)hipGetLastError();
+      (void)hipFree(p->dmem);
+      delete p;
+      return MUON_E_DEVICE;
+    }
+    p->d_items = static_cast<const muon_clip::Item*>(p->dmem);
+    p->d_ranges = reinterpret_cast<const muon_clip::Range*>(static_cast<char*>(p->dmem) + ib);
+    *plan = p;
+    return MUON_OK;
+  } catch (...) {
+    return MUON_E_ALLOC;
+  }
+}
+
+muon_status muon_clip_plan_norm(muon_clip_plan* plan, const muon_clip_config* cfg, muon_clip_result* result,
+                                float* norms, void* workspace, size_t workspace_bytes, void* stream) {
+  return enqueue(plan, cfg, result, norms, workspace, workspace_bytes, stream, false);
+}
+
+muon_status muon_clip_plan_step(muon_clip_plan* plan, const muon_clip_config* cfg, muon_clip_result* result,
+                                float* norms, void* workspace, size_t workspace_bytes, void* stream) {
+  return enqueue(plan, cfg, result, norms, workspace, workspace_bytes, stream, true);
+}
+
+void muon_clip_plan_destroy(muon_clip_plan* plan) {
+  if (!plan) return;
+  (void)hipDeviceSynchronize();
+  if (plan->dmem) (void)hipFree(plan->dmem);
+  delete plan;
+}
+
+}  // extern "C"

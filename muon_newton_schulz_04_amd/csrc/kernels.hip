@@ -255,6 +255,10 @@ __device__ __forceinline__ float form_u(float g, float nb, const StepArgs& A) {
   return A.nesterov ? __fmaf_rn(A.mu, nb, g) : nb;
 }
 
+// The plan's gradient factor: every kernel that reads the gradients takes
+// G * factor (one float32 product, exact for a factor of one) for G.
+__device__ __forceinline__ float grad_scale(const StepArgs& A) { return A.gscale ? *A.gscale : 1.f; }
+
 // --------------------------------------------------------- momentum kernel
 
 template <typename T>
@@ -266,6 +270,7 @@ __global__ __launch_bounds__(256) void momentum_kernel(StepArgs A) {
   ScaledSsq acc;
   const T* g = static_cast<const T*>(M.grad);
   T* mb = static_cast<T*>(M.mom);
+  const float gs = grad_scale(A);
   constexpr int V = 16 / sizeof(T);  // elements per 16-byte vector
   if (M.vec_ok) {
     const int32_t vpr = M.cols / V;
@@ -282,7 +287,7 @@ __global__ __launch_bounds__(256) void momentum_kernel(StepArgs A) {
         T* oe = reinterpret_cast<T*>(&ov);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float gf = Elem<T>::load(ge, e);
+          const float gf = Elem<T>::load(ge, e) * gs;
           const float nb = momentum_new<T>(A.mu, Elem<T>::load(be, e), gf);
           Elem<T>::store(oe, e, nb);
           acc.add(form_u(gf, nb, A));
@@ -290,14 +295,14 @@ __global__ __launch_bounds__(256) void momentum_kernel(StepArgs A) {
         *reinterpret_cast<uint4*>(mb + off) = ov;
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc.add(Elem<T>::load(ge, e));
+        for (int e = 0; e < V; ++e) acc.add(Elem<T>::load(ge, e) * gs);
       }
     }
   } else {
     const int32_t ne = nr * M.cols;
     for (int32_t e = threadIdx.x; e < ne; e += 256) {
       const int64_t off = int64_t(r0 + e / M.cols) * M.ld + (e % M.cols);
-      const float gf = Elem<T>::load(g, off);
+      const float gf = Elem<T>::load(g, off) * gs;
       float u = gf;
       if (A.use_mom) {
         const float nb = momentum_new<T>(A.mu, Elem<T>::load(mb, off), gf);
@@ -370,6 +375,7 @@ __global__ __launch_bounds__(256) void normalize_kernel(StepArgs A) {
   const int32_t cr0 = M.tall ? j0 : i0, cc0 = M.tall ? i0 : j0;
   const T* g = static_cast<const T*>(M.grad);
   const T* mb = static_cast<const T*>(M.mom);
+  const float gs = grad_scale(A);
   float u[2][8];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -384,7 +390,7 @@ __global__ __launch_bounds__(256) void normalize_kernel(StepArgs A) {
         if (A.use_mom) bw = *reinterpret_cast<const u32x4_t*>(mb + off);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          gv[e] = bf2f(static_cast<uint16_t>(gw[e >> 1] >> (16 * (e & 1))));
+          gv[e] = bf2f(static_cast<uint16_t>(gw[e >> 1] >> (16 * (e & 1)))) * gs;
           bv[e] = bf2f(static_cast<uint16_t>(bw[e >> 1] >> (16 * (e & 1))));
         }
       } else {
@@ -395,7 +401,7 @@ __global__ __launch_bounds__(256) void normalize_kernel(StepArgs A) {
           if (A.use_mom) bw = *reinterpret_cast<const f32x4_t*>(mb + off + 4 * q);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            gv[4 * q + e] = gw[e];
+            gv[4 * q + e] = gw[e] * gs;
             bv[4 * q + e] = bw[e];
           }
         }
@@ -407,7 +413,7 @@ __global__ __launch_bounds__(256) void normalize_kernel(StepArgs A) {
       for (int e = 0; e < 8; ++e) {
         float x = 0.f;
         if (cr < M.rows && cc + e < M.cols) {
-          const float gf = Elem<T>::load(g, off + e);
+          const float gf = Elem<T>::load(g, off + e) * gs;
           const float nb = A.use_mom ? Elem<T>::load(mb, off + e) : 0.f;
           x = form_u(gf, nb, A) * scale;
         }
@@ -553,6 +559,7 @@ __device__ __forceinline__ void tile_u_bf16(const StepArgs& A, const MatInfo& M,
                                             float (&u)[2][8]) {
   const uint16_t* g = static_cast<const uint16_t*>(M.grad);
   uint16_t* mb = static_cast<uint16_t*>(M.mom);
+  const float gs = grad_scale(A);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int v = threadIdx.x + 256 * h;
@@ -565,7 +572,7 @@ __device__ __forceinline__ void tile_u_bf16(const StepArgs& A, const MatInfo& M,
       u32x4_t nw = {0u, 0u, 0u, 0u};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float gf = bf2f(static_cast<uint16_t>(gw[e >> 1] >> (16 * (e & 1))));
+        const float gf = bf2f(static_cast<uint16_t>(gw[e >> 1] >> (16 * (e & 1)))) * gs;
         float nb = bf2f(static_cast<uint16_t>(bw[e >> 1] >> (16 * (e & 1))));
         if (STEP && A.use_mom) {
           nb = momentum_new<uint16_t>(A.mu, nb, gf);
@@ -579,7 +586,7 @@ __device__ __forceinline__ void tile_u_bf16(const StepArgs& A, const MatInfo& M,
       for (int e = 0; e < 8; ++e) {
         float x = 0.f;
         if (cr < M.rows && cc + e < M.cols) {
-          const float gf = bf2f(g[off + e]);
+          const float gf = bf2f(g[off + e]) * gs;
           float nb = A.use_mom ? bf2f(mb[off + e]) : 0.f;
           if (STEP && A.use_mom) {
             nb = momentum_new<uint16_t>(A.mu, nb, gf);

@@ -35,6 +35,7 @@ struct StepArgs {
   // chained schedule: workspace offset of its counters (the scale pass
   // clears them), -1 without one
   int64_t chain_off;
+  const float* gscale;  // gradients are multiplied by *gscale (nullptr: by one)
 };
 
 // The chained launch (plan.hpp): the lists, their bounds per XCD, the

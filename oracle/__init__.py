@@ -17,5 +17,8 @@ from .muon_oracle import (  # noqa: F401
     muon_update,
     apply_weight,
     adam_update,
+    gradient_norms,
+    clip_scale,
+    clip_gradient,
     falg_flops,
 )

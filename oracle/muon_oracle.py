@@ -269,6 +269,29 @@ def adam_update(p, g, m, v, *, lr: float, beta1: float, beta2: float, eps: float
     return p_new, m_new, v_new
 
 
+def gradient_norms(grads, mul: float = 1.0):
+    """(N, [N_i]): the L2 norm of all gradients together and of each, times
+    ``mul``. Squares of bf16 and float32 values are exact in float64."""
+    sums = [float(np.sum(np.square(np.asarray(g, dtype=np.float64)))) for g in grads]
+    return mul * float(np.sqrt(np.sum(sums))), [mul * float(np.sqrt(s)) for s in sums]
+
+
+def clip_scale(norm: float, *, max_norm: float, eps: float, mul: float = 1.0) -> float:
+    """The factor that clips gradients of global norm ``norm`` (``mul``
+    included in both): mul where norm + eps is within max_norm, else
+    mul * max_norm / (norm + eps). A NaN norm gives NaN."""
+    if norm + eps <= max_norm:
+        return float(mul)
+    return float(mul) * (float(max_norm) / (float(norm) + float(eps)))
+
+
+def clip_gradient(g, scale: float, dtype: str = "bf16") -> np.ndarray:
+    """g * scale, a float32 product (both factors float32 values), stored at
+    the gradient's dtype (round to nearest even)."""
+    x = fp32_round(np.asarray(g, dtype=np.float64) * float(scale))
+    return bf16_round(x) if dtype == "bf16" else x
+
+
 def falg_flops(rows: int, cols: int, steps: int) -> int:
     """Algorithmic flops of k steps on one matrix (m = min, n = max side):
     m(m+1)n for the symmetric Gram, m^2(m+1) for the symmetric A^2 and

@@ -1,0 +1,551 @@
+"""Global gradient norm, clipping, and the optimizer steps on clipped
+gradients (include/muon_clip.h, muon_plan_set_grad_scale,
+muon_adam_plan_set_grad_scale) through the C ABI.
+
+Tolerances. Sums of squares are float64 sums of at most 2^32 non-negative
+terms with exact squares: their relative error is below 2^32 2^-53 = 2^-21 in
+the worst order and, summed in trees and runs of under 2^15 terms each as
+here, below 2^-37; the square root, the division and the product add a few
+2^-53. The norm and the scale are then rounded once to float32, half a step:
+2^-24. So both are held to RTOL = 2^-24 + 2^-36 relative (for normal float32
+values). Clipped gradients are g * scale with the stored scale, a float32
+product rounded to the dtype: held bitwise. The optimizer steps on clipped
+gradients are held bitwise to the same step on gradients already multiplied
+(where the product is a value of the gradient's type), and to the oracle on
+the float32 products otherwise.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from workloads import CONFIGS, make_adam_state, make_gradients, to_f64
+
+pytestmark = pytest.mark.gpu
+
+mu = pytest.importorskip("muon_newton_schulz_04_amd")
+DEV = "cuda"
+TDT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+NAME = {v: k for k, v in TDT.items()}
+RTOL = 2.0 ** -24 + 2.0 ** -36
+QUINTIC = CONFIGS["gpt2_small_block"].coeffs
+
+
+def f32(x):
+    return float(np.float32(x))
+
+
+def say(msg):
+    print(msg, flush=True)
+
+
+def close(got, want, rtol=RTOL):
+    return got == want or abs(got - want) <= rtol * abs(want)
+
+
+def view_of(shape, dtype, offset, pad, gen, scale):
+    """A tensor `offset` elements into its storage, `pad` elements behind each row."""
+    rows = math.prod(shape[:-1]) if shape else 1
+    cols = shape[-1] if shape else 1
+    buf = torch.full((offset + rows * (cols + pad) + 3,), 77.0, dtype=TDT[dtype])
+    v = buf[offset:offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    v.copy_((scale * torch.randn(rows, cols, generator=gen)).to(TDT[dtype]))
+    buf = buf.to(DEV)
+    v = buf[offset:offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    return buf, (v if pad else v.reshape(shape))
+
+
+def make_list(shapes, dtypes, offsets, pads, seed, scale=0.1):
+    gen = torch.Generator().manual_seed(seed)
+    made = [view_of(s, d, o, p, gen, scale) for s, d, o, p in zip(shapes, dtypes, offsets, pads)]
+    return [b for b, _ in made], [v for _, v in made]
+
+
+def check_result(plan, res, norms, grads, max_norm, eps, mul):
+    r = res.cpu().double().tolist()
+    n, each = oracle.gradient_norms([to_f64(g) for g in grads], f32(mul))
+    want = oracle.clip_scale(n, max_norm=f32(max_norm), eps=f32(eps), mul=f32(mul))
+    assert close(r[0], n), (r[0], n)
+    assert close(r[1], want), (r[1], want)
+    if norms is not None:
+        for a, b in zip(norms.cpu().double().tolist(), each):
+            assert close(a, b), (a, b)
+    return r[1]
+
+
+def check_outs(before, outs, scale):
+    for g, o in zip(before, outs):
+        if o is not None and g.numel():
+            want = oracle.clip_gradient(to_f64(g), scale, NAME[o.dtype])
+            assert np.array_equal(to_f64(o), want.reshape(to_f64(o).shape))
+
+
+SHAPES = [(1,), (7,), (768,), (0,), (3, 5), (16389,), (765, 129), (2, 0, 4), (1000, 3), (64, 2048), (100003,), (333, 520)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32", "mixed"])
+@pytest.mark.parametrize("offset", [0, 1, 4, 5])
+@pytest.mark.parametrize("pad", [0, 1, 24])
+def test_norm_and_clip_match_oracle(dtype, offset, pad):
+    """Odd sizes, offsets into storage, strided rows, empty tensors; out of place and in place."""
+    dts = [("bf16", "fp32")[i % 2] if dtype == "mixed" else dtype for i in range(len(SHAPES))]
+    pads = [pad if len(s) == 2 else 0 for s in SHAPES]
+    offs = [offset] * len(SHAPES)
+    say(f"clip parity {dtype} offset {offset} pad {pad}")
+    bufs, grads = make_list(SHAPES, dts, offs, pads, seed=offset + 10 * pad)
+    obufs, outs = make_list(SHAPES, dts, [(o + 3 * i) % 7 for i, o in enumerate(offs)], pads, seed=99)
+    keep = [b.clone() for b in bufs]
+    plan = mu.ClipPlan(grads, outs)
+    norms = torch.full((len(grads),), -1.0, device=DEV)
+    for max_norm, eps, mul in [(1.0, 1e-6, 1.0), (1e6, 0.0, 1.0), (2.5, 1e-3, 1.0 / 3)]:
+        s = check_result(plan, plan.step(max_norm, eps, mul, norms=norms), norms, grads, max_norm, eps, mul)
+        check_outs(grads, outs, s)
+        assert all(torch.equal(a, b) for a, b in zip(bufs, keep))          # gradients are only read
+    for b, o in zip(obufs, outs):                                          # nothing beside the outs is written
+        o.fill_(77.0)
+        assert bool((b == 77.0).all())
+    plan.destroy()
+    # in place
+    before = [g.clone() for g in grads]
+    plan = mu.ClipPlan(grads)
+    s = check_result(plan, plan.norm(0.5), None, grads, 0.5, 1e-6, 1.0)
+    assert all(torch.equal(a, b) for a, b in zip(bufs, keep))
+    plan.step(0.5)
+    check_outs(before, grads, s)
+    for b, g in zip(bufs, grads):
+        g.fill_(77.0)
+        assert bool((b == 77.0).all())
+    plan.destroy()
+
+
+def test_dense_to_strided_permuted_and_partial_outs():
+    """A dense gradient into strided rows and the reverse, permuted dense tensors, entries that only count."""
+    gen = torch.Generator().manual_seed(5)
+    r = lambda *s: (0.1 * torch.randn(*s, generator=gen)).to(DEV)  # noqa: E731
+    grads = [r(40, 50), r(40, 64)[:, :50], r(6, 7, 8).permute(2, 0, 1), r(90), r(30, 70)[:, 5:40].t()]
+    outs = [torch.zeros(40, 64, device=DEV)[:, 3:53], torch.zeros(40, 50, device=DEV),
+            torch.zeros(6, 7, 8, device=DEV).permute(2, 0, 1), None, torch.zeros(30, 35, device=DEV).t()]
+    plan = mu.ClipPlan(grads, outs)
+    say("clip: dense to strided, permuted")
+    with pytest.raises(mu.MuonError) as e:                                  # one gradient has no out
+        plan.step(1.0)
+    assert e.value.code == 1
+    n = check_result(plan, plan.norm(1.0), None, grads, 1.0, 1e-6, 1.0)
+    plan.destroy()
+    grads, outs = [grads[i] for i in (0, 1, 2, 4)], [outs[i] for i in (0, 1, 2, 4)]
+    plan = mu.ClipPlan(grads, outs)
+    s = check_result(plan, plan.step(1.0), None, grads, 1.0, 1e-6, 1.0)
+    assert s != n
+    check_outs(grads, outs, s)
+    plan.destroy()
+
+
+def test_empty_lists():
+    norms = torch.full((2,), -1.0, device=DEV)
+    e = [torch.empty(0, device=DEV), torch.empty(3, 0, dtype=torch.bfloat16, device=DEV)]
+    for grads, nm in (([], None), (e, norms)):
+        plan = mu.ClipPlan(grads)
+        say(f"clip: {len(grads)} empty tensors")
+        for call in (plan.norm, plan.step):
+            assert call(1.0, norms=nm).cpu().tolist() == [0.0, 1.0]
+            assert call(0.0, eps=0.0, grad_mul=0.5, norms=nm).cpu().tolist() == [0.0, 0.5]
+            assert call(0.25, eps=1.0, norms=nm).cpu().tolist() == [0.0, 0.25]
+        plan.destroy()
+    assert norms.cpu().tolist() == [0.0, 0.0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("value", [2.0 ** 100, 2.0 ** -100, 2.0 ** 127, 2.0 ** -126, 2.0 ** -133])
+def test_extreme_magnitudes(dtype, value):
+    """Squares far outside float32's range, up to the largest and down to subnormal gradients."""
+    g = [torch.full((5000,), value, dtype=TDT[dtype], device=DEV), torch.full((33, 9), -value, dtype=TDT[dtype], device=DEV)]
+    n, each = oracle.gradient_norms([to_f64(x) for x in g])
+    norms = torch.zeros(2, device=DEV)
+    out = [torch.zeros_like(x) for x in g]
+    plan = mu.ClipPlan(g, out)
+    limit = 2.0 ** 120 if value > 1 else 2.0 ** -126      # keeps the scale a normal float32
+    say(f"clip: values {value}")
+    r = plan.step(limit, eps=0.0, norms=norms).cpu().double().tolist()
+    want = oracle.clip_scale(n, max_norm=limit, eps=0.0)
+    big = float(np.finfo(np.float32).max)
+    assert close(r[0], n) if 2.0 ** -126 <= n <= big else (r[0] == math.inf if n > big else abs(r[0] - n) <= 2.0 ** -150)
+    assert close(r[1], want)
+    check_outs(g, out, r[1])
+    for a, b in zip(norms.cpu().double().tolist(), each):
+        assert close(a, b) or (b > big and a == math.inf) or abs(a - b) <= 2.0 ** -150
+    plan.destroy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("place", [0, 4099, 9999])
+def test_nan_and_infinity_propagate(dtype, place):
+    g = torch.ones(10000, dtype=TDT[dtype], device=DEV)
+    other = torch.ones(10, dtype=torch.float32, device=DEV)
+    out, oout = torch.zeros_like(g), torch.zeros_like(other)
+    plan = mu.ClipPlan([g, other], [out, oout])
+    norms = torch.zeros(2, device=DEV)
+    say(f"clip: non-finite at {place}")
+    g[place] = -math.inf
+    assert plan.step(1.0, norms=norms).cpu().tolist() == [math.inf, 0.0]
+    assert norms[0].item() == math.inf and close(norms[1].item(), math.sqrt(10.0))
+    assert torch.isnan(out).nonzero().flatten().tolist() == [place]
+    assert int((out != 0).sum()) == 1 and not oout.any()
+    assert plan.norm(math.inf).cpu().tolist() == [math.inf, 1.0]
+    g[7] = math.nan
+    r = plan.step(1.0, norms=norms).cpu()
+    assert torch.isnan(r).all() and torch.isnan(norms[0]) and not torch.isnan(norms[1])
+    assert torch.isnan(out).all() and torch.isnan(oout).all()
+    assert torch.isnan(plan.norm(math.inf)).all()
+    plan.destroy()
+
+
+def test_long_list_of_tiny_tensors():
+    """Far more tensors than work items by size: one sum each, added up in two levels."""
+    n = 40000
+    flat = torch.randn(n * 3, generator=torch.Generator().manual_seed(3)).to(DEV)
+    grads = [t[: 1 + i % 3] for i, t in enumerate(flat.view(n, 3).unbind())]
+    norms = torch.zeros(n, device=DEV)
+    plan = mu.ClipPlan(grads)
+    say("clip: 40000 tensors")
+    host, lens = flat.view(n, 3).cpu().double().numpy(), 1 + np.arange(n) % 3
+    live = np.arange(3)[None, :] < lens[:, None]
+    each = np.sqrt(np.sum(np.where(live, host, 0.0) ** 2, axis=1))
+    r = plan.step(1.0, norms=norms).cpu().double().tolist()
+    total = math.sqrt(np.sum(each ** 2))
+    assert close(r[0], total) and close(r[1], 1.0 / (total + f32(1e-6)))
+    assert np.all(np.abs(norms.cpu().double().numpy() - each) <= RTOL * each)
+    got = flat.view(n, 3).cpu().double().numpy()
+    assert np.array_equal(got, np.where(live, oracle.clip_gradient(host, r[1], "fp32"), host))
+    plan.destroy()
+
+
+def test_offsets_beyond_32_bits():
+    """One bf16 tensor of 2^31 + 5 elements, and one of rows whose last starts beyond 2^32 bytes."""
+    n = (1 << 31) + 5
+    g = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    for at, v in ((0, 3.0), (1 << 30, 4.0), (n - 1, 12.0)):
+        g[at] = v
+    wide = torch.zeros(3, 1 << 30, dtype=torch.float32, device=DEV)[:, :1000]
+    wide[2, 999] = 84.0
+    plan = mu.ClipPlan([g, wide])
+    norms = torch.zeros(2, device=DEV)
+    say("clip: 2^31 + 5 elements")
+    r = plan.step(42.5, eps=0.0, norms=norms).cpu().tolist()
+    assert r == [85.0, 0.5] and norms.cpu().tolist() == [13.0, 84.0]
+    assert [g[i].item() for i in (0, 1, 1 << 30, n - 1)] == [1.5, 0.0, 2.0, 6.0]
+    assert wide[2, 999].item() == 42.0 and int(torch.count_nonzero(g)) == 3
+    plan.destroy()
+
+
+def test_deterministic_and_workspace_contents_do_not_matter():
+    _, grads = make_list([(3000, 1001), (777,), (512, 512)], ["bf16", "fp32", "bf16"], [1, 0, 2], [7, 0, 0], 8)
+    plan = mu.ClipPlan(grads, [None] * 3)
+    say("clip: determinism")
+    first = None
+    for fill in (0, 255, 90):
+        ws = torch.full((plan.workspace_bytes,), fill, dtype=torch.uint8, device=DEV)
+        norms = torch.full((3,), float(fill), device=DEV)
+        r = [plan.norm(1.0, norms=norms, workspace=ws).clone(), norms]
+        first = r if first is None else first
+        assert all(torch.equal(a, b) for a, b in zip(first, r))
+    plan.destroy()
+
+
+def test_two_graphs_of_one_plan_on_two_streams():
+    """Each captured graph has its workspace and result; replayed at once and
+    several times on new gradients, each is the eager result."""
+    _, grads = make_list([(2000, 700), (513,), (64, 900)], ["bf16", "fp32", "fp32"], [0, 1, 0], [0, 0, 4], 11)
+    plan = mu.ClipPlan(grads, [None] * 3)
+    res = [torch.zeros(2, device=DEV) for _ in range(2)]
+    nms = [torch.zeros(3, device=DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    plan.norm(1.0)
+    torch.cuda.synchronize()
+    say("clip: two graphs of one plan")
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=streams[i]):
+            plan.norm(1.0 + i, norms=nms[i], result=res[i])
+        graphs.append(graph)
+    for k in range(4):
+        for g in grads:
+            g.mul_(0.5)
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            norms = torch.zeros(3, device=DEV)
+            want = plan.norm(1.0 + i, norms=norms)
+            assert torch.equal(want, res[i]) and torch.equal(norms, nms[i])
+            check_result(plan, res[i], nms[i], grads, 1.0 + i, 1e-6, 1.0)
+    plan.destroy()
+
+
+def test_call_on_another_stream_without_a_workspace():
+    """The workspace the binding allocates belongs to the stream of the call."""
+    _, grads = make_list([(4000, 512)], ["fp32"], [0], [0], 12)
+    plan = mu.ClipPlan(grads, [None])
+    want = plan.norm(1.0).clone()
+    torch.cuda.synchronize()
+    say("clip: another stream")
+    for handle in (False, True):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        for _ in range(20):
+            plan.norm(1.0, stream=s.cuda_stream if handle else s)
+            torch.full((plan.workspace_bytes,), 255, dtype=torch.uint8, device=DEV)     # reuses what was dropped
+        s.synchronize()
+        assert torch.equal(plan.result, want)
+    plan.destroy()
+
+
+def test_refusals():
+    _, grads = make_list([(64, 64)], ["fp32"], [0], [0], 13)
+    before = grads[0].clone()
+    plan = mu.ClipPlan(grads)
+
+    def code(fn):
+        with pytest.raises(mu.MuonError) as e:
+            fn()
+        return e.value.code
+
+    say("clip: refusals")
+    for bad in (math.nan, -1.0, -math.inf):
+        assert code(lambda: plan.step(bad)) == 1
+    for bad in (math.nan, -1e-6, math.inf):
+        assert code(lambda: plan.step(1.0, eps=bad)) == 1
+    for bad in (math.nan, 0.0, -1.0, math.inf):
+        assert code(lambda: plan.step(1.0, grad_mul=bad)) == 1
+    ws = torch.empty(plan.workspace_bytes + 256, dtype=torch.uint8, device=DEV)
+    assert code(lambda: plan.step(1.0, workspace=ws[:16])) == 5
+    assert code(lambda: plan.step(1.0, workspace=ws[1:])) == 5
+    for bad in (torch.zeros(3, device=DEV), torch.zeros(2), torch.zeros(2, dtype=torch.float64, device=DEV)):
+        with pytest.raises(ValueError):
+            plan.step(1.0, result=bad)
+    with pytest.raises(ValueError):
+        plan.step(1.0, norms=torch.zeros(2, device=DEV))
+    lib = mu.load_library()
+    cfg = mu.MuonClipConfig(1.0, 0.0, 1.0)
+    args = lambda r, n: (plan.handle, r, n, ws.data_ptr(), ws.numel(), None)  # noqa: E731
+    import ctypes
+    for r, n, want in ((None, None, 1), (ws.data_ptr() + 2, None, 4), (plan.result.data_ptr(), ws.data_ptr() + 1, 4)):
+        p, r, n, w, b, s = args(r, n)
+        assert lib.muon_clip_plan_step(p, ctypes.byref(cfg), r, n, w, b, s) == want
+        assert lib.muon_clip_plan_step(p, None, r, n, w, b, s) == 1
+    torch.cuda.synchronize()
+    assert torch.equal(grads[0], before)                    # nothing was enqueued
+    mplan = mu.MuonPlan(grads, [torch.zeros_like(before)], [torch.empty_like(before)])
+    for bad in (torch.zeros(2, device=DEV), torch.zeros(1), torch.zeros(1, dtype=torch.float64, device=DEV)):
+        with pytest.raises(ValueError):
+            mplan.set_grad_scale(bad)
+    assert lib.muon_plan_set_grad_scale(mplan.handle, ws.data_ptr() + 2) == 4
+    mplan.destroy()
+    plan.destroy()
+
+
+# ------------------------------------------------ optimizer steps on clipped gradients
+
+HP = dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, wd=0.1)
+
+
+def adam_run(shapes, dtype, scale=None, mul=None, seed=6):
+    params, grads, ms, vs = make_adam_state(shapes, TDT[dtype], seed, DEV)
+    if mul is not None:
+        for g in grads:
+            g.copy_((g.float() * mul).to(g.dtype))
+    plan = mu.AdamPlan(params, grads, ms, vs)
+    plan.set_grad_scale(scale)
+    for t in range(1, 4):
+        plan.step(step=t, **HP)
+    torch.cuda.synchronize()
+    plan.destroy()
+    return params + ms + vs
+
+
+@pytest.mark.parametrize("dtype,factor", [("fp32", 0.3), ("fp32", 1.0), ("bf16", 0.25), ("bf16", 1.0), ("bf16", 0.0)])
+def test_adam_scale_equals_scaled_gradients(dtype, factor):
+    """Where the product is a value of the gradient's type: bitwise the step on multiplied gradients."""
+    shapes = [(1,), (7,), (2304,), (16389,), (123, 456)]
+    s = torch.tensor([factor], device=DEV)
+    say(f"adam scale {dtype} {factor}")
+    got = adam_run(shapes, dtype, scale=s)
+    want = adam_run(shapes, dtype, mul=None if factor == 1.0 else s)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    if factor == 1.0:
+        return
+    plain = adam_run(shapes, dtype)
+    assert not torch.equal(plain[-1], got[-1])
+
+
+def test_adam_scale_against_oracle_bf16():
+    """A scale whose products are no bf16 values: nothing is rounded to bf16 between the two.
+    Moments: a few float32 roundings of each term, as for the step without a scale."""
+    params, grads, ms, vs = make_adam_state([(16389,), (64, 65)], torch.bfloat16, 7, DEV)
+    s = torch.tensor([0.3], device=DEV)
+    before = [[to_f64(t).ravel() for t in (p, m, v)] for p, m, v in zip(params, ms, vs)]
+    plan = mu.AdamPlan(params, grads, ms, vs)
+    plan.set_grad_scale(s)
+    say("adam scale vs oracle")
+    plan.step(step=2, **HP)
+    torch.cuda.synchronize()
+    b1, b2 = f32(HP["beta1"]), f32(HP["beta2"])
+    for g, p, m, v, (p0, m0, v0) in zip(grads, params, ms, vs, before):
+        gs = oracle.clip_gradient(to_f64(g).ravel(), f32(0.3), "fp32")
+        po, mo, vo = oracle.adam_update(p0, gs, m0, v0, step=2, dtype="bf16", **{k: f32(x) for k, x in HP.items()})
+        assert np.all(np.abs(to_f64(m).ravel() - mo) <= 2.0 ** -21 * (b1 * np.abs(m0) + (1 - b1) * np.abs(gs)))
+        assert np.all(np.abs(to_f64(v).ravel() - vo) <= 2.0 ** -21 * (b2 * v0 + (1 - b2) * gs * gs))
+        ulp = np.ldexp(1.0, (np.floor(np.log2(np.maximum(np.abs(po), 1e-38))) - 7).astype(int))
+        assert np.all(np.abs(to_f64(p).ravel() - po) <= ulp + 1e-5 * HP["lr"])
+    plan.set_grad_scale(None)                    # detached: the step without a scale
+    plan.destroy()
+
+
+MSHAPES = [(200, 333), (333, 200), (64, 64), (5, 1), (256, 512)]
+
+
+def muon_run(shapes, dtype, cfg, scale=None, mul=None, apply=False, entry="step", offset=0, steps=2):
+    gen = torch.Generator().manual_seed(31)
+    mk = lambda f: [view_of(s, dtype, offset, 0, gen, f)[1] for s in shapes]  # noqa: E731
+    grads, bufs, ws = mk(0.02), mk(0.01), mk(0.02)
+    if mul is not None:
+        for g in grads:
+            g.copy_((g.float() * mul).to(g.dtype))
+    outs = [torch.zeros_like(g) for g in grads]
+    plan = mu.MuonPlan(grads, bufs if cfg.momentum else None, outs)
+    plan.set_grad_scale(scale)
+    if apply:
+        plan.set_weights(ws)
+    for k in range(steps):
+        for g in grads:
+            if k:
+                g.mul_(64.0)                     # the guess of X0's power of two is wrong: the rewrite pass runs
+        if apply:
+            plan.step_apply(cfg, 0.02, 0.1)
+        elif entry == "noalloc":
+            plan.step_noalloc(cfg)
+        else:
+            plan.step(cfg)
+    torch.cuda.synchronize()
+    plan.destroy()
+    return outs + bufs + ws
+
+
+@pytest.mark.parametrize("offset", [0, 3])
+@pytest.mark.parametrize("dtype,factor", [("bf16", 0.25), ("bf16", 1.0), ("fp32", 0.25), ("fp32", 0.3), ("fp32", 1.0)])
+@pytest.mark.parametrize("steps,momentum,nesterov,how", [
+    (5, 0.95, True, "step"), (5, 0.95, False, "apply"), (0, 0.95, True, "step"), (5, 0.0, False, "noalloc")])
+def test_muon_scale_equals_scaled_gradients(offset, dtype, factor, steps, momentum, nesterov, how):
+    cfg = mu.make_config(*QUINTIC, steps, momentum, nesterov, 1e-7)
+    s = torch.tensor([factor], device=DEV)
+    say(f"muon scale {dtype} {factor} k={steps} mu={momentum} {how} offset {offset}")
+    kw = dict(apply=how == "apply", entry=how, offset=offset)
+    got = muon_run(MSHAPES, dtype, cfg, scale=s, **kw)
+    want = muon_run(MSHAPES, dtype, cfg, mul=None if factor == 1.0 else s, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_muon_scale_against_oracle_bf16():
+    """Scaled products that are no bf16 values: momentum buffers bitwise the oracle's on the float32
+    products (rounded once), updates within the set's bar."""
+    wl = CONFIGS["gpt2_small_block"]
+    shapes = [(192, 320), (320, 192), (256, 256)]
+    grads = [g.to(DEV) for g in make_gradients(wl, step=0, device="cpu", shapes=shapes)]
+    bufs = [(0.5 * g.float()).to(g.dtype) for g in grads]
+    b0, outs = [b.clone() for b in bufs], [torch.empty_like(g) for g in grads]
+    s = torch.tensor([0.3], device=DEV)
+    plan = mu.MuonPlan(grads, bufs, outs)
+    plan.set_grad_scale(s)
+    say("muon scale vs oracle")
+    plan.step(mu.make_config(*wl.coeffs, wl.steps, wl.momentum, wl.nesterov, wl.eps))
+    torch.cuda.synchronize()
+    a, b, c = (f32(x) for x in wl.coeffs)
+    for g, bf, b_old, o in zip(grads, bufs, b0, outs):
+        gs = oracle.clip_gradient(to_f64(g), f32(0.3), "fp32")
+        want, wbuf = oracle.muon_update(gs, to_f64(b_old), a=a, b=b, c=c, steps=wl.steps, mu=f32(wl.momentum),
+                                        nesterov=wl.nesterov, eps=f32(wl.eps), buf_dtype="bf16")
+        assert np.array_equal(to_f64(bf), wbuf)
+        assert np.linalg.norm(to_f64(o) - want) <= wl.tol * np.linalg.norm(want)
+    plan.destroy()
+
+
+def test_orthogonalize_and_cached_steps_have_no_scale():
+    g = [torch.randn(64, 96, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)]
+    cfg = mu.make_config(*QUINTIC, 0, 0.0, False, 1e-7)
+    o1, o2 = [torch.empty_like(g[0])], [torch.empty_like(g[0])]
+    mu.muon_orthogonalize(g, o1, cfg)
+    plan = mu.MuonPlan(g, None, o2)
+    plan.set_grad_scale(torch.tensor([math.nan], device=DEV))
+    plan.step(cfg)
+    torch.cuda.synchronize()
+    assert torch.isnan(o2[0].float()).all() and not torch.isnan(o1[0].float()).any()
+    plan.set_grad_scale(None)
+    plan.step(cfg)
+    torch.cuda.synchronize()
+    assert torch.equal(o1[0], o2[0])
+    plan.destroy()
+
+
+def test_whole_step_captured_and_replayed():
+    """One norm over hidden matrices and other parameters, Muon applied to the weights and Adam, captured
+    into one graph and replayed on new gradients with eager work between: bitwise the eager steps. The set
+    is deep enough for Muon's chained launch."""
+    mats = [(768, 768)] * 12 + [(768, 1024), (1024, 768)] * 2
+    vecs = [(1000, 768), (768,), (2304,), (765,)]
+    cfg = mu.make_config(*QUINTIC, 5, 0.95, True, 1e-7)
+
+    def build():
+        gen = torch.Generator().manual_seed(17)
+        r = lambda s, f, d=torch.bfloat16: (f * torch.randn(s, generator=gen)).to(d).to(DEV)  # noqa: E731
+        st = {"g": [r(s, 0.02) for s in mats], "b": [r(s, 0.01) for s in mats], "w": [r(s, 0.02) for s in mats]}
+        st["p"], st["q"], st["m"], st["v"] = make_adam_state(vecs, torch.float32, 18, DEV)
+        st["clip"] = mu.ClipPlan(st["g"] + st["q"])
+        st["muon"] = mu.MuonPlan(st["g"], st["b"], st["g"])
+        st["muon"].set_weights(st["w"])
+        st["adam"] = mu.AdamPlan(st["p"], st["q"], st["m"], st["v"])
+        for k in ("muon", "adam"):
+            st[k].set_grad_scale(st["clip"].scale)
+        st["ws"] = [torch.empty(st[k].workspace_bytes, dtype=torch.uint8, device=DEV) for k in ("clip", "muon")]
+        st["norms"] = torch.zeros(len(mats) + len(vecs), device=DEV)
+        return st
+
+    def step(st):
+        st["clip"].norm(1.0, norms=st["norms"], workspace=st["ws"][0])
+        st["muon"].step_apply(cfg, 0.02, 0.01, st["ws"][1])
+        st["adam"].step(step=7, **HP)
+
+    def state(st):
+        return [t.clone() for k in ("w", "b", "p", "m", "v") for t in st[k]] + [st["clip"].result.clone(), st["norms"].clone()]
+
+    def gradients(st, k):
+        for i, g in enumerate(st["g"] + st["q"]):
+            g.copy_(((0.01 + 0.5 * k) * torch.randn(g.shape, generator=torch.Generator().manual_seed(100 * k + i))).to(g.dtype))
+
+    eager, graph = build(), build()
+    say("whole step: eager")
+    want = []
+    for k in range(3):
+        gradients(eager, k)
+        step(eager)
+        torch.cuda.synchronize()
+        want.append(state(eager))
+        check_result(None, eager["clip"].result, eager["norms"], eager["g"] + eager["q"], 1.0, 1e-6, 1.0)
+    say("whole step: captured")
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        step(graph)
+    for k in range(3):
+        gradients(graph, k)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[k], state(graph)))
+    assert graph["muon"].chain_state() == (1, 0)
+    for st in (eager, graph):
+        for k in ("clip", "muon", "adam"):
+            st[k].destroy()
