@@ -30,6 +30,9 @@ constexpr int64_t kMinBytes = 4096;       // smallest work item
 constexpr int64_t kMaxBytes = 1 << 28;    // largest (its element count fits an int32)
 constexpr int64_t kTargetItems = 8192;    // 32 waves on each of the 256 CUs
 constexpr int kReduced = 1024;            // partials of a long list are first added up to this many
+constexpr int kWide = 512;                // tensors of more items get a block for their norm, others a wave
+constexpr int kSmall = 64;                // lists of at most this many items run in one block
+constexpr int kSmallWaves = 16;
 
 // One wave's work: `rows` rows of `n` consecutive elements.
 struct Item {
@@ -53,6 +56,8 @@ struct Args {
   double* isum;        // one sum per item (nullptr: not wanted)
   const Range* ranges; // items of each tensor
   int32_t n_tensors;
+  const int32_t* wide; // tensors of more than kWide items
+  int32_t n_wide;
   float* norms;        // nullptr: not wanted
   muon_clip_result* res;
   float max_norm, eps, mul;
@@ -168,21 +173,33 @@ __device__ __forceinline__ double wave_sum(double x) {
   return x;
 }
 
+template <int W = kWaves>
 __device__ __forceinline__ double block_sum(double x, double* red) {
   x = wave_sum(x);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
   __syncthreads();
   double s = 0.0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) s += red[w];
+  for (int w = 0; w < W; ++w) s += red[w];
+  return s;
+}
+
+// A thread's share (of T threads) of the sum of n partials, eight loads at once.
+template <int T>
+__device__ __forceinline__ double sum_share(const double* part, int n, int t) {
+  double s = 0.0;
+  for (int i = t; i < n; i += 8 * T) {
+    double x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = i + j * T < n ? part[i + j * T] : 0.0;
+    s += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+  }
   return s;
 }
 
 // Sum of n partials, the same for every thread of the block.
 __device__ __forceinline__ double sum_partials(const double* part, int n, double* red) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) s += part[i];
-  return block_sum(s, red);
+  return block_sum(sum_share<kThreads>(part, n, threadIdx.x), red);
 }
 
 __device__ __forceinline__ muon_clip_result result_of(double total, const Args& A) {
@@ -221,22 +238,38 @@ __global__ __launch_bounds__(kThreads) void clip_reduce_kernel(const double* par
   if (threadIdx.x == 0) out[blockIdx.x] = s;
 }
 
-// Block 0: the norm and the factor. The others: tensor norms, a wave each.
-__global__ __launch_bounds__(kThreads) void clip_finish_kernel(Args A) {
-  __shared__ double red[kWaves];
-  if (blockIdx.x == 0) {
-    const double s = sum_partials(A.part, A.n_part, red);
-    if (threadIdx.x == 0) *A.res = result_of(s, A);
+__device__ __forceinline__ float tensor_norm(double s, const Args& A) {
+  return static_cast<float>(sqrt(s) * double(A.mul));
+}
+
+// Norms of tensors from their items' sums: blocks 0 .. n_wide - 1 take a
+// tensor of many items each, the others four tensors, a wave each.
+__device__ __forceinline__ void tensor_norms(const Args& A, int b, double* red) {
+  if (b < A.n_wide) {
+    const int t = A.wide[b];
+    const Range r = A.ranges[t];
+    const double s = sum_partials(A.isum + r.beg, r.end - r.beg, red);
+    if (threadIdx.x == 0) A.norms[t] = tensor_norm(s, A);
     return;
   }
-  const int64_t t = int64_t(blockIdx.x - 1) * kWaves + (threadIdx.x >> 6);
+  const int64_t t = int64_t(b - A.n_wide) * kWaves + (threadIdx.x >> 6);
   if (t >= A.n_tensors) return;
-  const int lane = threadIdx.x & 63;
   const Range r = A.ranges[t];
-  double s = 0.0;
-  for (int i = r.beg + lane; i < r.end; i += 64) s += A.isum[i];
-  s = wave_sum(s);
-  if (lane == 0) A.norms[t] = static_cast<float>(sqrt(s) * double(A.mul));
+  if (r.end - r.beg > kWide) return;
+  const int lane = threadIdx.x & 63;
+  const double s = wave_sum(sum_share<64>(A.isum + r.beg, r.end - r.beg, lane));
+  if (lane == 0) A.norms[t] = tensor_norm(s, A);
+}
+
+// Block 0: the norm and the factor. The others: tensor norms.
+__global__ __launch_bounds__(kThreads) void clip_finish_kernel(Args A) {
+  __shared__ double red[kWaves];
+  if (blockIdx.x > 0) {
+    tensor_norms(A, blockIdx.x - 1, red);
+    return;
+  }
+  const double s = sum_partials(A.part, A.n_part, red);
+  if (threadIdx.x == 0) *A.res = result_of(s, A);
 }
 
 // o = g s for n consecutive elements, aligned on the output.
@@ -284,17 +317,50 @@ __device__ __forceinline__ void scale_item(const Item& it, float s, int lane) {
     scale_run<E>(g + int64_t(r) * it.ld, o + int64_t(r) * it.out_ld, it.n, s, lane);
 }
 
-// out = g factor, an item a wave. In place with a factor of one there is
-// nothing to do.
-__global__ __launch_bounds__(kThreads) void clip_scale_kernel(Args A) {
-  const int i = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
-  if (i >= A.n_items) return;
-  const Item it = A.items[i];
-  const float s = A.res->scale;
-  if (it.g == it.o && s == 1.f) return;
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void scale_any(const Item& it, float s, int lane) {
+  if (it.g == it.o && s == 1.f) return;  // in place with a factor of one: nothing to do
   if (it.dtype == MUON_F32) scale_item<F32>(it, s, lane);
   else scale_item<Bf16>(it, s, lane);
+}
+
+// out = g factor, an item a wave. Every block adds the partials up itself
+// (16 KB from L2), which takes less time than a launch that does it once;
+// block 0 leaves the result, the blocks behind the items the tensor norms.
+__global__ __launch_bounds__(kThreads) void clip_scale_kernel(Args A, int item_blocks) {
+  __shared__ double red[kWaves];
+  if (int(blockIdx.x) >= item_blocks) {
+    tensor_norms(A, blockIdx.x - item_blocks, red);
+    return;
+  }
+  const muon_clip_result r = result_of(sum_partials(A.part, A.n_part, red), A);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *A.res = r;
+  const int i = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
+  if (i >= A.n_items) return;
+  scale_any(A.items[i], r.scale, threadIdx.x & 63);
+}
+
+// Short lists, where launches are most of the time: one block does the whole
+// call, norm and scaling, sums in LDS.
+__global__ __launch_bounds__(64 * kSmallWaves) void clip_small_kernel(Args A, int scale) {
+  __shared__ double isum[kSmall];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int i = wave; i < A.n_items; i += kSmallWaves) {
+    const Item it = A.items[i];
+    const double s = wave_sum(it.dtype == MUON_F32 ? ssq_item<F32>(it, lane) : ssq_item<Bf16>(it, lane));
+    if (lane == 0) isum[i] = s;
+  }
+  __syncthreads();
+  const muon_clip_result r = result_of(wave_sum(lane < A.n_items ? isum[lane] : 0.0), A);
+  if (threadIdx.x == 0) *A.res = r;
+  if (A.norms != nullptr)
+    for (int t = threadIdx.x; t < A.n_tensors; t += 64 * kSmallWaves) {
+      const Range q = A.ranges[t];
+      double s = 0.0;
+      for (int i = q.beg; i < q.end; ++i) s += isum[i];
+      A.norms[t] = tensor_norm(s, A);
+    }
+  if (scale)
+    for (int i = wave; i < A.n_items; i += kSmallWaves) scale_any(A.items[i], r.scale, lane);
 }
 
 // ------------------------------------------------------------------ host
@@ -307,6 +373,7 @@ struct Interval {
 struct Host {
   std::vector<Item> items;
   std::vector<Range> ranges;
+  std::vector<int32_t> wide;
   bool all_out = true;  // every non-empty tensor has an out
 };
 
@@ -387,6 +454,7 @@ muon_status build(const muon_clip_tensor* ts, int32_t n, Host* H) {
       }
     }
     R.end = static_cast<int32_t>(H->items.size());
+    if (R.end - R.beg > kWide) H->wide.push_back(i);
   }
   return MUON_OK;
 }
@@ -403,7 +471,8 @@ struct muon_clip_plan_s {
   void* dmem = nullptr;
   const muon_clip::Item* d_items = nullptr;
   const muon_clip::Range* d_ranges = nullptr;
-  int32_t n_items = 0, n_tensors = 0;
+  const int32_t* d_wide = nullptr;
+  int32_t n_items = 0, n_tensors = 0, n_wide = 0;
   bool all_out = true;
   size_t ws_bytes = 0;
 };
@@ -432,6 +501,8 @@ muon_status enqueue(muon_clip_plan* plan, const muon_clip_config* cfg, muon_clip
   a.n_part = blocks;
   a.ranges = plan->d_ranges;
   a.n_tensors = plan->n_tensors;
+  a.wide = plan->d_wide;
+  a.n_wide = plan->n_wide;
   a.norms = norms;
   a.res = result;
   a.max_norm = cfg->max_norm;
@@ -439,10 +510,12 @@ muon_status enqueue(muon_clip_plan* plan, const muon_clip_config* cfg, muon_clip
   a.mul = cfg->grad_mul;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const dim3 block(kThreads);
-  if (blocks > 0) {
-    hipLaunchKernelGGL(clip_norm_kernel, dim3(unsigned(blocks)), block, 0, s, a);
-    if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
+  if (plan->n_items <= kSmall) {
+    hipLaunchKernelGGL(clip_small_kernel, dim3(1), dim3(64 * kSmallWaves), 0, s, a, scale ? 1 : 0);
+    return hipGetLastError() == hipSuccess ? MUON_OK : MUON_E_LAUNCH;
   }
+  hipLaunchKernelGGL(clip_norm_kernel, dim3(unsigned(blocks)), block, 0, s, a);
+  if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
   if (blocks > 4 * kReduced) {
     const int32_t each = (blocks + kReduced - 1) / kReduced;
     hipLaunchKernelGGL(clip_reduce_kernel, dim3(kReduced), block, 0, s, a.part, a.part + blocks, blocks, each);
@@ -450,14 +523,12 @@ muon_status enqueue(muon_clip_plan* plan, const muon_clip_config* cfg, muon_clip
     a.part += blocks;
     a.n_part = kReduced;
   }
-  const unsigned fin = 1u + (norms ? unsigned((plan->n_tensors + kWaves - 1) / kWaves) : 0u);
-  hipLaunchKernelGGL(clip_finish_kernel, dim3(fin), block, 0, s, a);
-  if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
-  if (scale && blocks > 0) {
-    hipLaunchKernelGGL(clip_scale_kernel, dim3(unsigned(blocks)), block, 0, s, a);
-    if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
-  }
-  return MUON_OK;
+  const unsigned extra = norms ? unsigned(plan->n_wide + (plan->n_tensors + kWaves - 1) / kWaves) : 0u;
+  if (scale)
+    hipLaunchKernelGGL(clip_scale_kernel, dim3(unsigned(blocks) + extra), block, 0, s, a, blocks);
+  else
+    hipLaunchKernelGGL(clip_finish_kernel, dim3(1u + extra), block, 0, s, a);
+  return hipGetLastError() == hipSuccess ? MUON_OK : MUON_E_LAUNCH;
 }
 
 }  // namespace
@@ -489,14 +560,17 @@ muon_status muon_clip_plan_create(const muon_clip_tensor* ts, int32_t n, muon_cl
         std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
       return MUON_E_DEVICE;
     const size_t ib = (sizeof(muon_clip::Item) * H.items.size() + 255) / 256 * 256;
-    std::vector<char> h(std::max<size_t>(256, ib + sizeof(muon_clip::Range) * H.ranges.size()), 0);
+    const size_t rb = ib + (sizeof(muon_clip::Range) * H.ranges.size() + 255) / 256 * 256;
+    std::vector<char> h(std::max<size_t>(256, rb + sizeof(int32_t) * H.wide.size()), 0);
     if (!H.items.empty()) std::memcpy(h.data(), H.items.data(), sizeof(muon_clip::Item) * H.items.size());
     if (!H.ranges.empty()) std::memcpy(h.data() + ib, H.ranges.data(), sizeof(muon_clip::Range) * H.ranges.size());
+    if (!H.wide.empty()) std::memcpy(h.data() + rb, H.wide.data(), sizeof(int32_t) * H.wide.size());
     muon_clip_plan_s* p = new (std::nothrow) muon_clip_plan_s();
     if (!p) return MUON_E_ALLOC;
     p->device = dev;
     p->n_items = static_cast<int32_t>(H.items.size());
     p->n_tensors = n;
+    p->n_wide = static_cast<int32_t>(H.wide.size());
     p->all_out = H.all_out;
     p->ws_bytes = muon_clip::workspace_of(H.items.size());
     if (hipMalloc(&p->dmem, h.size()) != hipSuccess) {
@@ -512,6 +586,7 @@ muon_status muon_clip_plan_create(const muon_clip_tensor* ts, int32_t n, muon_cl
     }
     p->d_items = static_cast<const muon_clip::Item*>(p->dmem);
     p->d_ranges = reinterpret_cast<const muon_clip::Range*>(static_cast<char*>(p->dmem) + ib);
+    p->d_wide = reinterpret_cast<const int32_t*>(static_cast<char*>(p->dmem) + rb);
     *plan = p;
     return MUON_OK;
   } catch (...) {
