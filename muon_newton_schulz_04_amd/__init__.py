@@ -233,10 +233,17 @@ def make_config(a: float, b: float, c: float, steps: int, momentum: float = 0.0,
     return MuonConfig(a, b, c, int(steps), momentum, 1 if nesterov else 0, eps, int(precision))
 
 
+def _current_stream(index: int) -> int:
+    # the handle alone: building the Stream object around it takes about 2 us
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _stream_handle(stream) -> Optional[int]:
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _current_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -691,21 +698,23 @@ class ClipPlan:
                                   or t.device != self.device):
                 raise ValueError(f"result and norms are contiguous float32 tensors of 2 and {self.n} "
                                  f"elements on {self.device}")
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        if workspace is None:
+        if workspace is None and stream is None:
+            workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+        elif workspace is None:
             # allocated and, once dropped, reused in the order of the stream that uses it
             s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), self.device)
             with torch.cuda.stream(s):
                 workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
         cfg = MuonClipConfig(float(max_norm), float(eps), float(grad_mul))
+        index = self.device.index
+        handle = _current_stream(index) if stream is None else _stream_handle(stream)
         args = (self.handle, ctypes.byref(cfg), result.data_ptr(), _ptr(norms), workspace.data_ptr(),
-                workspace.numel() * workspace.element_size(), _stream_handle(stream))
+                workspace.numel() * workspace.element_size(), handle)
         fn = getattr(load_library(), entry)
-        if torch.cuda.current_device() == self.device.index:
+        if torch.cuda.current_device() == index:
             _check(fn(*args), entry)
         else:
-            with torch.cuda.device(self.device):
+            with torch.cuda.device(index):
                 _check(fn(*args), entry)
         return result
 

@@ -32,7 +32,9 @@ namespace muon_adam {
 
 constexpr int kChunk = 16384;  // elements per work item
 constexpr int kThreads = 256;
-constexpr int kVec = 8;        // elements per thread per pass
+constexpr int kVec = 8;        // elements per thread
+constexpr int kBlock = kThreads * kVec;
+constexpr int kSplit = kChunk / kBlock;  // blocks per work item
 
 struct Tensor {
   void* p;
@@ -41,8 +43,6 @@ struct Tensor {
   float* v;
   int64_t numel;
   float lr_mul, wd_mul;
-  int32_t vec;  // 16-byte vector access legal for all four buffers
-  int32_t pad_;
 };
 
 struct Item {
@@ -95,6 +95,9 @@ __device__ __forceinline__ float adam_elem(float p, float g, float& m, float& v,
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// the same at an element's alignment (the hardware takes any address)
+typedef f32x4 f32x4_u __attribute__((aligned(4)));
+typedef u32x4 u32x4_u __attribute__((aligned(2)));
 
 // Eight consecutive elements of one tensor in registers.
 struct Vec8 {
@@ -104,8 +107,8 @@ struct Vec8 {
 template <typename T>
 __device__ __forceinline__ void load8(const Tensor& t, int64_t e0, Vec8& x) {
   if constexpr (sizeof(T) == 2) {
-    const u32x4 pw = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(t.p) + e0);
-    const u32x4 gw = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(t.g) + e0);
+    const u32x4 pw = *reinterpret_cast<const u32x4_u*>(static_cast<const uint16_t*>(t.p) + e0);
+    const u32x4 gw = *reinterpret_cast<const u32x4_u*>(static_cast<const uint16_t*>(t.g) + e0);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       x.p[2 * q] = __uint_as_float(pw[q] << 16);
@@ -116,8 +119,8 @@ __device__ __forceinline__ void load8(const Tensor& t, int64_t e0, Vec8& x) {
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const f32x4 pv = *reinterpret_cast<const f32x4*>(static_cast<const float*>(t.p) + e0 + 4 * h);
-      const f32x4 gv = *reinterpret_cast<const f32x4*>(static_cast<const float*>(t.g) + e0 + 4 * h);
+      const f32x4 pv = *reinterpret_cast<const f32x4_u*>(static_cast<const float*>(t.p) + e0 + 4 * h);
+      const f32x4 gv = *reinterpret_cast<const f32x4_u*>(static_cast<const float*>(t.g) + e0 + 4 * h);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         x.p[4 * h + q] = pv[q];
@@ -127,8 +130,8 @@ __device__ __forceinline__ void load8(const Tensor& t, int64_t e0, Vec8& x) {
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const f32x4 mv = *reinterpret_cast<const f32x4*>(t.m + e0 + 4 * h);
-    const f32x4 vv = *reinterpret_cast<const f32x4*>(t.v + e0 + 4 * h);
+    const f32x4 mv = *reinterpret_cast<const f32x4_u*>(t.m + e0 + 4 * h);
+    const f32x4 vv = *reinterpret_cast<const f32x4_u*>(t.v + e0 + 4 * h);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       x.m[4 * h + q] = mv[q];
@@ -141,20 +144,20 @@ template <typename T>
 __device__ __forceinline__ void store8(const Tensor& t, int64_t e0, const Vec8& x) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    *reinterpret_cast<f32x4*>(t.m + e0 + 4 * h) =
+    *reinterpret_cast<f32x4_u*>(t.m + e0 + 4 * h) =
         f32x4{x.m[4 * h], x.m[4 * h + 1], x.m[4 * h + 2], x.m[4 * h + 3]};
-    *reinterpret_cast<f32x4*>(t.v + e0 + 4 * h) =
+    *reinterpret_cast<f32x4_u*>(t.v + e0 + 4 * h) =
         f32x4{x.v[4 * h], x.v[4 * h + 1], x.v[4 * h + 2], x.v[4 * h + 3]};
   }
   if constexpr (sizeof(T) == 2) {
     u32x4 pw;
 #pragma unroll
     for (int q = 0; q < 4; ++q) pw[q] = uint32_t(f2bf(x.p[2 * q])) | (uint32_t(f2bf(x.p[2 * q + 1])) << 16);
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(t.p) + e0) = pw;
+    *reinterpret_cast<u32x4_u*>(static_cast<uint16_t*>(t.p) + e0) = pw;
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<f32x4*>(static_cast<float*>(t.p) + e0 + 4 * h) =
+      *reinterpret_cast<f32x4_u*>(static_cast<float*>(t.p) + e0 + 4 * h) =
           f32x4{x.p[4 * h], x.p[4 * h + 1], x.p[4 * h + 2], x.p[4 * h + 3]};
   }
 }
@@ -164,30 +167,12 @@ __device__ __forceinline__ void update8(Vec8& x, const Consts& k) {
   for (int e = 0; e < kVec; ++e) x.p[e] = adam_elem(x.p[e], x.g[e], x.m[e], x.v[e], k);
 }
 
-// Elements e0 .. min(e0 + 8, end) - 1, vector or scalar.
-template <typename T>
-__device__ __forceinline__ void run8(const Tensor& t, int64_t e0, int64_t end, const Consts& k) {
-  if (t.vec && e0 + kVec <= end) {
-    Vec8 x;
-    load8<T>(t, e0, x);
-    update8(x, k);
-    store8<T>(t, e0, x);
-  } else {
-    const int64_t e1 = e0 + kVec < end ? e0 + kVec : end;
-    for (int64_t e = e0; e < e1; ++e) {
-      float m = t.m[e], v = t.v[e];
-      const float p = adam_elem(PElem<T>::load(t.p, e), PElem<T>::load(t.g, e), m, v, k);
-      t.m[e] = m;
-      t.v[e] = v;
-      PElem<T>::store(t.p, e, p);
-    }
-  }
-}
-
 template <typename T>
 __global__ __launch_bounds__(kThreads) void adam_kernel(Args A) {
-  const Item it = A.items[blockIdx.x];
+  const Item it = A.items[blockIdx.x / kSplit];
   const Tensor t = A.ts[it.t];
+  const int64_t base = int64_t(it.chunk) * kChunk + int64_t(blockIdx.x % kSplit) * kBlock;
+  if (base >= t.numel) return;
   const float lr_e = A.lr * t.lr_mul;
   Consts k;
   k.b1 = A.b1;
@@ -199,23 +184,20 @@ __global__ __launch_bounds__(kThreads) void adam_kernel(Args A) {
   k.step = lr_e * A.inv_bc1;
   k.isb2 = A.inv_sqrt_bc2;
   k.gs = A.gscale ? *A.gscale : 1.f;
-  const int64_t base = int64_t(it.chunk) * kChunk;
-  const int64_t end = base + kChunk < t.numel ? base + kChunk : t.numel;
-  // two vectors per thread per pass, both loaded before either is updated
-  constexpr int64_t kPass = int64_t(kThreads) * kVec;
-  for (int64_t e0 = base + int64_t(threadIdx.x) * kVec; e0 < end; e0 += 2 * kPass) {
-    const int64_t e1 = e0 + kPass;
-    if (t.vec && e1 + kVec <= end) {
-      Vec8 x, y;
-      load8<T>(t, e0, x);
-      load8<T>(t, e1, y);
-      update8(x, k);
-      update8(y, k);
-      store8<T>(t, e0, x);
-      store8<T>(t, e1, y);
-    } else {
-      run8<T>(t, e0, end, k);
-      if (e1 < end) run8<T>(t, e1, end, k);
+  const int64_t end = base + kBlock < t.numel ? base + kBlock : t.numel;
+  const int64_t e0 = base + int64_t(threadIdx.x) * kVec;
+  if (e0 + kVec <= end) {
+    Vec8 x;
+    load8<T>(t, e0, x);
+    update8(x, k);
+    store8<T>(t, e0, x);
+  } else {
+    for (int64_t e = e0; e < end; ++e) {
+      float m = t.m[e], v = t.v[e];
+      const float p = adam_elem(PElem<T>::load(t.p, e), PElem<T>::load(t.g, e), m, v, k);
+      t.m[e] = m;
+      t.v[e] = v;
+      PElem<T>::store(t.p, e, p);
     }
   }
 }
@@ -258,7 +240,6 @@ muon_status build(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype, std::
     D.numel = T.numel;
     D.lr_mul = T.lr_mul;
     D.wd_mul = T.wd_mul;
-    D.vec = (addr(T.param) | addr(T.grad) | addr(T.exp_avg) | addr(T.exp_avg_sq)) % 16 == 0;
     const int64_t chunks = (T.numel + kChunk - 1) / kChunk;
     for (int64_t c = 0; c < chunks; ++c) items->push_back({i, static_cast<int32_t>(c)});
   }
@@ -361,7 +342,7 @@ muon_status muon_adam_plan_step(muon_adam_plan* plan, const muon_adam_config* cf
   a.inv_sqrt_bc2 =
       static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(double(cfg->beta2), double(cfg->step))));
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(plan->nitems)), block(muon_adam::kThreads);
+  const dim3 grid(static_cast<unsigned>(plan->nitems * muon_adam::kSplit)), block(muon_adam::kThreads);
   if (plan->dtype == MUON_F32)
     hipLaunchKernelGGL(muon_adam::adam_kernel<float>, grid, block, 0, s, a);
   else

@@ -33,6 +33,7 @@ constexpr int kReduced = 1024;            // partials of a long list are first a
 constexpr int kWide = 512;                // tensors of more items get a block for their norm, others a wave
 constexpr int kSmall = 64;                // lists of at most this many items run in one block
 constexpr int kSmallWaves = 16;
+constexpr int64_t kKeepBytes = 256 << 20; // what the norm of a clipping call leaves in the last-level cache (256 MB)
 
 // One wave's work: `rows` rows of `n` consecutive elements.
 struct Item {
@@ -41,7 +42,7 @@ struct Item {
   int64_t ld, out_ld;  // elements
   int32_t n, rows;
   int32_t dtype;       // muon_dtype
-  int32_t pad_;
+  uint32_t magic;      // rows > 1: (2^32 - 1) / vectors in a row, see div_row
 };
 
 struct Range {
@@ -51,6 +52,7 @@ struct Range {
 struct Args {
   const Item* items;
   int32_t n_items;
+  int32_t n_stream;    // the norm reads the first n_stream items past the caches
   int32_t n_part;      // block sums in `part`
   double* part;        // one sum per block of the norm kernel
   double* isum;        // one sum per item (nullptr: not wanted)
@@ -103,7 +105,33 @@ struct Bf16 {
   }
 };
 
+// One vector at an element's alignment; NT: not kept in the caches.
+template <typename E, bool NT>
+__device__ __forceinline__ typename E::Vec load_vec(const typename E::T* p) {
+  const typename E::VecU* q = reinterpret_cast<const typename E::VecU*>(p);
+  if constexpr (NT) return __builtin_nontemporal_load(q);
+  else return *q;
+}
+template <typename E>
+__device__ __forceinline__ void store_vec(typename E::T* p, const typename E::Vec& x) {
+  const typename E::VecU y = x;
+  __builtin_nontemporal_store(y, reinterpret_cast<typename E::VecU*>(p));
+}
+
 __device__ __forceinline__ double sq(float x) { return double(x) * double(x); }
+
+// Adds one vector's squares. The barrier keeps the scheduler from converting
+// several vectors ahead: 64 float64 values in flight would leave room for
+// three waves on a SIMD instead of eight.
+template <typename E>
+__device__ __forceinline__ void add_vec(const typename E::Vec& x, double& a, double& b) {
+#pragma unroll
+  for (int e = 0; e < E::V; e += 2) {
+    a += sq(E::get(x, e));
+    b += sq(E::get(x, e + 1));
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
 
 // Elements before the first 16-byte boundary at or after p, at most n.
 template <typename E>
@@ -113,7 +141,7 @@ __device__ __forceinline__ int head_of(const typename E::T* p, int n) {
 }
 
 // A lane's share of the sum of squares of n consecutive elements.
-template <typename E>
+template <typename E, bool NT>
 __device__ __forceinline__ double ssq_run(const typename E::T* p, int n, int lane) {
   double a = 0.0, b = 0.0;
   const int head = head_of<E>(p, n);
@@ -121,50 +149,78 @@ __device__ __forceinline__ double ssq_run(const typename E::T* p, int n, int lan
   p += head;
   n -= head;
   const int nv = n / E::V;
-  const typename E::Vec* v = reinterpret_cast<const typename E::Vec*>(p);
   constexpr int U = 8;
   int k = lane;
+#pragma unroll 1
   for (; k + 64 * (U - 1) < nv; k += 64 * U) {
     typename E::Vec x[U];
 #pragma unroll
-    for (int j = 0; j < U; ++j) x[j] = v[k + 64 * j];
+    for (int j = 0; j < U; ++j) x[j] = load_vec<E, NT>(p + int64_t(k + 64 * j) * E::V);
 #pragma unroll
-    for (int j = 0; j < U; ++j)
-#pragma unroll
-      for (int e = 0; e < E::V; e += 2) {
-        a += sq(E::get(x[j], e));
-        b += sq(E::get(x[j], e + 1));
-      }
+    for (int j = 0; j < U; ++j) add_vec<E>(x[j], a, b);
   }
+#pragma unroll 1
   for (; k < nv; k += 64) {
-    const typename E::Vec x = v[k];
-#pragma unroll
-    for (int e = 0; e < E::V; e += 2) {
-      a += sq(E::get(x, e));
-      b += sq(E::get(x, e + 1));
-    }
+    const typename E::Vec x = load_vec<E, NT>(p + int64_t(k) * E::V);
+    add_vec<E>(x, a, b);
   }
   const int t = nv * E::V + lane;
   if (t < n) b += sq(E::load(p + t));
   return a + b;
 }
 
-template <typename E>
+// k / d for magic = (2^32 - 1) / d: 2^32 - magic d lies in [1, d], so the
+// product's high word is the quotient or one less.
+__device__ __forceinline__ uint32_t div_row(uint32_t k, uint32_t d, uint32_t magic) {
+  const uint32_t q = __umulhi(k, magic);
+  return k - q * d >= d ? q + 1 : q;
+}
+
+// Strided rows: the vectors of all rows in one index space (rows may start
+// at any element, so the accesses are those of an element's alignment), then
+// the elements behind each row's last vector.
+template <typename E, bool NT>
+__device__ __forceinline__ double ssq_rows(const typename E::T* g, const Item& it, int lane) {
+  const uint32_t vpr = static_cast<uint32_t>(it.n) / E::V, nv = vpr * static_cast<uint32_t>(it.rows);
+  double a = 0.0, b = 0.0;
+  auto at = [&](uint32_t k) {
+    const uint32_t r = div_row(k, vpr, it.magic);
+    return g + int64_t(r) * it.ld + (k - r * vpr) * E::V;
+  };
+  constexpr uint32_t U = 8;
+  uint32_t k = lane;
+#pragma unroll 1
+  for (; k + 64 * (U - 1) < nv; k += 64 * U) {
+    typename E::Vec x[U];
+#pragma unroll
+    for (uint32_t j = 0; j < U; ++j) x[j] = load_vec<E, NT>(at(k + 64 * j));
+#pragma unroll
+    for (uint32_t j = 0; j < U; ++j) add_vec<E>(x[j], a, b);
+  }
+#pragma unroll 1
+  for (; k < nv; k += 64) {
+    const typename E::Vec x = load_vec<E, NT>(at(k));
+    add_vec<E>(x, a, b);
+  }
+  const uint32_t done = vpr * E::V, tail = static_cast<uint32_t>(it.n) - done;
+#pragma unroll 1
+  for (uint32_t e = lane; e < tail * static_cast<uint32_t>(it.rows); e += 64) {
+    const uint32_t r = e / tail;
+    a += sq(E::load(g + int64_t(r) * it.ld + done + (e - r * tail)));
+  }
+  return a + b;
+}
+
+template <typename E, bool NT>
 __device__ __forceinline__ double ssq_item(const Item& it, int lane) {
   typedef typename E::T T;
   const T* g = reinterpret_cast<const T*>(it.g);
-  if (it.rows > 1 && it.n < 64 * E::V) {  // short rows: one element a lane, rows one after the other
-    double a = 0.0;
-    const uint32_t all = static_cast<uint32_t>(it.rows) * static_cast<uint32_t>(it.n);
-    for (uint32_t e = lane; e < all; e += 64) {
-      const uint32_t r = e / static_cast<uint32_t>(it.n), c = e - r * static_cast<uint32_t>(it.n);
-      a += sq(E::load(g + int64_t(r) * it.ld + c));
-    }
-    return a;
-  }
-  double a = 0.0;
-  for (int r = 0; r < it.rows; ++r) a += ssq_run<E>(g + int64_t(r) * it.ld, it.n, lane);
-  return a;
+  return it.rows > 1 ? ssq_rows<E, NT>(g, it, lane) : ssq_run<E, NT>(g, it.n, lane);
+}
+
+template <bool NT>
+__device__ __forceinline__ double ssq_any(const Item& it, int lane) {
+  return it.dtype == MUON_F32 ? ssq_item<F32, NT>(it, lane) : ssq_item<Bf16, NT>(it, lane);
 }
 
 __device__ __forceinline__ double wave_sum(double x) {
@@ -209,14 +265,14 @@ __device__ __forceinline__ muon_clip_result result_of(double total, const Args& 
 }
 
 // Sums of squares: block b takes items 4 b .. 4 b + 3, a wave each.
-__global__ __launch_bounds__(kThreads) void clip_norm_kernel(Args A) {
+__global__ __launch_bounds__(kThreads, 8) void clip_norm_kernel(Args A) {
   __shared__ double red[kWaves];
   const int lane = threadIdx.x & 63;
   const int i = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
   double s = 0.0;
   if (i < A.n_items) {
     const Item it = A.items[i];
-    s = wave_sum(it.dtype == MUON_F32 ? ssq_item<F32>(it, lane) : ssq_item<Bf16>(it, lane));
+    s = wave_sum(i < A.n_stream ? ssq_any<true>(it, lane) : ssq_any<false>(it, lane));
     if (A.isum != nullptr && lane == 0) A.isum[i] = s;
   }
   if (lane == 0) red[threadIdx.x >> 6] = s;
@@ -281,23 +337,58 @@ __device__ __forceinline__ void scale_run(const typename E::T* g, typename E::T*
   o += head;
   n -= head;
   const int nv = n / E::V;
-  const typename E::VecU* v = reinterpret_cast<const typename E::VecU*>(g);
-  typename E::Vec* w = reinterpret_cast<typename E::Vec*>(o);
   constexpr int U = 4;
   int k = lane;
+#pragma unroll 1
   for (; k + 64 * (U - 1) < nv; k += 64 * U) {
     typename E::Vec x[U];
 #pragma unroll
-    for (int j = 0; j < U; ++j) x[j] = v[k + 64 * j];
+    for (int j = 0; j < U; ++j) x[j] = load_vec<E, true>(g + int64_t(k + 64 * j) * E::V);
 #pragma unroll
-    for (int j = 0; j < U; ++j) w[k + 64 * j] = E::scale(x[j], s);
+    for (int j = 0; j < U; ++j) store_vec<E>(o + int64_t(k + 64 * j) * E::V, E::scale(x[j], s));
   }
+#pragma unroll 1
   for (; k < nv; k += 64) {
-    const typename E::Vec x = v[k];
-    w[k] = E::scale(x, s);
+    const typename E::Vec x = load_vec<E, true>(g + int64_t(k) * E::V);
+    store_vec<E>(o + int64_t(k) * E::V, E::scale(x, s));
   }
   const int t = nv * E::V + lane;
   if (t < n) E::store(o + t, E::load(g + t) * s);
+}
+
+// The same for strided rows (see ssq_rows).
+template <typename E>
+__device__ __forceinline__ void scale_rows(const typename E::T* g, typename E::T* o, const Item& it, float s, int lane) {
+  const uint32_t vpr = static_cast<uint32_t>(it.n) / E::V, nv = vpr * static_cast<uint32_t>(it.rows);
+  constexpr uint32_t U = 4;
+  uint32_t k = lane;
+#pragma unroll 1
+  for (; k + 64 * (U - 1) < nv; k += 64 * U) {
+    typename E::Vec x[U];
+#pragma unroll
+    for (uint32_t j = 0; j < U; ++j) {
+      const uint32_t r = div_row(k + 64 * j, vpr, it.magic), c = (k + 64 * j - r * vpr) * E::V;
+      x[j] = load_vec<E, true>(g + int64_t(r) * it.ld + c);
+    }
+    asm volatile("" : "+v"(k));  // the rows are worked out again: addresses kept take registers that waves need
+#pragma unroll
+    for (uint32_t j = 0; j < U; ++j) {
+      const uint32_t r = div_row(k + 64 * j, vpr, it.magic), c = (k + 64 * j - r * vpr) * E::V;
+      store_vec<E>(o + int64_t(r) * it.out_ld + c, E::scale(x[j], s));
+    }
+  }
+#pragma unroll 1
+  for (; k < nv; k += 64) {
+    const uint32_t r = div_row(k, vpr, it.magic), c = (k - r * vpr) * E::V;
+    const typename E::Vec x = load_vec<E, true>(g + int64_t(r) * it.ld + c);
+    store_vec<E>(o + int64_t(r) * it.out_ld + c, E::scale(x, s));
+  }
+  const uint32_t done = vpr * E::V, tail = static_cast<uint32_t>(it.n) - done;
+#pragma unroll 1
+  for (uint32_t e = lane; e < tail * static_cast<uint32_t>(it.rows); e += 64) {
+    const uint32_t r = e / tail, c = done + (e - r * tail);
+    E::store(o + int64_t(r) * it.out_ld + c, E::load(g + int64_t(r) * it.ld + c) * s);
+  }
 }
 
 template <typename E>
@@ -305,16 +396,8 @@ __device__ __forceinline__ void scale_item(const Item& it, float s, int lane) {
   typedef typename E::T T;
   const T* g = reinterpret_cast<const T*>(it.g);
   T* o = reinterpret_cast<T*>(it.o);
-  if (it.rows > 1 && it.n < 64 * E::V) {
-    const uint32_t all = static_cast<uint32_t>(it.rows) * static_cast<uint32_t>(it.n);
-    for (uint32_t e = lane; e < all; e += 64) {
-      const uint32_t r = e / static_cast<uint32_t>(it.n), c = e - r * static_cast<uint32_t>(it.n);
-      E::store(o + int64_t(r) * it.out_ld + c, E::load(g + int64_t(r) * it.ld + c) * s);
-    }
-    return;
-  }
-  for (int r = 0; r < it.rows; ++r)
-    scale_run<E>(g + int64_t(r) * it.ld, o + int64_t(r) * it.out_ld, it.n, s, lane);
+  if (it.rows > 1) scale_rows<E>(g, o, it, s, lane);
+  else scale_run<E>(g, o, it.n, s, lane);
 }
 
 __device__ __forceinline__ void scale_any(const Item& it, float s, int lane) {
@@ -332,11 +415,11 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(Args A, int item_b
     tensor_norms(A, blockIdx.x - item_blocks, red);
     return;
   }
+  const int lane = threadIdx.x & 63;
+  const int i = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
   const muon_clip_result r = result_of(sum_partials(A.part, A.n_part, red), A);
   if (blockIdx.x == 0 && threadIdx.x == 0) *A.res = r;
-  const int i = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
-  if (i >= A.n_items) return;
-  scale_any(A.items[i], r.scale, threadIdx.x & 63);
+  if (i < A.n_items) scale_any(A.items[i], r.scale, lane);
 }
 
 // Short lists, where launches are most of the time: one block does the whole
@@ -346,7 +429,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void clip_small_kernel(Args A, in
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int i = wave; i < A.n_items; i += kSmallWaves) {
     const Item it = A.items[i];
-    const double s = wave_sum(it.dtype == MUON_F32 ? ssq_item<F32>(it, lane) : ssq_item<Bf16>(it, lane));
+    const double s = wave_sum(ssq_any<false>(it, lane));
     if (lane == 0) isum[i] = s;
   }
   __syncthreads();
@@ -375,6 +458,7 @@ struct Host {
   std::vector<Range> ranges;
   std::vector<int32_t> wide;
   bool all_out = true;  // every non-empty tensor has an out
+  int32_t n_stream = 0; // items before the last kKeepBytes
 };
 
 int64_t size_of(int32_t dtype) { return dtype == MUON_F32 ? 4 : 2; }
@@ -447,15 +531,23 @@ muon_status build(const muon_clip_tensor* ts, int32_t n, Host* H) {
             H->items.push_back({g + (r * T.ld + c) * es, o ? o + (r * T.out_ld + c) * es : nullptr, 0, 0,
                                 static_cast<int32_t>(std::min(chunk, cols - c)), 1, T.dtype, 0});
       } else {              // whole rows, at most about one item's bytes
-        const int64_t each = std::max<int64_t>(1, chunk / cols);
+        const int64_t each = std::max<int64_t>(1, chunk / cols), vpr = cols * es / 16;
+        const uint32_t magic = static_cast<uint32_t>(UINT32_MAX / std::max<int64_t>(1, vpr));
         for (int64_t r = 0; r < rows; r += each)
           H->items.push_back({g + r * T.ld * es, o ? o + r * T.out_ld * es : nullptr, T.ld, T.out_ld,
-                              static_cast<int32_t>(cols), static_cast<int32_t>(std::min(each, rows - r)), T.dtype, 0});
+                              static_cast<int32_t>(cols), static_cast<int32_t>(std::min(each, rows - r)), T.dtype, magic});
       }
     }
     R.end = static_cast<int32_t>(H->items.size());
     if (R.end - R.beg > kWide) H->wide.push_back(i);
   }
+  int64_t kept = 0;
+  size_t k = H->items.size();
+  while (k > 0 && kept < kKeepBytes) {
+    const Item& it = H->items[--k];
+    kept += int64_t(it.n) * it.rows * size_of(it.dtype);
+  }
+  H->n_stream = static_cast<int32_t>(k);
   return MUON_OK;
 }
 
@@ -472,7 +564,7 @@ struct muon_clip_plan_s {
   const muon_clip::Item* d_items = nullptr;
   const muon_clip::Range* d_ranges = nullptr;
   const int32_t* d_wide = nullptr;
-  int32_t n_items = 0, n_tensors = 0, n_wide = 0;
+  int32_t n_items = 0, n_tensors = 0, n_wide = 0, n_stream = 0;
   bool all_out = true;
   size_t ws_bytes = 0;
 };
@@ -496,6 +588,7 @@ muon_status enqueue(muon_clip_plan* plan, const muon_clip_config* cfg, muon_clip
   Args a{};
   a.items = plan->d_items;
   a.n_items = plan->n_items;
+  a.n_stream = scale ? plan->n_stream : plan->n_items;
   a.isum = norms ? static_cast<double*>(ws) : nullptr;
   a.part = static_cast<double*>(ws) + plan->n_items;
   a.n_part = blocks;
@@ -570,6 +663,7 @@ muon_status muon_clip_plan_create(const muon_clip_tensor* ts, int32_t n, muon_cl
     p->device = dev;
     p->n_items = static_cast<int32_t>(H.items.size());
     p->n_tensors = n;
+    p->n_stream = H.n_stream;
     p->n_wide = static_cast<int32_t>(H.wide.size());
     p->all_out = H.all_out;
     p->ws_bytes = muon_clip::workspace_of(H.items.size());
