@@ -41,7 +41,7 @@ extern "C" {
 /* One parameter tensor, flattened: numel contiguous elements. numel == 0 is
  * skipped (its pointers are ignored). param and grad are of the set's dtype
  * and aligned to its size; exp_avg / exp_avg_sq are fp32, 4-byte aligned.
- * 16-byte alignment of all four selects the vector path. param, exp_avg and
+ * param, exp_avg and
  * exp_avg_sq are read and written; grad is read; no buffer may overlap
  * another one of the list (grad with grad excepted). */
 typedef struct {
@@ -92,7 +92,8 @@ muon_status muon_adam_plan_set_grad_scale(muon_adam_plan* plan, const float* sca
 /* Frees a plan after waiting for the device (NULL is a no-op). */
 void muon_adam_plan_destroy(muon_adam_plan* plan);
 
-/* Host-only: the number of work items (kernel blocks) a list needs. */
+/* Host-only: the number of work items a list needs (one per 16384 elements
+ * begun of each tensor). */
 muon_status muon_adam_work_items(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype,
                                  int64_t* items);
 

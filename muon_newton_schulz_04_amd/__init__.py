@@ -667,7 +667,9 @@ class ClipPlan:
     clipped gradients (an entry None: that gradient only counts in the norm).
 
     ``result`` holds {norm, scale} of the last call on the device, ``scale`` is a view of
-    its second element (what ``set_grad_scale`` of the optimizer plans takes)."""
+    its second element (what ``set_grad_scale`` of the optimizer plans takes). Calls that
+    overlap in time, graphs replayed at once among them, need a ``workspace``, a ``result``
+    and ``norms`` each (a workspace is allocated per call unless one is given)."""
 
     def __init__(self, grads, outs=None):
         import torch
@@ -687,7 +689,9 @@ class ClipPlan:
         with torch.cuda.device(self.device):
             _check(lib.muon_clip_plan_create(arr, n, ctypes.byref(h)), "muon_clip_plan_create")
         self.handle = h
+        # complete before any stream's call can write it
         self.result = torch.zeros(2, dtype=torch.float32, device=self.device)
+        torch.cuda.current_stream(self.device).synchronize()
         self.scale = self.result[1:2]
 
     def _run(self, entry, max_norm, eps, grad_mul, norms, result, workspace, stream):
@@ -705,6 +709,8 @@ class ClipPlan:
             s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), self.device)
             with torch.cuda.stream(s):
                 workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {self.device}")
         cfg = MuonClipConfig(float(max_norm), float(eps), float(grad_mul))
         index = self.device.index
         handle = _current_stream(index) if stream is None else _stream_handle(stream)

@@ -239,6 +239,47 @@ def test_offsets_beyond_32_bits():
     plan.destroy()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_tensor_of_many_items(dtype):
+    """Tensors of more than 512 work items (4 KB each here) take another path to their norm than short ones."""
+    _, grads = make_list([(1500, 2048), (5,), (4100, 513)], [dtype] * 3, [0, 1, 1], [0, 0, 3], 21)
+    norms = torch.zeros(3, device=DEV)
+    plan = mu.ClipPlan(grads, [torch.zeros_like(g) for g in grads])
+    say(f"clip: many items {dtype}")
+    for call in (plan.norm, plan.step):
+        norms.fill_(-1.0)
+        check_result(plan, call(0.75, norms=norms), norms, grads, 0.75, 1e-6, 1.0)
+    plan.destroy()
+
+
+@pytest.mark.parametrize("items", [1, 15, 16, 17, 18, 64, 65])
+def test_item_counts_around_the_one_launch_limit(items):
+    """Lists of so many work items of 4 KB (the last one shorter): one launch up to 16, two above."""
+    n = items * 1024 - 7
+    for shapes in ([(n,)], [(1024,)] * (items - 1) + [(1017,)]):
+        _, grads = make_list(shapes, ["fp32"] * len(shapes), [0] * len(shapes), [0] * len(shapes), items)
+        before = [g.clone() for g in grads]
+        norms = torch.zeros(len(grads), device=DEV)
+        plan = mu.ClipPlan(grads)
+        say(f"clip: {items} items in {len(shapes)} tensors")
+        check_result(plan, plan.norm(0.5, norms=norms), norms, grads, 0.5, 1e-6, 1.0)
+        s = check_result(plan, plan.step(0.5, norms=norms), norms, before, 0.5, 1e-6, 1.0)
+        check_outs(before, grads, s)
+        plan.destroy()
+
+
+def test_default_stream_handle_and_no_workspace():
+    _, grads = make_list([(4000, 512)], ["bf16"], [0], [0], 14)
+    plan = mu.ClipPlan(grads, [None])
+    say("clip: handle of the default stream")
+    want = plan.norm(1.0).clone()
+    plan.result.zero_()
+    plan.norm(1.0, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(plan.result, want)
+    plan.destroy()
+
+
 def test_deterministic_and_workspace_contents_do_not_matter():
     _, grads = make_list([(3000, 1001), (777,), (512, 512)], ["bf16", "fp32", "bf16"], [1, 0, 2], [7, 0, 0], 8)
     plan = mu.ClipPlan(grads, [None] * 3)
@@ -329,6 +370,9 @@ def test_refusals():
             plan.step(1.0, result=bad)
     with pytest.raises(ValueError):
         plan.step(1.0, norms=torch.zeros(2, device=DEV))
+    for bad in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError):
+            plan.step(1.0, workspace=bad)
     lib = mu.load_library()
     cfg = mu.MuonClipConfig(1.0, 0.0, 1.0)
     args = lambda r, n: (plan.handle, r, n, ws.data_ptr(), ws.numel(), None)  # noqa: E731
