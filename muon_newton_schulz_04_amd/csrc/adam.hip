@@ -39,12 +39,11 @@
 
 namespace muon_adam {
 
-constexpr int kChunk = 16384;  // elements per work item
+constexpr int kChunk = 16384;  // elements per work item (what muon_adam_work_items counts)
 constexpr int kThreads = 256;
 constexpr int kVec = 4;        // consecutive elements per thread
 constexpr int kRuns = 2;       // such runs per thread, kThreads * kVec apart
 constexpr int kBlock = kThreads * kVec * kRuns;
-constexpr int kSplit = kChunk / kBlock;  // blocks per work item
 
 struct Tensor {
   void* p;
@@ -55,9 +54,10 @@ struct Tensor {
   float lr_mul, wd_mul;
 };
 
+// A block's work.
 struct Item {
-  int32_t t;      // tensor index
-  int32_t chunk;  // elements chunk * kChunk .. + kChunk - 1 of the tensor
+  int32_t t;    // tensor index
+  int32_t run;  // elements run * kBlock .. + kBlock - 1 of the tensor
 };
 
 struct Args {
@@ -138,10 +138,9 @@ __device__ __forceinline__ void store4(uint16_t* a, const float (&x)[kVec]) {
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void adam_kernel(Args A) {
-  const Item it = A.items[blockIdx.x / kSplit];
+  const Item it = A.items[blockIdx.x];
   const Tensor t = A.ts[it.t];
-  const int64_t base = int64_t(it.chunk) * kChunk + int64_t(blockIdx.x % kSplit) * kBlock;
-  if (base >= t.numel) return;
+  const int64_t base = int64_t(it.run) * kBlock;
   const float lr_e = A.lr * t.lr_mul;
   Consts k;
   k.b1 = A.b1;
@@ -191,15 +190,16 @@ struct Interval {
   bool write;
 };
 
+// blocks: nullptr to count the work items only.
 muon_status build(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype, std::vector<Tensor>* out,
-                  std::vector<Item>* items) {
+                  std::vector<Item>* blocks, int64_t* items) {
   if (dtype != MUON_F32 && dtype != MUON_BF16) return MUON_E_DTYPE;
   if (n < 0 || n > MUON_ADAM_MAX_TENSORS) return MUON_E_SHAPE;
   if (n > 0 && ts == nullptr) return MUON_E_INVALID;
   const size_t es = dtype == MUON_F32 ? 4 : 2;
   std::vector<Interval> iv;
   out->assign(static_cast<size_t>(n), Tensor{});
-  items->clear();
+  *items = 0;
   for (int32_t i = 0; i < n; ++i) {
     const muon_adam_tensor& T = ts[i];
     if (T.numel < 0 || T.numel > MUON_ADAM_MAX_NUMEL) return MUON_E_SHAPE;
@@ -222,8 +222,9 @@ muon_status build(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype, std::
     D.numel = T.numel;
     D.lr_mul = T.lr_mul;
     D.wd_mul = T.wd_mul;
-    const int64_t chunks = (T.numel + kChunk - 1) / kChunk;
-    for (int64_t c = 0; c < chunks; ++c) items->push_back({i, static_cast<int32_t>(c)});
+    *items += (T.numel + kChunk - 1) / kChunk;
+    if (blocks != nullptr)
+      for (int64_t r = 0; r * kBlock < T.numel; ++r) blocks->push_back({i, static_cast<int32_t>(r)});
   }
   std::sort(iv.begin(), iv.end(), [](const Interval& x, const Interval& y) { return x.lo < y.lo; });
   uintptr_t max_hi_any = 0, max_hi_w = 0;
@@ -243,7 +244,7 @@ struct muon_adam_plan_s {
   void* dmem = nullptr;
   const muon_adam::Tensor* d_ts = nullptr;
   const muon_adam::Item* d_items = nullptr;
-  int64_t nitems = 0;
+  int64_t nblocks = 0;
   const float* gscale = nullptr;  // muon_adam_plan_set_grad_scale
 };
 
@@ -253,11 +254,10 @@ muon_status muon_adam_work_items(const muon_adam_tensor* ts, int32_t n, muon_dty
                                  int64_t* items) {
   if (items == nullptr) return MUON_E_INVALID;
   std::vector<muon_adam::Tensor> t;
-  std::vector<muon_adam::Item> it;
-  const muon_status st = muon_adam::build(ts, n, dtype, &t, &it);
-  if (st != MUON_OK) return st;
-  *items = static_cast<int64_t>(it.size());
-  return MUON_OK;
+  int64_t count = 0;
+  const muon_status st = muon_adam::build(ts, n, dtype, &t, nullptr, &count);
+  if (st == MUON_OK) *items = count;
+  return st;
 }
 
 muon_status muon_adam_plan_create(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype,
@@ -266,7 +266,8 @@ muon_status muon_adam_plan_create(const muon_adam_tensor* ts, int32_t n, muon_dt
   *plan = nullptr;
   std::vector<muon_adam::Tensor> t;
   std::vector<muon_adam::Item> it;
-  muon_status st = muon_adam::build(ts, n, dtype, &t, &it);
+  int64_t count = 0;
+  muon_status st = muon_adam::build(ts, n, dtype, &t, &it, &count);
   if (st != MUON_OK) return st;
   int dev = 0;
   hipDeviceProp_t prop;
@@ -277,7 +278,7 @@ muon_status muon_adam_plan_create(const muon_adam_tensor* ts, int32_t n, muon_dt
   if (!p) return MUON_E_ALLOC;
   p->device = dev;
   p->dtype = dtype;
-  p->nitems = static_cast<int64_t>(it.size());
+  p->nblocks = static_cast<int64_t>(it.size());
   const size_t tb = (sizeof(muon_adam::Tensor) * std::max<size_t>(1, t.size()) + 255) / 256 * 256;
   const size_t bytes = tb + sizeof(muon_adam::Item) * std::max<size_t>(1, it.size());
   std::vector<char> h(bytes, 0);
@@ -308,7 +309,7 @@ muon_status muon_adam_plan_step(muon_adam_plan* plan, const muon_adam_config* cf
   if (cfg->beta1 < 0.f || cfg->beta1 >= 1.f || cfg->beta2 < 0.f || cfg->beta2 >= 1.f ||
       cfg->eps < 0.f || cfg->step < 1)
     return MUON_E_INVALID;
-  if (plan->nitems == 0) return MUON_OK;
+  if (plan->nblocks == 0) return MUON_OK;
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess || dev != plan->device) return MUON_E_DEVICE;
   muon_adam::Args a{};
@@ -324,7 +325,7 @@ muon_status muon_adam_plan_step(muon_adam_plan* plan, const muon_adam_config* cf
   a.inv_sqrt_bc2 =
       static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(double(cfg->beta2), double(cfg->step))));
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(plan->nitems * muon_adam::kSplit)), block(muon_adam::kThreads);
+  const dim3 grid(static_cast<unsigned>(plan->nblocks)), block(muon_adam::kThreads);
   if (plan->dtype == MUON_F32)
     hipLaunchKernelGGL(muon_adam::adam_kernel<float>, grid, block, 0, s, a);
   else

@@ -426,6 +426,41 @@ def test_adam_scale_equals_scaled_gradients(dtype, factor):
     assert not torch.equal(plain[-1], got[-1])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("offset", [0, 1, 3])
+def test_adam_sizes_around_its_blocks(dtype, offset):
+    """Sizes around a block's 2048 elements at any alignment, many short tensors, with a scale, against
+    the oracle on the float32 products (moments: a few float32 roundings of each term)."""
+    shapes = [(n,) for n in (1, 3, 2047, 2048, 2049, 4095, 4096, 6145, 16383, 16385)] + [(1 + i % 9,) for i in range(700)]
+    state = []
+    for group in make_adam_state(shapes, TDT[dtype], 40 + offset, "cpu"):
+        flat = torch.zeros(sum(t.numel() for t in group) + offset, dtype=group[0].dtype, device=DEV)
+        views, at = [], offset                   # one bucket: neighbours touch, most are off any boundary
+        for t in group:
+            views.append(flat[at:at + t.numel()].copy_(t.flatten()))
+            at += t.numel()
+        state.append((flat, views))
+    (pf, params), (gf, grads), (mf, ms), (vf, vs) = state
+    s = torch.tensor([0.3], device=DEV)
+    plan = mu.AdamPlan(params, grads, ms, vs)
+    plan.set_grad_scale(s)
+    p0, m0, v0 = (to_f64(t)[offset:] for t in (pf, mf, vf))
+    gs = oracle.clip_gradient(to_f64(gf)[offset:], f32(0.3), "fp32")
+    say(f"adam sizes {dtype} offset {offset}")
+    plan.step(step=3, **HP)
+    torch.cuda.synchronize()
+    po, mo, vo = oracle.adam_update(p0, gs, m0, v0, step=3, dtype=dtype, **{k: f32(x) for k, x in HP.items()})
+    b1, b2 = f32(HP["beta1"]), f32(HP["beta2"])
+    assert np.all(np.abs(to_f64(mf)[offset:] - mo) <= 2.0 ** -21 * (b1 * np.abs(m0) + (1 - b1) * np.abs(gs)))
+    assert np.all(np.abs(to_f64(vf)[offset:] - vo) <= 2.0 ** -21 * (b2 * v0 + (1 - b2) * gs * gs))
+    bits = 8 if dtype == "bf16" else 24
+    ulp = np.ldexp(1.0, (np.floor(np.log2(np.maximum(np.abs(po), 1e-38))) - (bits - 1)).astype(int))
+    assert np.all(np.abs(to_f64(pf)[offset:] - po) <= ulp + 1e-5 * HP["lr"])
+    for t in (pf, mf, vf):
+        assert not t[:offset].any()              # nothing before the first tensor is written
+    plan.destroy()
+
+
 def test_adam_scale_against_oracle_bf16():
     """A scale whose products are no bf16 values: nothing is rounded to bf16 between the two.
     Moments: a few float32 roundings of each term, as for the step without a scale."""
