@@ -626,14 +626,19 @@ def _clip_tensors(grads, outs):
     if len(outs) != n:
         raise ValueError("grads and outs must have the same length")
     arr = (MuonClipTensor * max(n, 1))()
+    device = grads[0].device if n else None
     for i, (g, o) in enumerate(zip(grads, outs)):
         dt = _dtype_code(g)
-        if g.device != grads[0].device or (o is not None and o.device != g.device):
+        if g.device != device or (o is not None and o is not g and o.device != device):
             raise ValueError("all tensors of a list must be on one device")
-        if o is not None and (o.dtype != g.dtype or o.shape != g.shape):
+        if o is not None and o is not g and (o.dtype != g.dtype or o.shape != g.shape):
             raise ValueError("an out must match its grad's shape and dtype")
-        if g.numel() == 0:
+        numel = g.numel()
+        if numel == 0:
             arr[i] = MuonClipTensor(0, 0, 0, 0, None, None, dt, 0)
+            continue
+        if g.is_contiguous() and (o is None or o is g or o.is_contiguous()):
+            arr[i] = MuonClipTensor(1, numel, numel, numel, g.data_ptr(), _ptr(o), dt, 0)
             continue
         rows, cols, ld, dims = _row_layout(g)
         old = ld
