@@ -70,7 +70,8 @@ typedef struct muon_adam_plan_s muon_adam_plan;
 
 /* Validates the list, splits it into work items of at most 16384 elements
  * and uploads the tensor table and the schedule to the current device (a few
- * KB to MB owned by the plan; *plan receives NULL on error). */
+ * KB to MB owned by the plan; *plan receives NULL on error). MUON_E_SHAPE for
+ * a list of more than 2^24 runs of 2048 elements. */
 muon_status muon_adam_plan_create(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype,
                                   muon_adam_plan** plan);
 

@@ -44,6 +44,7 @@ constexpr int kThreads = 256;
 constexpr int kVec = 4;        // consecutive elements per thread
 constexpr int kRuns = 2;       // such runs per thread, kThreads * kVec apart
 constexpr int kBlock = kThreads * kVec * kRuns;
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // a launch holds under 2^32 threads
 
 struct Tensor {
   void* p;
@@ -223,6 +224,7 @@ muon_status build(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype, std::
     D.lr_mul = T.lr_mul;
     D.wd_mul = T.wd_mul;
     *items += (T.numel + kChunk - 1) / kChunk;
+    if (blocks != nullptr && int64_t(blocks->size()) + (T.numel + kBlock - 1) / kBlock > kMaxBlocks) return MUON_E_SHAPE;
     if (blocks != nullptr)
       for (int64_t r = 0; r * kBlock < T.numel; ++r) blocks->push_back({i, static_cast<int32_t>(r)});
   }
@@ -253,11 +255,15 @@ extern "C" {
 muon_status muon_adam_work_items(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype,
                                  int64_t* items) {
   if (items == nullptr) return MUON_E_INVALID;
-  std::vector<muon_adam::Tensor> t;
-  int64_t count = 0;
-  const muon_status st = muon_adam::build(ts, n, dtype, &t, nullptr, &count);
-  if (st == MUON_OK) *items = count;
-  return st;
+  try {
+    std::vector<muon_adam::Tensor> t;
+    int64_t count = 0;
+    const muon_status st = muon_adam::build(ts, n, dtype, &t, nullptr, &count);
+    if (st == MUON_OK) *items = count;
+    return st;
+  } catch (...) {
+    return MUON_E_ALLOC;
+  }
 }
 
 muon_status muon_adam_plan_create(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype,
@@ -266,9 +272,18 @@ muon_status muon_adam_plan_create(const muon_adam_tensor* ts, int32_t n, muon_dt
   *plan = nullptr;
   std::vector<muon_adam::Tensor> t;
   std::vector<muon_adam::Item> it;
-  int64_t count = 0;
-  muon_status st = muon_adam::build(ts, n, dtype, &t, &it, &count);
-  if (st != MUON_OK) return st;
+  std::vector<char> h;
+  size_t tb = 0, bytes = 0;
+  try {
+    int64_t count = 0;
+    const muon_status st = muon_adam::build(ts, n, dtype, &t, &it, &count);
+    if (st != MUON_OK) return st;
+    tb = (sizeof(muon_adam::Tensor) * std::max<size_t>(1, t.size()) + 255) / 256 * 256;
+    bytes = tb + sizeof(muon_adam::Item) * std::max<size_t>(1, it.size());
+    h.assign(bytes, 0);
+  } catch (...) {
+    return MUON_E_ALLOC;
+  }
   int dev = 0;
   hipDeviceProp_t prop;
   if (hipGetDevice(&dev) != hipSuccess || hipGetDeviceProperties(&prop, dev) != hipSuccess ||
@@ -279,9 +294,6 @@ muon_status muon_adam_plan_create(const muon_adam_tensor* ts, int32_t n, muon_dt
   p->device = dev;
   p->dtype = dtype;
   p->nblocks = static_cast<int64_t>(it.size());
-  const size_t tb = (sizeof(muon_adam::Tensor) * std::max<size_t>(1, t.size()) + 255) / 256 * 256;
-  const size_t bytes = tb + sizeof(muon_adam::Item) * std::max<size_t>(1, it.size());
-  std::vector<char> h(bytes, 0);
   if (!t.empty()) std::memcpy(h.data(), t.data(), sizeof(muon_adam::Tensor) * t.size());
   if (!it.empty()) std::memcpy(h.data() + tb, it.data(), sizeof(muon_adam::Item) * it.size());
   if (hipMalloc(&p->dmem, bytes) != hipSuccess) {

@@ -199,3 +199,16 @@ def test_binding_refuses_mismatched_lists():
         mu.muon_clip_workspace_bytes([torch.zeros(3, dtype=torch.float64)])
     with pytest.raises(ValueError):
         mu.ClipPlan(g)                                     # not in device memory
+
+
+def test_adam_plan_refuses_a_list_beyond_one_launch():
+    """16 tensors of 2^31 elements need 2^24 blocks, one more than a launch holds: refused before any device call."""
+    arr = (mu.MuonAdamTensor * 16)()
+    for i in range(16):
+        at = (1 << 44) + i * (1 << 40)
+        arr[i] = mu.MuonAdamTensor(1 << 31, at, at + (1 << 36), at + (1 << 37), at + (1 << 38), 1.0, 0.0)
+    plan = ctypes.c_void_p(1)
+    lib = mu.load_library()
+    assert lib.muon_adam_plan_create(arr, 16, BF16, ctypes.byref(plan)) == 3 and not plan.value
+    items = ctypes.c_int64(0)
+    assert lib.muon_adam_work_items(arr, 16, BF16, ctypes.byref(items)) == 0 and items.value == 16 << 17
