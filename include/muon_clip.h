@@ -114,7 +114,8 @@ muon_status muon_clip_plan_step(muon_clip_plan* plan, const muon_clip_config* cf
                                 muon_clip_result* result, float* norms, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
-/* Frees a plan after waiting for the device (NULL is a no-op). */
+/* Frees a plan after waiting for the device (NULL is a no-op). A captured
+ * graph reads the plan's tables: it must not be replayed afterwards. */
 void muon_clip_plan_destroy(muon_clip_plan* plan);
 
 #ifdef __cplusplus
