@@ -114,27 +114,59 @@ struct Vec4 {
   float p[kVec], g[kVec], m[kVec], v[kVec];
 };
 
+// NT: past the caches (blocks of whole kBlock elements). Part blocks take
+// plain accesses: 300 tensors of 2000 fp32 elements 4.4 us, 5.4 with the hints
+// (of 5000 such tensors, more than the caches hold, 58 and 53 us).
+template <bool NT>
 __device__ __forceinline__ void load4(const float* a, float (&x)[kVec]) {
-  const f32x4 w = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(a));
+  const f32x4* q4 = reinterpret_cast<const f32x4*>(a);
+  f32x4 w;
+  if constexpr (NT) w = __builtin_nontemporal_load(q4);
+  else w = *q4;
 #pragma unroll
   for (int q = 0; q < 4; ++q) x[q] = w[q];
 }
+template <bool NT>
 __device__ __forceinline__ void load4(const uint16_t* a, float (&x)[kVec]) {
-  const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(a));
+  const u32x2* q2 = reinterpret_cast<const u32x2*>(a);
+  u32x2 w;
+  if constexpr (NT) w = __builtin_nontemporal_load(q2);
+  else w = *q2;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     x[2 * q] = __uint_as_float(w[q] << 16);
     x[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
   }
 }
+template <bool NT>
 __device__ __forceinline__ void store4(float* a, const float (&x)[kVec]) {
   const f32x4 w = {x[0], x[1], x[2], x[3]};
-  __builtin_nontemporal_store(w, reinterpret_cast<f32x4*>(a));
+  if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<f32x4*>(a));
+  else *reinterpret_cast<f32x4*>(a) = w;
 }
+template <bool NT>
 __device__ __forceinline__ void store4(uint16_t* a, const float (&x)[kVec]) {
   const u32x2 w = {uint32_t(f2bf(x[0])) | (uint32_t(f2bf(x[1])) << 16),
                    uint32_t(f2bf(x[2])) | (uint32_t(f2bf(x[3])) << 16)};
-  __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(a));
+  if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(a));
+  else *reinterpret_cast<u32x2*>(a) = w;
+}
+
+// The four arrays of elements e .. e + 3, and back with their update.
+template <typename T, bool NT>
+__device__ __forceinline__ void load_vec4(const Tensor& t, int64_t e, Vec4& x) {
+  load4<NT>(static_cast<const T*>(t.p) + e, x.p);
+  load4<NT>(static_cast<const T*>(t.g) + e, x.g);
+  load4<NT>(t.m + e, x.m);
+  load4<NT>(t.v + e, x.v);
+}
+template <typename T, bool NT>
+__device__ __forceinline__ void update_vec4(const Tensor& t, int64_t e, Vec4& x, const Consts& k) {
+#pragma unroll
+  for (int q = 0; q < kVec; ++q) x.p[q] = adam_elem(x.p[q], x.g[q], x.m[q], x.v[q], k);
+  store4<NT>(t.m + e, x.m);
+  store4<NT>(t.v + e, x.v);
+  store4<NT>(static_cast<T*>(t.p) + e, x.p);
 }
 
 template <typename T>
@@ -153,34 +185,41 @@ __global__ __launch_bounds__(kThreads) void adam_kernel(Args A) {
   k.step = lr_e * A.inv_bc1;
   k.isb2 = A.inv_sqrt_bc2;
   k.gs = A.gscale ? *A.gscale : 1.f;
-  const int64_t end = base + kBlock < t.numel ? base + kBlock : t.numel;
-  if (base + kBlock <= end) {
-    Vec4 x[kRuns];
+  const int64_t left = t.numel - base;
+  Vec4 x[kRuns];
+  if (left >= kBlock) {
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r) {
-      const int64_t e = base + (r * kThreads + threadIdx.x) * kVec;
-      load4(static_cast<const T*>(t.p) + e, x[r].p);
-      load4(static_cast<const T*>(t.g) + e, x[r].g);
-      load4(t.m + e, x[r].m);
-      load4(t.v + e, x[r].v);
-    }
+    for (int r = 0; r < kRuns; ++r) load_vec4<T, true>(t, base + (r * kThreads + threadIdx.x) * kVec, x[r]);
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r) {
-      const int64_t e = base + (r * kThreads + threadIdx.x) * kVec;
+    for (int r = 0; r < kRuns; ++r) update_vec4<T, true>(t, base + (r * kThreads + threadIdx.x) * kVec, x[r], k);
+    return;
+  }
+  // A tensor's last elements: whole vectors, and one element a lane for what
+  // is behind them (for all of it where that is enough: 10000 tensors of 100
+  // elements 9.3 us, 9.7 in vectors). Everything is loaded before the first
+  // store: a loop of one element a lane, each round waited for, took 6.2 us
+  // for 4.9 on 300 tensors of 2000 bf16 elements and 3.6 for 2.9 on one.
+  const int n = static_cast<int>(left), nv = n > kThreads ? n / kVec : 0;
+  const int64_t z = base + nv * kVec + threadIdx.x;
 #pragma unroll
-      for (int q = 0; q < kVec; ++q) x[r].p[q] = adam_elem(x[r].p[q], x[r].g[q], x[r].m[q], x[r].v[q], k);
-      store4(t.m + e, x[r].m);
-      store4(t.v + e, x[r].v);
-      store4(static_cast<T*>(t.p) + e, x[r].p);
-    }
-  } else {
-    for (int64_t e = base + threadIdx.x; e < end; e += kThreads) {
-      float m = t.m[e], v = t.v[e];
-      const float p = adam_elem(PElem<T>::load(t.p, e), PElem<T>::load(t.g, e), m, v, k);
-      t.m[e] = m;
-      t.v[e] = v;
-      PElem<T>::store(t.p, e, p);
-    }
+  for (int r = 0; r < kRuns; ++r)
+    if (r * kThreads + int(threadIdx.x) < nv) load_vec4<T, false>(t, base + (r * kThreads + threadIdx.x) * kVec, x[r]);
+  float zp = 0.f, zg = 0.f, zm = 0.f, zv = 0.f;
+  if (z < t.numel) {
+    zp = PElem<T>::load(t.p, z);
+    zg = PElem<T>::load(t.g, z);
+    zm = t.m[z];
+    zv = t.v[z];
+  }
+#pragma unroll
+  for (int r = 0; r < kRuns; ++r)
+    if (r * kThreads + int(threadIdx.x) < nv)
+      update_vec4<T, false>(t, base + (r * kThreads + threadIdx.x) * kVec, x[r], k);
+  if (z < t.numel) {
+    zp = adam_elem(zp, zg, zm, zv, k);
+    t.m[z] = zm;
+    t.v[z] = zv;
+    PElem<T>::store(t.p, z, zp);
   }
 }
 

@@ -177,3 +177,38 @@ def test_adam_empty_and_zero_sized_lists():
     plan.step(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, wd=0.0, step=1)
     torch.cuda.synchronize()
     plan.destroy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_adam_part_blocks(dtype, offset):
+    """Lengths around the borders inside a tensor's last block of 2048 elements (one element a lane up
+    to 256, vectors of four and up to three elements behind them above), alone and behind two whole blocks,
+    in one buffer: every element is updated once and no other is touched."""
+    lens = [n + k for n in (0, 4096) for k in (1, 2, 63, 64, 65, 255, 256, 257, 258, 259, 260, 261, 511, 512, 513,
+                                               1023, 1024, 1025, 1026, 1027, 1028, 1029, 2043, 2044, 2045, 2046, 2047)]
+    gap = 5                                        # elements between neighbours, never written
+    total = offset + sum(lens) + gap * len(lens)
+    gen = torch.Generator().manual_seed(60 + offset)
+    full = [(0.02 * torch.randn(total, generator=gen)).to(TDT[dtype]), (1e-3 * torch.randn(total, generator=gen)).to(TDT[dtype]),
+            1e-4 * torch.randn(total, generator=gen), 1e-6 * torch.rand(total, generator=gen)]
+    live = torch.zeros(total, dtype=torch.bool)
+    at, spans = offset, []
+    for n in lens:
+        spans.append(slice(at, at + n))
+        live[at:at + n] = True
+        at += n + gap
+    dev = [t.to(DEV) for t in full]
+    plan = mu.AdamPlan(*[[t[s] for s in spans] for t in dev])
+    say(f"adam part blocks {dtype} offset {offset}")
+    plan.step(step=2, **HP)
+    torch.cuda.synchronize()
+    plan.destroy()
+    p0, g, m0, v0 = (to_f64(t) for t in full)
+    po, mo, vo = oracle.adam_update(p0, g, m0, v0, step=2, dtype=dtype, **{k: f32(x) for k, x in HP.items()})
+    on = live.numpy()
+    for t, was, want in zip((dev[0], dev[2], dev[3]), (p0, m0, v0), (po, mo, vo)):
+        got = to_f64(t)
+        assert np.array_equal(got[~on], was[~on])
+        want[~on] = was[~on]
+    check(dev[0], dev[2], dev[3], po, mo, vo, dtype, HP["lr"], m0, v0, g)
