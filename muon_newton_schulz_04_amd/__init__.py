@@ -672,7 +672,8 @@ class ClipPlan:
     clipped gradients (an entry None: that gradient only counts in the norm).
 
     ``result`` holds {norm, scale} of the last call on the device, ``scale`` is a view of
-    its second element (what ``set_grad_scale`` of the optimizer plans takes). Calls that
+    its second element (what ``set_grad_scale`` of the optimizer plans takes; 1 before the
+    first call). Calls that
     overlap in time, graphs replayed at once among them, need a ``workspace``, a ``result``
     and ``norms`` each (a workspace is allocated per call unless one is given)."""
 
@@ -694,8 +695,8 @@ class ClipPlan:
         with torch.cuda.device(self.device):
             _check(lib.muon_clip_plan_create(arr, n, ctypes.byref(h)), "muon_clip_plan_create")
         self.handle = h
-        # complete before any stream's call can write it
-        self.result = torch.zeros(2, dtype=torch.float32, device=self.device)
+        # a factor of one until the first call; complete before any stream's call can write it
+        self.result = torch.tensor([0.0, 1.0], dtype=torch.float32, device=self.device)
         torch.cuda.current_stream(self.device).synchronize()
         self.scale = self.result[1:2]
 

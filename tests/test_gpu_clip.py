@@ -628,3 +628,14 @@ def test_whole_step_captured_and_replayed():
     for st in (eager, graph):
         for k in ("clip", "muon", "adam"):
             st[k].destroy()
+
+
+def test_scale_is_one_before_the_first_norm():
+    """An optimizer step that comes before the plan's first call does not lose its gradients."""
+    _, grads = make_list([(200, 333), (700,)], ["bf16", "fp32"], [0, 0], [0, 0], 23)
+    plan = mu.ClipPlan(grads, [None, None])
+    say("clip: scale before the first norm")
+    assert plan.result.cpu().tolist() == [0.0, 1.0] and plan.scale.item() == 1.0
+    got, want = (adam_run([(2304,), (123, 45)], "bf16", scale=s) for s in (plan.scale, None))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    plan.destroy()
