@@ -203,7 +203,7 @@ muon_status step_impl(muon_plan_s* p, const muon_config* cfg, void* ws, size_t w
   a.tmax_off = H.tmax_off;
   a.x0s_off = H.x0s_off;
   a.hint = p->d_hint;
-  a.gscale = orthogonalize_only ? nullptr : p->gscale;
+  a.gscale = p->gscale;  // never set on the plans behind muon_step and muon_orthogonalize
   // the chained schedule (not under per-kernel timing, which times each
   // kernel's own launch)
   const bool chain = fused && H.chained && p->chain_ok && p->chain_on && !(p->timing == 1 && allow_timing);

@@ -639,3 +639,40 @@ def test_scale_is_one_before_the_first_norm():
     got, want = (adam_run([(2304,), (123, 45)], "bf16", scale=s) for s in (plan.scale, None))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     plan.destroy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_scale_of_a_plan_does_not_reach_the_calls_without_a_plan(dtype):
+    """muon_step and muon_orthogonalize on the very tensors of a plan with a NaN factor, attached before
+    the library has seen the list and after: the results of a list whose plan has none."""
+    gen = torch.Generator().manual_seed(33)
+    mk = lambda f: [view_of(s, dtype, 0, 0, gen, f)[1] for s in [(64, 96), (200, 130)]]  # noqa: E731
+    g, b = mk(0.02), mk(0.01)
+    o = [torch.zeros_like(t) for t in g]
+    cfg = mu.make_config(*QUINTIC, 5, 0.95, True, 1e-7)
+    say(f"muon: no scale without a plan, {dtype}")
+
+    def run(call, *lists):
+        keep = [t.clone() for t in b]
+        call(*lists, cfg)
+        torch.cuda.synchronize()
+        out = [t.clone() for t in o + b]
+        for t, k in zip(b, keep):
+            t.copy_(k)
+        return out
+
+    plan = mu.MuonPlan(g, b, o)
+    plan.set_grad_scale(torch.tensor([math.nan], device=DEV))
+    got = [run(mu.muon_step, g, b, o), run(mu.muon_orthogonalize, g, o)]
+    assert all(torch.isnan(t.float()).all() for t in run(lambda *a: plan.step(a[-1])))
+    got += [run(mu.muon_step, g, b, o), run(mu.muon_orthogonalize, g, o)]
+    plan.destroy()
+    plain = mu.MuonPlan(g, b, o)
+    want = run(lambda *a: plain.step(a[-1]))
+    plain.destroy()
+    alone = mu.MuonPlan(g, None, o)
+    want_x = run(lambda *a: alone.step(mu.make_config(*QUINTIC, 5, 0.0, False, 1e-7)))
+    alone.destroy()
+    for k in (0, 2):
+        assert all(torch.equal(x, y) for x, y in zip(got[k], want))
+        assert all(torch.equal(x, y) for x, y in zip(got[k + 1][:2], want_x[:2]))
