@@ -57,9 +57,11 @@ extern "C" {
  * contiguous tensor of any shape is one row of all its elements. rows == 0
  * or cols == 0 is an empty tensor (N_i = 0; its pointers are ignored). out
  * may be NULL (the plan then computes norms only), equal to grad with the
- * same ld (in place), or a buffer of its own. A written range (from its
- * first to its last element) may not overlap any other range of the list;
- * ranges that are only read may. */
+ * same ld (in place), or a buffer of its own. What is written may not
+ * overlap anything else of the list, else MUON_E_INVALID; what is only read
+ * may. Tensors count from their first to their last element, except column
+ * slices of one matrix: where such ranges run into each other, all of them
+ * with one row stride, tensors in disjoint columns do not overlap. */
 typedef struct {
   int64_t rows;
   int64_t cols;

@@ -669,7 +669,10 @@ def muon_clip_workspace_bytes(grads, outs=None) -> int:
 class ClipPlan:
     """Global norm of a fixed list of gradients (bf16 and float32 may be mixed) and
     clipping by it. ``outs`` None clips in place; a list of tensors receives the
-    clipped gradients (an entry None: that gradient only counts in the norm).
+    clipped gradients. With a None among them the plan computes norms only and
+    refuses ``step``; ``[None] * n`` also takes lists with a gradient twice or with
+    overlapping views, which cannot be clipped in place (column slices of one
+    matrix can, if their columns are disjoint).
 
     ``result`` holds {norm, scale} of the last call on the device, ``scale`` is a view of
     its second element (what ``set_grad_scale`` of the optimizer plans takes; 1 before the

@@ -471,8 +471,11 @@ __global__ __launch_bounds__(64 * kSmall) void clip_small_kernel(Args A, int sca
 
 // ------------------------------------------------------------------ host
 
+// A tensor's place in memory: rows of `width` bytes, `stride` bytes apart
+// (one row: stride 0), from the first byte to behind the last.
 struct Interval {
   uintptr_t lo, hi;
+  uintptr_t width, stride;
   bool write;
 };
 
@@ -485,6 +488,58 @@ struct Host {
 };
 
 int64_t size_of(int32_t dtype) { return dtype == MUON_F32 ? 4 : 2; }
+
+// Whether a written span meets another one (sorted by lo).
+bool spans_meet(const Interval* beg, const Interval* end) {
+  uintptr_t max_hi_any = 0, max_hi_w = 0;
+  for (const Interval* x = beg; x < end; ++x) {
+    if (x->lo < max_hi_w || (x->write && x->lo < max_hi_any)) return true;
+    max_hi_any = std::max(max_hi_any, x->hi);
+    if (x->write) max_hi_w = std::max(max_hi_w, x->hi);
+  }
+  return false;
+}
+
+// The same for tensors whose spans run into each other (sorted by lo), when
+// they are column slices of one matrix: all rows one stride apart, so every
+// byte of a tensor lies in its columns [c, c + width) modulo the stride, and
+// tensors in separate groups of columns share none. True also where that
+// cannot be told (other strides, columns across the end of the stride).
+bool slices_meet(const Interval* beg, const Interval* end) {
+  uintptr_t stride = 0;
+  for (const Interval* x = beg; x < end; ++x) {
+    if (x->stride != 0 && stride != 0 && x->stride != stride) return true;
+    stride = std::max(stride, x->stride);
+  }
+  if (stride == 0) return true;
+  auto column = [=](const Interval& x) { return (x.lo - beg->lo) % stride; };
+  std::vector<Interval> by_column(beg, end);
+  for (const Interval& x : by_column)
+    if (x.width > stride - column(x)) return true;
+  std::stable_sort(by_column.begin(), by_column.end(),
+                   [&](const Interval& x, const Interval& y) { return column(x) < column(y); });
+  for (size_t i = 0, j; i < by_column.size(); i = j) {
+    uintptr_t right = 0;
+    for (j = i; j < by_column.size() && (j == i || column(by_column[j]) < right); ++j)
+      right = std::max(right, column(by_column[j]) + by_column[j].width);
+    std::sort(by_column.begin() + i, by_column.begin() + j,
+              [](const Interval& x, const Interval& y) { return x.lo < y.lo; });
+    if (spans_meet(by_column.data() + i, by_column.data() + j)) return true;
+  }
+  return false;
+}
+
+// Whether a written tensor may share a byte with another one of the list.
+bool overlaps(std::vector<Interval>& iv) {
+  std::sort(iv.begin(), iv.end(), [](const Interval& x, const Interval& y) { return x.lo < y.lo; });
+  const Interval* const p = iv.data();
+  for (size_t i = 0, j; i < iv.size(); i = j) {  // runs of spans that meet
+    uintptr_t hi = 0;
+    for (j = i; j < iv.size() && (j == i || iv[j].lo < hi); ++j) hi = std::max(hi, iv[j].hi);
+    if (spans_meet(p + i, p + j) && slices_meet(p + i, p + j)) return true;
+  }
+  return false;
+}
 
 muon_status build(const muon_clip_tensor* ts, int32_t n, Host* H) {
   if (n < 0 || n > MUON_CLIP_MAX_TENSORS) return MUON_E_SHAPE;
@@ -504,6 +559,7 @@ muon_status build(const muon_clip_tensor* ts, int32_t n, Host* H) {
     const uintptr_t es = static_cast<uintptr_t>(size_of(T.dtype));
     const uintptr_t g = reinterpret_cast<uintptr_t>(T.grad), o = reinterpret_cast<uintptr_t>(T.out);
     if (g % es != 0 || o % es != 0) return MUON_E_ALIGN;
+    const uintptr_t width = static_cast<uintptr_t>(T.cols) * es;
     const uintptr_t span = static_cast<uintptr_t>((T.rows - 1) * T.ld + T.cols) * es;
     if (g > UINTPTR_MAX - span) return MUON_E_SHAPE;
     if (o != 0) {
@@ -512,22 +568,16 @@ muon_status build(const muon_clip_tensor* ts, int32_t n, Host* H) {
       const uintptr_t ospan = static_cast<uintptr_t>((T.rows - 1) * T.out_ld + T.cols) * es;
       if (o > UINTPTR_MAX - ospan) return MUON_E_SHAPE;
       if (g == o && T.rows > 1 && T.ld != T.out_ld) return MUON_E_INVALID;
-      iv.push_back({o, o + ospan, true});
+      iv.push_back({o, o + ospan, width, T.rows > 1 ? static_cast<uintptr_t>(T.out_ld) * es : 0, true});
     } else {
       H->all_out = false;
     }
-    if (g != o) iv.push_back({g, g + span, false});
+    if (g != o) iv.push_back({g, g + span, width, T.rows > 1 ? static_cast<uintptr_t>(T.ld) * es : 0, false});
     total += double(T.rows) * double(T.cols) * double(es);
     elems += T.rows * T.cols;
     if (elems > MUON_CLIP_MAX_NUMEL) return MUON_E_SHAPE;
   }
-  std::sort(iv.begin(), iv.end(), [](const Interval& x, const Interval& y) { return x.lo < y.lo; });
-  uintptr_t max_hi_any = 0, max_hi_w = 0;
-  for (const Interval& x : iv) {
-    if (x.lo < max_hi_w || (x.write && x.lo < max_hi_any)) return MUON_E_INVALID;
-    max_hi_any = std::max(max_hi_any, x.hi);
-    if (x.write) max_hi_w = std::max(max_hi_w, x.hi);
-  }
+  if (overlaps(iv)) return MUON_E_INVALID;
 
   // Items of about equal bytes: at most twice kTargetItems of them (twice
   // 2^42 / kMaxBytes for the longest list) and one more per tensor.

@@ -212,3 +212,78 @@ def test_adam_plan_refuses_a_list_beyond_one_launch():
     assert lib.muon_adam_plan_create(arr, 16, BF16, ctypes.byref(plan)) == 3 and not plan.value
     items = ctypes.c_int64(0)
     assert lib.muon_adam_work_items(arr, 16, BF16, ctypes.byref(items)) == 0 and items.value == 16 << 17
+
+
+# ------------------------------------------------------- column slices
+
+def rect(base, ld, r0, rows, c0, cols, write, dtype=BF16):
+    es = 4 if dtype == F32 else 2
+    at = base + (r0 * ld + c0) * es
+    return (rows, cols, ld, ld if write else 0, at, at if write else 0, dtype, 0)
+
+
+def test_column_slices_of_one_matrix_are_accepted():
+    """q, k and v of a fused gradient, clipped in place: their ranges run into each other, their columns do not."""
+    for dtype in (BF16, F32):
+        d, rows = 48, 64
+        qkv = [rect(B, 3 * d, 0, rows, k * d, d, True, dtype) for k in range(3)]
+        assert status(qkv)[0] == 0 and status(qkv[::-1])[0] == 0
+        assert status(qkv + [rect(B + (1 << 20), 7, 0, 5, 0, 7, True)])[0] == 0
+        assert status(qkv[:2] + [rect(B, 3 * d, 0, rows, 2 * d, d, False, dtype)])[0] == 0      # one of them only read
+        assert status(qkv[1:] + [rect(B, 3 * d, 0, 5, 0, d, True, dtype), rect(B, 3 * d, 5, rows - 5, 0, d, True, dtype)])[0] == 0
+        assert status(qkv[:2] + [rect(B, 3 * d, 9, 1, 2 * d, d, True, dtype)])[0] == 0          # one row of the last
+        for bad in (rect(B, 3 * d, 0, rows, 2 * d - 1, d, True, dtype),                         # a column too far left
+                    rect(B, 3 * d, 0, rows, 2 * d - 1, d, False, dtype),
+                    rect(B, 3 * d, 1, rows, 2 * d + 1, d, True, dtype),                         # into the next row's first column
+                    rect(B, 3 * d, 9, 1, 2 * d, d + 1, True, dtype),
+                    rect(B, 3 * d + 1, 0, rows, 2 * d, d, True, dtype),                         # another stride
+                    rect(B, 3 * d, 3, 2, 0, 3 * d, True, dtype),                                # whole rows
+                    rect(B, 3 * d, 0, rows, d, d, True, dtype)):                                # the same slice twice
+            assert status(qkv[:2] + [bad])[0] == 1 and status([bad] + qkv[:2])[0] == 1
+    x = torch.zeros(20, 30)
+    assert mu.muon_clip_workspace_bytes([x[:, :10], x[:, 10:20], x[:, 20:]]) > 0                # in place
+    assert mu.muon_clip_workspace_bytes([x[:, :10]], [x[:, 20:]]) > 0
+    with pytest.raises(mu.MuonError):
+        mu.muon_clip_workspace_bytes([x[:, :11], x[:, 10:20]])
+
+
+def cells(t):
+    rows, cols, ld, _, at, _, dtype, _ = t
+    es = 4 if dtype == F32 else 2
+    return {at + (r * ld + c) * es + b for r in range(rows) for c in range(cols) for b in range(es)}
+
+
+def meets(ts):
+    made = [(cells(t), t[5] != 0) for t in ts]
+    return any(a[0] & b[0] for i, a in enumerate(made) for b in made[:i] if a[1] or b[1])
+
+
+def test_overlaps_against_every_byte():
+    """Random lists in a small buffer: a list with a shared written byte is never accepted, and a matrix cut
+    into columns (each possibly into rows, all shuffled) always is."""
+    rng = np.random.default_rng(12)
+    kept = refused = 0
+    for _ in range(3000):
+        ld = int(rng.integers(2, 9))
+        ts = []
+        for _ in range(int(rng.integers(2, 5))):
+            cols, stride = int(rng.integers(1, ld + 1)), ld if rng.random() < 0.9 else ld + 1
+            ts.append(rect(B, stride, int(rng.integers(0, 6)), int(rng.integers(1, 5)), int(rng.integers(0, ld)), cols,
+                           rng.random() < 0.6, F32 if rng.random() < 0.1 else BF16))
+        code = status(ts)[0]
+        assert code in (0, 1)
+        if meets(ts):
+            refused += 1
+            assert code == 1
+        kept += code == 0
+    assert kept > 300 and refused > 300
+    for _ in range(500):
+        ld, rows = int(rng.integers(3, 12)), int(rng.integers(1, 9))
+        cuts = [0, *sorted(rng.choice(np.arange(1, ld), size=int(rng.integers(1, ld)), replace=False).tolist()), ld]
+        ts = []
+        for a, b in zip(cuts, cuts[1:]):
+            at = 0 if rng.random() < 0.7 else int(rng.integers(0, rows))
+            mid = int(rng.integers(at, rows + 1))
+            ts += [rect(B, ld, r0, n, a, b - a, rng.random() < 0.7) for r0, n in ((at, mid - at), (mid, rows - mid)) if n]
+        order = rng.permutation(len(ts))
+        assert not meets(ts) and status([ts[i] for i in order])[0] == 0

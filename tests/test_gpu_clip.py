@@ -676,3 +676,29 @@ def test_scale_of_a_plan_does_not_reach_the_calls_without_a_plan(dtype):
     for k in (0, 2):
         assert all(torch.equal(x, y) for x, y in zip(got[k], want))
         assert all(torch.equal(x, y) for x, y in zip(got[k + 1][:2], want_x[:2]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,d", [(5, 3), (70, 65), (3000, 129), (900, 1040)])
+def test_column_slices_in_place(dtype, rows, d):
+    """q, k and v of a fused gradient as three tensors, clipped in place; the columns behind them stay. Then
+    from the first slice into the last one."""
+    buf, x = view_of((rows, 3 * d), dtype, 1, 2, torch.Generator().manual_seed(rows), 0.1)
+    qkv = [x[:, k * d:(k + 1) * d] for k in range(3)]
+    before, keep = [t.clone() for t in qkv], buf.clone()
+    plan = mu.ClipPlan(qkv)
+    norms = torch.zeros(3, device=DEV)
+    say(f"clip: column slices {dtype} {rows} x 3 x {d}")
+    s = check_result(plan, plan.step(0.5, norms=norms), norms, before, 0.5, 1e-6, 1.0)
+    assert s < 1.0
+    check_outs(before, qkv, s)
+    for t, b in zip(qkv, before):
+        t.copy_(b)
+    assert torch.equal(buf, keep)
+    plan.destroy()
+    plan = mu.ClipPlan(qkv[:1], qkv[2:])
+    s = check_result(plan, plan.step(0.5), None, before[:1], 0.5, 1e-6, 1.0)
+    check_outs(before[:1], qkv[2:], s)
+    qkv[2].copy_(before[2])
+    assert torch.equal(buf, keep)
+    plan.destroy()
