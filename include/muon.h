@@ -270,10 +270,13 @@ muon_status muon_plan_step_apply(muon_plan* plan, const muon_config* cfg, const 
  * `scale` of a muon_clip_result (muon_clip.h) this is the Muon step on
  * gradients clipped by their global norm, without a pass that writes them.
  * A factor of one gives the results of a plan without one, bit for bit.
- * `grad` is only read. *scale must stay valid while attached and be written
- * before the step on the step's stream (or ordered before it); a captured
- * graph keeps the pointer it was captured with. MUON_E_ALIGN if scale is
- * not 4-byte aligned. muon_step and muon_orthogonalize have no factor. */
+ * `grad` is only read. *scale must stay valid while attached, be written
+ * before the step on the step's stream (or ordered before it) and not change
+ * until the step has ended, since more than one of its kernels reads it; a
+ * captured graph keeps the pointer it was captured with. Gradients that
+ * muon_clip_plan_step has already multiplied take no factor here: detach it,
+ * or it is applied twice. MUON_E_ALIGN if scale is not 4-byte aligned.
+ * muon_step and muon_orthogonalize have no factor. */
 muon_status muon_plan_set_grad_scale(muon_plan* plan, const float* scale);
 
 /* ---- introspection (tests, benchmarks, profiling) ---------------------- */

@@ -68,10 +68,11 @@ typedef struct {
 
 typedef struct muon_adam_plan_s muon_adam_plan;
 
-/* Validates the list, splits it into work items of at most 16384 elements
- * and uploads the tensor table and the schedule to the current device (a few
- * KB to MB owned by the plan; *plan receives NULL on error). MUON_E_SHAPE for
- * a list of more than 2^24 runs of 2048 elements. */
+/* Validates the list, splits each tensor into blocks of 2048 elements (the
+ * last one shorter) and uploads the tensor table and the schedule to the
+ * current device (a few KB to MB owned by the plan; *plan receives NULL on
+ * error). MUON_E_SHAPE for a list of 2^24 blocks or more, which is more than
+ * one launch holds. */
 muon_status muon_adam_plan_create(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype,
                                   muon_adam_plan** plan);
 
@@ -85,16 +86,19 @@ muon_status muon_adam_plan_step(muon_adam_plan* plan, const muon_adam_config* cf
  * list clipped by its global norm (`scale` of a muon_clip_result,
  * muon_clip.h) needs no pass that writes clipped gradients. A factor of one
  * gives the results of a plan without one, bit for bit. *scale must stay
- * valid while attached and be written before the step on the step's stream
- * (or ordered before it); a captured graph keeps the pointer it was captured
- * with. MUON_E_ALIGN if scale is not 4-byte aligned. */
+ * valid while attached, be written before the step on the step's stream (or
+ * ordered before it) and not change until the step has ended; a captured
+ * graph keeps the pointer it was captured with. Gradients that
+ * muon_clip_plan_step has already multiplied take no factor here: detach it,
+ * or it is applied twice. MUON_E_ALIGN if scale is not 4-byte aligned. */
 muon_status muon_adam_plan_set_grad_scale(muon_adam_plan* plan, const float* scale);
 
 /* Frees a plan after waiting for the device (NULL is a no-op). */
 void muon_adam_plan_destroy(muon_adam_plan* plan);
 
-/* Host-only: the number of work items a list needs (one per 16384 elements
- * begun of each tensor). */
+/* Host-only: validates the list and counts one item per 16384 elements begun
+ * of each tensor, a measure of its size that does not change with the blocks
+ * of a launch (and has no limit of 2^24). */
 muon_status muon_adam_work_items(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype,
                                  int64_t* items);
 

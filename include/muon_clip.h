@@ -16,7 +16,11 @@
  * The factor is left in device memory. Instead of writing clipped gradients,
  * the optimizer steps can read it and multiply each gradient as they load it:
  * muon_plan_set_grad_scale (muon.h) and muon_adam_plan_set_grad_scale
- * (muon_adam.h).
+ * (muon_adam.h). One or the other: muon_clip_plan_step leaves the same factor
+ * as muon_clip_plan_norm, and a step that still reads it would multiply
+ * gradients clipped in place a second time. A call writes the factor when it
+ * runs, so the call for the next step has to be ordered behind the steps that
+ * read the last one (the same stream does), or write another result.
  *
  * Arithmetic: squares and sums are float64 (no finite gradient over- or
  * underflows them), in a fixed order, and so are N and the factor before

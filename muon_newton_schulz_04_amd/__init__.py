@@ -359,8 +359,8 @@ class MuonPlan:
 
     def set_grad_scale(self, scale):
         """Later steps use grad * scale, ``scale`` a one-element float32 tensor on the
-        plan's device that is read when the step runs (e.g. ``ClipPlan.scale``);
-        None detaches it."""
+        plan's device that is read when the step runs (e.g. ``ClipPlan.scale``) and may not
+        change until it has ended; None detaches it."""
         p = _scale_ptr(scale, self.device)
         _check(load_library().muon_plan_set_grad_scale(self.handle, p), "muon_plan_set_grad_scale")
         self._grad_scale = scale
@@ -742,7 +742,8 @@ class ClipPlan:
 
     def step(self, max_norm: float, eps: float = 1e-6, grad_mul: float = 1.0, norms=None, result=None,
              workspace=None, stream=None):
-        """``norm``, then every gradient times the scale into its out (in place without outs)."""
+        """``norm``, then every gradient times the scale into its out (in place without outs).
+        An optimizer plan that takes these gradients must not have the scale attached too."""
         return self._run("muon_clip_plan_step", max_norm, eps, grad_mul, norms, result, workspace, stream)
 
     def destroy(self):

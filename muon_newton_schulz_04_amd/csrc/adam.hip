@@ -39,7 +39,7 @@
 
 namespace muon_adam {
 
-constexpr int kChunk = 16384;  // elements per work item (what muon_adam_work_items counts)
+constexpr int kChunk = 16384;  // the unit of muon_adam_work_items; blocks are kBlock elements
 constexpr int kThreads = 256;
 constexpr int kVec = 4;        // consecutive elements per thread
 constexpr int kRuns = 2;       // such runs per thread, kThreads * kVec apart
