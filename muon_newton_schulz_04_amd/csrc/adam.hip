@@ -230,16 +230,16 @@ struct Interval {
   bool write;
 };
 
-// blocks: nullptr to count the work items only.
+// *blocks receives the kernel's blocks, *items what muon_adam_work_items counts.
 muon_status build(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype, std::vector<Tensor>* out,
-                  std::vector<Item>* blocks, int64_t* items) {
+                  int64_t* blocks, int64_t* items) {
   if (dtype != MUON_F32 && dtype != MUON_BF16) return MUON_E_DTYPE;
   if (n < 0 || n > MUON_ADAM_MAX_TENSORS) return MUON_E_SHAPE;
   if (n > 0 && ts == nullptr) return MUON_E_INVALID;
   const size_t es = dtype == MUON_F32 ? 4 : 2;
   std::vector<Interval> iv;
   out->assign(static_cast<size_t>(n), Tensor{});
-  *items = 0;
+  *blocks = *items = 0;
   for (int32_t i = 0; i < n; ++i) {
     const muon_adam_tensor& T = ts[i];
     if (T.numel < 0 || T.numel > MUON_ADAM_MAX_NUMEL) return MUON_E_SHAPE;
@@ -263,9 +263,7 @@ muon_status build(const muon_adam_tensor* ts, int32_t n, muon_dtype dtype, std::
     D.lr_mul = T.lr_mul;
     D.wd_mul = T.wd_mul;
     *items += (T.numel + kChunk - 1) / kChunk;
-    if (blocks != nullptr && int64_t(blocks->size()) + (T.numel + kBlock - 1) / kBlock > kMaxBlocks) return MUON_E_SHAPE;
-    if (blocks != nullptr)
-      for (int64_t r = 0; r * kBlock < T.numel; ++r) blocks->push_back({i, static_cast<int32_t>(r)});
+    *blocks += (T.numel + kBlock - 1) / kBlock;
   }
   std::sort(iv.begin(), iv.end(), [](const Interval& x, const Interval& y) { return x.lo < y.lo; });
   uintptr_t max_hi_any = 0, max_hi_w = 0;
@@ -296,8 +294,8 @@ muon_status muon_adam_work_items(const muon_adam_tensor* ts, int32_t n, muon_dty
   if (items == nullptr) return MUON_E_INVALID;
   try {
     std::vector<muon_adam::Tensor> t;
-    int64_t count = 0;
-    const muon_status st = muon_adam::build(ts, n, dtype, &t, nullptr, &count);
+    int64_t blocks = 0, count = 0;
+    const muon_status st = muon_adam::build(ts, n, dtype, &t, &blocks, &count);
     if (st == MUON_OK) *items = count;
     return st;
   } catch (...) {
@@ -310,15 +308,16 @@ muon_status muon_adam_plan_create(const muon_adam_tensor* ts, int32_t n, muon_dt
   if (plan == nullptr) return MUON_E_INVALID;
   *plan = nullptr;
   std::vector<muon_adam::Tensor> t;
-  std::vector<muon_adam::Item> it;
-  std::vector<char> h;
+  std::vector<char> h;  // the tensor table, then the blocks
+  int64_t nblocks = 0;
   size_t tb = 0, bytes = 0;
   try {
     int64_t count = 0;
-    const muon_status st = muon_adam::build(ts, n, dtype, &t, &it, &count);
+    const muon_status st = muon_adam::build(ts, n, dtype, &t, &nblocks, &count);
     if (st != MUON_OK) return st;
+    if (nblocks > muon_adam::kMaxBlocks) return MUON_E_SHAPE;
     tb = (sizeof(muon_adam::Tensor) * std::max<size_t>(1, t.size()) + 255) / 256 * 256;
-    bytes = tb + sizeof(muon_adam::Item) * std::max<size_t>(1, it.size());
+    bytes = tb + sizeof(muon_adam::Item) * static_cast<size_t>(std::max<int64_t>(1, nblocks));
     h.assign(bytes, 0);
   } catch (...) {
     return MUON_E_ALLOC;
@@ -332,9 +331,14 @@ muon_status muon_adam_plan_create(const muon_adam_tensor* ts, int32_t n, muon_dt
   if (!p) return MUON_E_ALLOC;
   p->device = dev;
   p->dtype = dtype;
-  p->nblocks = static_cast<int64_t>(it.size());
+  p->nblocks = nblocks;
   if (!t.empty()) std::memcpy(h.data(), t.data(), sizeof(muon_adam::Tensor) * t.size());
-  if (!it.empty()) std::memcpy(h.data() + tb, it.data(), sizeof(muon_adam::Item) * it.size());
+  char* at = h.data() + tb;
+  for (int32_t i = 0; i < n; ++i)
+    for (int64_t r = 0; r * muon_adam::kBlock < t[i].numel; ++r, at += sizeof(muon_adam::Item)) {
+      const muon_adam::Item it = {i, static_cast<int32_t>(r)};
+      std::memcpy(at, &it, sizeof(it));
+    }
   if (hipMalloc(&p->dmem, bytes) != hipSuccess) {
     (void)hipGetLastError();
     delete p;
