@@ -702,3 +702,35 @@ def test_column_slices_in_place(dtype, rows, d):
     qkv[2].copy_(before[2])
     assert torch.equal(buf, keep)
     plan.destroy()
+
+
+@pytest.mark.parametrize("mul", [1.0, 0.25])
+def test_steps_on_gradients_clipped_in_place(mul):
+    """float32: clipping in place and then Muon and Adam without the factor is bitwise the norm and the two
+    steps with it (one float32 product either way); with the factor still attached it is applied twice."""
+    mats, vecs = [(64, 96), (130, 70)], [(2304,), (123, 45)]
+    cfg = mu.make_config(*QUINTIC, 5, 0.95, True, 1e-7)
+    say(f"clip in place, then the steps, mul {mul}")
+
+    def run(in_place, attached):
+        gen = torch.Generator().manual_seed(41)
+        mk = lambda f: [(f * torch.randn(s, generator=gen)).to(DEV) for s in mats]  # noqa: E731
+        g, b, w = mk(0.2), mk(0.01), mk(0.02)
+        p, q, m, v = make_adam_state(vecs, torch.float32, 42, DEV)
+        clip, muon, adam = mu.ClipPlan(g + q), mu.MuonPlan(g, b, [torch.empty_like(x) for x in g]), mu.AdamPlan(p, q, m, v)
+        muon.set_weights(w)
+        for plan in (muon, adam):
+            plan.set_grad_scale(clip.scale if attached else None)
+        (clip.step if in_place else clip.norm)(0.5, grad_mul=mul)
+        muon.step_apply(cfg, 0.02, 0.1)
+        adam.step(step=2, **HP)
+        torch.cuda.synchronize()
+        assert 0.0 < clip.scale.item() < mul
+        for plan in (clip, muon, adam):
+            plan.destroy()
+        return b + w + p + m + v
+
+    want = run(False, True)
+    assert all(torch.equal(x, y) for x, y in zip(run(True, False), want))
+    twice = run(True, True)
+    assert not any(torch.equal(x, y) for x, y in zip(twice[:2], want[:2]))
