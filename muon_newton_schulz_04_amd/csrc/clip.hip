@@ -22,7 +22,7 @@
 // 39.5 M fp32, 328 MB) with every tensor's norm 53 us (6.2 TB/s); of 2.15 GB
 // 325 us (6.6 TB/s, the rate of the best plain copy kernel); norm and scaling
 // of the 328 MB into other buffers 153 us (984 MB moved, 6.4 TB/s); 1.2 GB in
-// place 194 us when not clipped, 658 us when clipped; 64 KB 3.6 and 5.6 us.
+// place 194 us when not clipped, 643 us when clipped; 64 KB 3.6 and 5.6 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
