@@ -734,3 +734,44 @@ def test_steps_on_gradients_clipped_in_place(mul):
     assert all(torch.equal(x, y) for x, y in zip(run(True, False), want))
     twice = run(True, True)
     assert not any(torch.equal(x, y) for x, y in zip(twice[:2], want[:2]))
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_chained_step_after_a_broken_gradient(bad):
+    """One infinity (norm infinite, factor zero) or NaN (factor NaN) in a set deep enough for the chained
+    launch: the step ends, without an error of the launch, as the step on gradients multiplied beforehand,
+    and so does the next one on whole gradients for the matrices that the bad one has not reached."""
+    mats = [(768, 768)] * 12 + [(768, 1024), (1024, 768)] * 2
+    cfg = mu.make_config(*QUINTIC, 5, 0.95, True, 1e-7)
+    say(f"muon chained, one {bad}")
+
+    def build():
+        gen = torch.Generator().manual_seed(51)
+        r = lambda f: [(f * torch.randn(s, generator=gen)).to(torch.bfloat16).to(DEV) for s in mats]  # noqa: E731
+        g, b = r(0.02), r(0.01)
+        return g, b, [torch.empty_like(x) for x in g]
+
+    def same(x, y):
+        return torch.equal(torch.nan_to_num(x.float(), nan=12345.0), torch.nan_to_num(y.float(), nan=12345.0))
+
+    (g, b, o), (h, c, q) = build(), build()
+    clip, plan, plain = mu.ClipPlan(g), mu.MuonPlan(g, b, o), mu.MuonPlan(h, c, q)
+    plan.set_grad_scale(clip.scale)
+    for step in range(3):
+        good = g[3][7, 11].clone()
+        if step == 1:
+            g[3][7, 11] = bad
+        n, s = clip.norm(math.inf if step != 1 else 1.0).cpu().tolist()
+        assert (s == 1.0) if step != 1 else (s == 0.0 if bad == math.inf else math.isnan(s))
+        for x, y in zip(h, g):
+            x.copy_((y.float() * s).to(y.dtype))
+        plan.step(cfg)
+        plain.step(cfg)
+        torch.cuda.synchronize()
+        assert plan.chain_state() == (1, 0) and plain.chain_state() == (1, 0)
+        assert all(same(x, y) for x, y in zip(o + b, q + c))
+        g[3][7, 11] = good
+        whole = [not torch.isnan(x.float()).any().item() for x in o]
+        assert whole == ([True] * 16 if step == 0 else [i != 3 and bad == math.inf for i in range(16)])
+    for x in (clip, plan, plain):
+        x.destroy()
