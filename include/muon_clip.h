@@ -120,6 +120,18 @@ muon_status muon_clip_plan_step(muon_clip_plan* plan, const muon_clip_config* cf
                                 muon_clip_result* result, float* norms, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* Tensor `tensor` of the plan holds rows of `cols` elements of which only the
+ * first *count take part: later calls read *count (an int32 in device
+ * memory, written before them on their stream or ordered before it) when
+ * they run, and neither read nor write the rows behind it, as if they were
+ * not there. For the row form of an embedding's gradient
+ * (muon_embed_plan_gradient_rows). count == NULL: the whole tensor again.
+ * The tensor must be contiguous (and its out with it) and whole rows, else
+ * MUON_E_SHAPE. Waits for the device, then updates the plan's table (do not
+ * call while another thread uses the plan); captured graphs follow. */
+muon_status muon_clip_plan_set_live_rows(muon_clip_plan* plan, int32_t tensor, const int32_t* count,
+                                         int64_t cols);
+
 /* Frees a plan after waiting for the device (NULL is a no-op). A captured
  * graph reads the plan's tables: it must not be replayed afterwards. */
 void muon_clip_plan_destroy(muon_clip_plan* plan);

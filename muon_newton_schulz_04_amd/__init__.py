@@ -28,7 +28,11 @@ __all__ = [
     "muon_plan_set_grad_scale", "muon_adam_plan_set_grad_scale",
     "MuonClipTensor", "MuonClipConfig", "ClipPlan", "muon_clip_plan_create",
     "muon_clip_plan_norm", "muon_clip_plan_step", "muon_clip_plan_destroy",
-    "muon_clip_workspace_bytes",
+    "muon_clip_workspace_bytes", "muon_clip_plan_set_live_rows",
+    "MuonEmbedTable", "MuonEmbedTokens", "MuonEmbedActs", "EmbeddingPlan",
+    "muon_embed_workspace_bytes", "muon_embed_plan_create", "muon_embed_plan_lookup",
+    "muon_embed_plan_gradient", "muon_embed_plan_gradient_rows", "muon_embed_plan_adam_rows",
+    "muon_embed_plan_set_grad_scale", "muon_embed_plan_destroy",
     "MUON_F32", "MUON_BF16", "MUON_PRECISION_DEFAULT",
 ]
 
@@ -89,6 +93,22 @@ class MuonClipConfig(ctypes.Structure):
     _fields_ = [("max_norm", ctypes.c_float), ("eps", ctypes.c_float), ("grad_mul", ctypes.c_float)]
 
 
+class MuonEmbedTable(ctypes.Structure):
+    _fields_ = [("vocab", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("lr_mul", ctypes.c_float), ("wd_mul", ctypes.c_float)]
+
+
+class MuonEmbedTokens(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("wide", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class MuonEmbedActs(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 class MuonBufferInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("m", "n", "mp", "np", "x_lo", "x_op0", "x_op1", "gram", "poly", "x0_scale")]
@@ -138,6 +158,17 @@ def load_library(path: str = LIB_PATH):
         "muon_clip_plan_norm": (i32, [vp, P(MuonClipConfig), vp, vp, vp, sz, vp]),
         "muon_clip_plan_step": (i32, [vp, P(MuonClipConfig), vp, vp, vp, sz, vp]),
         "muon_clip_plan_destroy": (None, [vp]),
+        "muon_clip_plan_set_live_rows": (i32, [vp, i32, vp, i64]),
+        "muon_embed_workspace_bytes": (i32, [i64, i64, i64, P(sz)]),
+        "muon_embed_plan_create": (i32, [P(MuonEmbedTable), i32, i64, P(vp)]),
+        "muon_embed_plan_lookup": (i32, [vp, P(MuonEmbedTokens), ctypes.c_float, P(MuonEmbedActs), vp]),
+        "muon_embed_plan_gradient": (i32, [vp, P(MuonEmbedTokens), P(MuonEmbedActs), ctypes.c_float, vp, i64, i32,
+                                           vp, sz, vp]),
+        "muon_embed_plan_gradient_rows": (i32, [vp, P(MuonEmbedTokens), P(MuonEmbedActs), ctypes.c_float, vp, vp, vp,
+                                                vp, sz, vp]),
+        "muon_embed_plan_adam_rows": (i32, [vp, P(MuonAdamConfig), vp, vp, vp, i64, vp]),
+        "muon_embed_plan_set_grad_scale": (i32, [vp, vp]),
+        "muon_embed_plan_destroy": (None, [vp]),
         "muon_adam_work_items": (i32, [P(MuonAdamTensor), i32, i32, P(i64)]),
     }
     for name, (res, args) in sig.items():
@@ -746,6 +777,21 @@ class ClipPlan:
         An optimizer plan that takes these gradients must not have the scale attached too."""
         return self._run("muon_clip_plan_step", max_norm, eps, grad_mul, norms, result, workspace, stream)
 
+    def set_live_rows(self, index: int, count, cols: Optional[int] = None):
+        """Tensor ``index`` holds rows of ``cols`` elements (its last dimension unless given), of
+        which later calls take the first ``count``, a one-element int32 tensor on the plan's device
+        that is read when they run; the rows behind it are neither read nor written. None: all rows."""
+        import torch
+        g = self._keep[0][index]
+        if count is not None and (count.dtype != torch.int32 or count.numel() != 1 or count.device != self.device):
+            raise ValueError("the number of live rows is one int32 element on the plan's device")
+        cols = (g.shape[-1] if g.dim() else 1) if cols is None else int(cols)
+        index = index % self.n
+        with torch.cuda.device(self.device):
+            _check(load_library().muon_clip_plan_set_live_rows(self.handle, index, _ptr(count), cols),
+                   "muon_clip_plan_set_live_rows")
+        self._live = {**getattr(self, "_live", {}), index: count}
+
     def destroy(self):
         if self.handle:
             load_library().muon_clip_plan_destroy(self.handle)
@@ -773,4 +819,198 @@ def muon_clip_plan_step(plan: ClipPlan, max_norm, eps=1e-6, grad_mul=1.0, norms=
 
 
 def muon_clip_plan_destroy(plan: ClipPlan):
+    plan.destroy()
+
+
+def muon_clip_plan_set_live_rows(plan: ClipPlan, index: int, count, cols: Optional[int] = None):
+    plan.set_live_rows(index, count, cols)
+
+
+# ------------------------------------------------------------ embedding table
+
+def muon_embed_workspace_bytes(vocab: int, cols: int, max_tokens: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().muon_embed_workspace_bytes(vocab, cols, max_tokens, ctypes.byref(out)),
+           "muon_embed_workspace_bytes")
+    return out.value
+
+
+class EmbeddingPlan:
+    """One embedding table (vocab x cols, bf16 or float32, rows at any stride) and its
+    float32 moments, for batches of at most ``max_tokens`` tokens.
+
+    Tokens are int32 or int64 tensors of any contiguous shape; one outside [0, vocab) looks
+    up zeros and carries no gradient. Activations (``out``, ``dout``) have the tokens' shape
+    and ``cols`` behind it, in bf16 or float32 whatever the table's type, and rows at one
+    stride. A gradient needs a ``workspace``, allocated per call unless one is given; calls
+    that overlap in time need one each. Nothing waits for the device."""
+
+    def __init__(self, table, max_tokens: int, exp_avg=None, exp_avg_sq=None, lr_mul: float = 1.0,
+                 wd_mul: float = 1.0):
+        import torch
+        lib = load_library()
+        self.handle = ctypes.c_void_p(None)
+        if not table.is_cuda:
+            raise ValueError("the table must be in device memory")
+        self.dtype, self.device = _dtype_code(table), table.device
+        ld = _ld(table)
+        for t in (exp_avg, exp_avg_sq):
+            if t is None:
+                continue
+            if t.dtype != torch.float32:
+                raise TypeError("Adam moments are float32")
+            if t.shape != table.shape or not t.is_contiguous() or t.device != self.device:
+                raise ValueError("moments must be contiguous, of the table's shape and on its device")
+        self.vocab, self.cols = table.shape
+        self.max_tokens = int(max_tokens)
+        self._keep = (table, exp_avg, exp_avg_sq)
+        self.workspace_bytes = muon_embed_workspace_bytes(self.vocab, self.cols, self.max_tokens)
+        t = MuonEmbedTable(self.vocab, self.cols, max(ld, self.cols), _ptr(table), _ptr(exp_avg), _ptr(exp_avg_sq),
+                           float(lr_mul), float(wd_mul))
+        h = ctypes.c_void_p(None)
+        with torch.cuda.device(self.device):
+            _check(lib.muon_embed_plan_create(ctypes.byref(t), self.dtype, self.max_tokens, ctypes.byref(h)),
+                   "muon_embed_plan_create")
+        self.handle = h
+
+    def _tokens(self, tokens):
+        import torch
+        if tokens.dtype not in (torch.int32, torch.int64):
+            raise TypeError("tokens are int32 or int64")
+        if tokens.device != self.device or not tokens.is_contiguous():
+            raise ValueError(f"tokens must be contiguous and on {self.device}")
+        return MuonEmbedTokens(tokens.data_ptr(), tokens.numel(), 1 if tokens.dtype == torch.int64 else 0, 0)
+
+    def _acts(self, x, tokens):
+        dt = _dtype_code(x)
+        if x.device != self.device or x.shape != (*tokens.shape, self.cols):
+            raise ValueError(f"activations have the tokens' shape and {self.cols} columns, on {self.device}")
+        if x.is_contiguous():
+            ld = self.cols
+        else:
+            y = x.flatten(0, -2) if x.dim() > 2 else x
+            if y.dim() != 2 or y.data_ptr() != x.data_ptr():
+                raise ValueError("activations must be rows of consecutive elements at one row stride")
+            ld = max(_ld(y), self.cols)
+        return MuonEmbedActs(x.data_ptr(), ld, dt, 0)
+
+    def _rows(self, rows, values, count, need):
+        import torch
+        for t, dt in ((rows, torch.int32), (count, torch.int32)):
+            if t.dtype != dt or not t.is_contiguous() or t.device != self.device:
+                raise ValueError(f"rows and count are contiguous int32 tensors on {self.device}")
+        if _dtype_code(values) != self.dtype or not values.is_contiguous() or values.device != self.device:
+            raise ValueError(f"values must be contiguous, of the table's type and on {self.device}")
+        if values.dim() != 2 or values.shape[1] != self.cols or rows.shape != values.shape[:1] or count.numel() != 1:
+            raise ValueError("rows, values and count have shapes (r,), (r, cols) and one element")
+        if rows.numel() < need:
+            raise ValueError(f"rows and values need room for {need} rows")
+
+    def _call(self, entry, *args, stream=None):
+        import torch
+        index = self.device.index
+        handle = _current_stream(index) if stream is None else _stream_handle(stream)
+        fn = getattr(load_library(), entry)
+        if torch.cuda.current_device() == index:
+            _check(fn(self.handle, *args, handle), entry)
+        else:
+            with torch.cuda.device(index):
+                _check(fn(self.handle, *args, handle), entry)
+
+    def _ws(self, workspace, stream):
+        import torch
+        if workspace is None:
+            if stream is None:
+                return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+            # allocated and, once dropped, reused in the order of the stream that uses it
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), self.device)
+            with torch.cuda.stream(s):
+                return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+        if workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {self.device}")
+        return workspace
+
+    def lookup(self, tokens, out, scale: float = 1.0, stream=None):
+        """out[i] = scale * table[tokens[i]]; returns ``out``."""
+        t, o = self._tokens(tokens), self._acts(out, tokens)
+        self._call("muon_embed_plan_lookup", ctypes.byref(t), float(scale), ctypes.byref(o), stream=stream)
+        return out
+
+    def gradient(self, tokens, dout, grad, scale: float = 1.0, accumulate: bool = False, workspace=None, stream=None):
+        """The lookup's gradient into ``grad`` (the table's shape and type): every row is written,
+        or with ``accumulate`` the rows that have tokens are added to. Returns ``grad``."""
+        t, d = self._tokens(tokens), self._acts(dout, tokens)
+        if _dtype_code(grad) != self.dtype or grad.shape != self._keep[0].shape or grad.device != self.device:
+            raise ValueError("grad must match the table's shape, type and device")
+        ws = self._ws(workspace, stream)
+        self._call("muon_embed_plan_gradient", ctypes.byref(t), ctypes.byref(d), float(scale), grad.data_ptr(),
+                   max(_ld(grad), self.cols), 1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(),
+                   stream=stream)
+        return grad
+
+    def gradient_rows(self, tokens, dout, rows, values, count, scale: float = 1.0, workspace=None, stream=None):
+        """The gradient as rows: the distinct tokens ascending into ``rows`` (int32), their sums into
+        ``values`` (the table's type) and their number into ``count`` (one int32). ``rows`` and
+        ``values`` have room for min(number of tokens, vocab) rows; those behind ``count`` stay as they are."""
+        t, d = self._tokens(tokens), self._acts(dout, tokens)
+        self._rows(rows, values, count, min(tokens.numel(), self.vocab))
+        ws = self._ws(workspace, stream)
+        self._call("muon_embed_plan_gradient_rows", ctypes.byref(t), ctypes.byref(d), float(scale), rows.data_ptr(),
+                   values.data_ptr(), count.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), stream=stream)
+        return rows, values, count
+
+    def set_grad_scale(self, scale):
+        """Later ``adam_rows`` use values * scale (see ``MuonPlan.set_grad_scale``)."""
+        p = _scale_ptr(scale, self.device)
+        _check(load_library().muon_embed_plan_set_grad_scale(self.handle, p), "muon_embed_plan_set_grad_scale")
+        self._grad_scale = scale
+
+    def adam_rows(self, rows, values, count, lr: float, beta1: float, beta2: float, eps: float, wd: float, step: int,
+                  stream=None):
+        """The Adam step (``AdamPlan.step``) of the table's rows ``rows[:count]`` with gradients
+        ``values[:count]``; the other rows and their moments stay as they are."""
+        self._rows(rows, values, count, 0)
+        cfg = MuonAdamConfig(float(lr), float(beta1), float(beta2), float(eps), float(wd), int(step))
+        self._call("muon_embed_plan_adam_rows", ctypes.byref(cfg), rows.data_ptr(), values.data_ptr(),
+                   count.data_ptr(), min(rows.numel(), self.vocab), stream=stream)
+
+    def destroy(self):
+        if self.handle:
+            load_library().muon_embed_plan_destroy(self.handle)
+            self.handle = ctypes.c_void_p(None)
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def muon_embed_plan_create(table, max_tokens, exp_avg=None, exp_avg_sq=None, lr_mul=1.0, wd_mul=1.0) -> EmbeddingPlan:
+    return EmbeddingPlan(table, max_tokens, exp_avg, exp_avg_sq, lr_mul, wd_mul)
+
+
+def muon_embed_plan_lookup(plan: EmbeddingPlan, tokens, out, scale=1.0, stream=None):
+    return plan.lookup(tokens, out, scale, stream)
+
+
+def muon_embed_plan_gradient(plan: EmbeddingPlan, tokens, dout, grad, scale=1.0, accumulate=False, workspace=None,
+                             stream=None):
+    return plan.gradient(tokens, dout, grad, scale, accumulate, workspace, stream)
+
+
+def muon_embed_plan_gradient_rows(plan: EmbeddingPlan, tokens, dout, rows, values, count, scale=1.0, workspace=None,
+                                  stream=None):
+    return plan.gradient_rows(tokens, dout, rows, values, count, scale, workspace, stream)
+
+
+def muon_embed_plan_adam_rows(plan: EmbeddingPlan, rows, values, count, lr, beta1, beta2, eps, wd, step, stream=None):
+    plan.adam_rows(rows, values, count, lr, beta1, beta2, eps, wd, step, stream)
+
+
+def muon_embed_plan_set_grad_scale(plan: EmbeddingPlan, scale):
+    plan.set_grad_scale(scale)
+
+
+def muon_embed_plan_destroy(plan: EmbeddingPlan):
     plan.destroy()

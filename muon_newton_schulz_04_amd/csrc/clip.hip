@@ -61,7 +61,20 @@ struct Item {
   int32_t n, rows;
   int32_t dtype;       // muon_dtype
   uint32_t magic;      // rows > 1: (2^32 - 1) / vectors in a row, see div_row
+  // muon_clip_plan_set_live_rows: elements of the tensor at or behind *live * width do not count
+  const int32_t* live; // nullptr: all count
+  int64_t pos;         // first element of the item in its tensor
+  int64_t width;
 };
+
+__device__ __forceinline__ Item live_item(const Item& item) {
+  Item it = item;
+  if (it.live != nullptr) {
+    const int64_t left = int64_t(*it.live) * it.width - it.pos;
+    it.n = static_cast<int32_t>(left < 0 ? 0 : left < it.n ? left : it.n);
+  }
+  return it;
+}
 
 struct Range {
   int32_t beg, end;  // work items of a tensor
@@ -292,7 +305,7 @@ __global__ __launch_bounds__(kThreads, 8) void clip_norm_kernel(Args A) {
   const int i = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
   double s = 0.0;
   if (i < A.n_items) {
-    const Item it = A.items[i];
+    const Item it = live_item(A.items[i]);
     s = wave_sum(i < A.n_stream ? ssq_any<true>(it, lane) : ssq_any<false>(it, lane));
     if (A.isum != nullptr && lane == 0) A.isum[i] = s;
   }
@@ -442,7 +455,7 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(Args A, int item_b
   const int i = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
   const muon_clip_result r = result_of(sum_partials(A.part, A.n_part, red), A);
   if (blockIdx.x == 0 && threadIdx.x == 0) *A.res = r;
-  if (i < A.n_items) scale_any(A.items[i], r.scale, lane);
+  if (i < A.n_items) scale_any(live_item(A.items[i]), r.scale, lane);
 }
 
 // Short lists, where launches are most of the time: one block does the whole
@@ -453,7 +466,7 @@ __global__ __launch_bounds__(64 * kSmall) void clip_small_kernel(Args A, int sca
   __shared__ double isum[kSmall];
   const int lane = threadIdx.x & 63, i = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (i < A.n_items) {
-    const double s = wave_sum(ssq_any<false>(A.items[i], lane));
+    const double s = wave_sum(ssq_any<false>(live_item(A.items[i]), lane));
     if (lane == 0) isum[i] = s;
   }
   __syncthreads();
@@ -466,7 +479,7 @@ __global__ __launch_bounds__(64 * kSmall) void clip_small_kernel(Args A, int sca
       for (int k = q.beg; k < q.end; ++k) s += isum[k];
       A.norms[t] = tensor_norm(s, A);
     }
-  if (scale && i < A.n_items) scale_any(A.items[i], r.scale, lane);
+  if (scale && i < A.n_items) scale_any(live_item(A.items[i]), r.scale, lane);
 }
 
 // ------------------------------------------------------------------ host
@@ -602,13 +615,13 @@ muon_status build(const muon_clip_tensor* ts, int32_t n, Host* H) {
         for (int64_t r = 0; r < rows; ++r)
           for (int64_t c = 0; c < cols; c += chunk)
             H->items.push_back({g + (r * T.ld + c) * es, o ? o + (r * T.out_ld + c) * es : nullptr, 0, 0,
-                                static_cast<int32_t>(std::min(chunk, cols - c)), 1, T.dtype, 0});
+                                static_cast<int32_t>(std::min(chunk, cols - c)), 1, T.dtype, 0, nullptr, 0, 0});
       } else {              // whole rows, at most about one item's bytes
         const int64_t each = std::max<int64_t>(1, chunk / cols), vpr = cols * es / 16;
         const uint32_t magic = static_cast<uint32_t>(UINT32_MAX / std::max<int64_t>(1, vpr));
         for (int64_t r = 0; r < rows; r += each)
           H->items.push_back({g + r * T.ld * es, o ? o + r * T.out_ld * es : nullptr, T.ld, T.out_ld,
-                              static_cast<int32_t>(cols), static_cast<int32_t>(std::min(each, rows - r)), T.dtype, magic});
+                              static_cast<int32_t>(cols), static_cast<int32_t>(std::min(each, rows - r)), T.dtype, magic, nullptr, 0, 0});
       }
     }
     R.end = static_cast<int32_t>(H->items.size());
@@ -769,6 +782,41 @@ muon_status muon_clip_plan_norm(muon_clip_plan* plan, const muon_clip_config* cf
 muon_status muon_clip_plan_step(muon_clip_plan* plan, const muon_clip_config* cfg, muon_clip_result* result,
                                 float* norms, void* workspace, size_t workspace_bytes, void* stream) {
   return enqueue(plan, cfg, result, norms, workspace, workspace_bytes, stream, true);
+}
+
+muon_status muon_clip_plan_set_live_rows(muon_clip_plan* plan, int32_t tensor, const int32_t* count, int64_t cols) {
+  using namespace muon_clip;
+  if (plan == nullptr || tensor < 0 || tensor >= plan->n_tensors) return MUON_E_INVALID;
+  if (count != nullptr && (cols < 1 || cols > MUON_CLIP_MAX_NUMEL)) return MUON_E_SHAPE;
+  if (reinterpret_cast<uintptr_t>(count) % 4 != 0) return MUON_E_ALIGN;
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess || dev != plan->device) return MUON_E_DEVICE;
+  if (hipDeviceSynchronize() != hipSuccess) return MUON_E_DEVICE;
+  try {
+    Range r{};
+    if (hipMemcpy(&r, plan->d_ranges + tensor, sizeof(r), hipMemcpyDeviceToHost) != hipSuccess) return MUON_E_DEVICE;
+    std::vector<Item> items(static_cast<size_t>(r.end - r.beg));
+    if (items.empty()) return MUON_OK;  // an empty tensor
+    const size_t bytes = sizeof(Item) * items.size();
+    if (hipMemcpy(items.data(), plan->d_items + r.beg, bytes, hipMemcpyDeviceToHost) != hipSuccess) return MUON_E_DEVICE;
+    int64_t pos = 0;
+    for (size_t i = 0; i < items.size(); ++i) {
+      Item& it = items[i];
+      const int64_t es = size_of(it.dtype);
+      if (it.rows != 1 || it.g != items[0].g + pos * es || (it.o != nullptr && it.o != items[0].o + pos * es))
+        return MUON_E_SHAPE;  // strided
+      it.live = count;
+      it.pos = pos;
+      it.width = cols;
+      pos += it.n;
+    }
+    if (count != nullptr && pos % cols != 0) return MUON_E_SHAPE;
+    if (hipMemcpy(const_cast<Item*>(plan->d_items) + r.beg, items.data(), bytes, hipMemcpyHostToDevice) != hipSuccess)
+      return MUON_E_DEVICE;
+    return MUON_OK;
+  } catch (...) {
+    return MUON_E_ALLOC;
+  }
 }
 
 void muon_clip_plan_destroy(muon_clip_plan* plan) {

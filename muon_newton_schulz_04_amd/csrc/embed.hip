@@ -1,0 +1,962 @@
+// Embedding table on the Adam path (include/muon_embed.h): lookup, gradient by
+// sorted tokens, and the Adam step of the rows a batch has touched.
+//
+//   out_i = s E[t_i];   G[v] = s sum_{i: t_i = v} dout_i
+//
+// All of it is bound by HBM, or by the launches for small batches. The
+// gradient takes three launches:
+//  - sort: block b owns R consecutive vocabulary entries. It reads all n tokens
+//    twice, counts its own and those below its range (which gives the place of
+//    its first token without any other block's word), and writes its tokens'
+//    records ordered by token, then by position. No atomics across blocks, no
+//    dependence on how tokens are spread, any n.
+//  - sum: the sorted records are cut into chunks of equal length, whatever
+//    tokens they hold. A wave takes the columns of a slab through one chunk and
+//    writes the sum of each token that lies within it; a token that crosses a
+//    chunk's border leaves float32 partial sums, one per chunk.
+//  - join: adds a crossing token's partial sums in order.
+// Equal inputs give equal bits: no sum depends on which wave comes first.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+
+#include "../../include/muon_embed.h"
+#include "adam_elem.hpp"
+
+namespace muon_embed {
+
+using muon_adam::kVec;
+
+constexpr int kThreads = 256;
+constexpr int kLookVec = 8;        // consecutive elements per thread of the lookup
+constexpr int kLookRuns = 4;       // such vectors per thread, kThreads apart
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kMaxRange = 2048;    // vocabulary entries of a sort block: 16 waves' counters fill 128 KB of LDS
+constexpr int kSortBlocks = 256;   // sort blocks while the range allows: one per CU
+constexpr int kSlab = 64 * kVec;   // columns of a wave in the sum
+constexpr int64_t kSumWaves = 4096;  // waves of the sum aimed at: 16 on each CU
+constexpr int64_t kMaxWaves = 1 << 23;  // of one launch (the join has a block for each)
+
+// A sorted token.
+struct Rec {
+  int32_t pos;   // its position in the batch
+  int32_t key;   // the token
+  int32_t slot;  // the token's rank among the distinct tokens of its sort block
+  int32_t end;   // index behind the token's last record
+};
+
+// Vectors at an element's alignment (the hardware takes any address).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // round to nearest even
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
+}
+
+// Eight consecutive elements, the first `n` of them if fewer are left.
+__device__ __forceinline__ void load8(const uint16_t* p, int n, float (&x)[8]) {
+  if (n >= 8) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      x[2 * q] = __uint_as_float(w[q] << 16);
+      x[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = q < n ? muon_adam::bf2f(p[q]) : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const float* p, int n, float (&x)[8]) {
+  if (n >= 8) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      x[q] = a[q];
+      x[q + 4] = b[q];
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = q < n ? p[q] : 0.f;
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, int n, const float (&x)[8]) {
+  if (n >= 8) {
+    const u32x4 w = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+    *reinterpret_cast<u32x4*>(p) = w;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) p[q] = static_cast<uint16_t>(pack_bf16(x[q], 0.f));
+  }
+}
+__device__ __forceinline__ void store8(float* p, int n, const float (&x)[8]) {
+  if (n >= 8) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) p[q] = x[q];
+  }
+}
+// The same for four.
+template <typename T>
+__device__ __forceinline__ void load4_of(const T* p, int n, float (&x)[kVec]) {
+  if (n >= kVec) {
+    muon_adam::load4<false>(p, x);
+  } else {
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) x[q] = q < n ? muon_adam::PElem<T>::load(p, q) : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store4_of(T* p, int n, const float (&x)[kVec]) {
+  if (n >= kVec) {
+    muon_adam::store4<false>(p, x);
+  } else {
+#pragma unroll
+    for (int q = 0; q < kVec; ++q)
+      if (q < n) muon_adam::PElem<T>::store(p, q, x[q]);
+  }
+}
+
+// The token at i, or -1 where it is outside the vocabulary.
+template <typename I>
+__device__ __forceinline__ int32_t token(const I* tokens, int64_t i, int32_t vocab) {
+  const I t = tokens[i];
+  return t >= 0 && t < static_cast<I>(vocab) ? static_cast<int32_t>(t) : -1;
+}
+
+// k / d for magic = (2^32 - 1) / d: 2^32 - magic d lies in [1, d], so the
+// product's high word is the quotient or one less.
+__device__ __forceinline__ uint32_t div_by(uint32_t k, uint32_t d, uint32_t magic) {
+  const uint32_t q = __umulhi(k, magic);
+  return k - q * d >= d ? q + 1 : q;
+}
+
+// ----------------------------------------------------------------- lookup
+
+struct LookArgs {
+  const void* table;
+  const void* tokens;
+  void* out;
+  int64_t ld, out_ld;
+  int64_t n;
+  int32_t vocab, cols;
+  int32_t vpr;      // vectors in a row
+  int32_t per;      // tokens of a block
+  uint32_t magic;   // for divisions by vpr
+  float scale;
+};
+
+template <typename E, typename O, typename I>
+__global__ __launch_bounds__(kThreads) void embed_lookup_kernel(LookArgs A) {
+  const int64_t first = int64_t(blockIdx.x) * A.per;
+  const int64_t left = A.n - first;
+  const uint32_t vpr = static_cast<uint32_t>(A.vpr);
+  const uint32_t nv = vpr * static_cast<uint32_t>(left < A.per ? left : A.per);
+  const E* table = static_cast<const E*>(A.table);
+  O* out = static_cast<O*>(A.out);
+  for (uint32_t k0 = threadIdx.x; k0 < nv; k0 += kThreads * kLookRuns) {
+    float x[kLookRuns][8];
+#pragma unroll
+    for (int j = 0; j < kLookRuns; ++j) {
+      const uint32_t k = k0 + j * kThreads;
+      if (k >= nv) break;
+      const uint32_t r = div_by(k, vpr, A.magic);
+      const int c = static_cast<int>(k - r * vpr) * kLookVec;
+      const int32_t t = token(static_cast<const I*>(A.tokens), first + r, A.vocab);
+      if (t >= 0) {
+        load8(table + int64_t(t) * A.ld + c, A.cols - c, x[j]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[j][q] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kLookRuns; ++j) {
+      const uint32_t k = k0 + j * kThreads;
+      if (k >= nv) break;
+      const uint32_t r = div_by(k, vpr, A.magic);
+      const int c = static_cast<int>(k - r * vpr) * kLookVec;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[j][q] *= A.scale;
+      store8(out + (first + r) * A.out_ld + c, A.cols - c, x[j]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- sort
+
+struct SortArgs {
+  const void* tokens;
+  Rec* recs;
+  int32_t* distinct;  // per block: distinct tokens of its range
+  int32_t* live;      // tokens inside the vocabulary
+  void* grad;         // dense form: rows without a token are cleared here (nullptr: not)
+  int64_t grad_ld;
+  int32_t n, vocab, cols, range;
+  int32_t grad_f32;
+};
+
+__device__ __forceinline__ int lanes_below(uint64_t mask, int lane) {
+  return __popcll(mask & ((uint64_t(1) << lane) - 1));
+}
+
+template <typename I>
+__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(SortArgs A) {
+  extern __shared__ int32_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lo = blockIdx.x * A.range;
+  const int nk = min(A.range, A.vocab - lo);
+  int32_t* const cnt = lds;                       // [wave][key]: the wave's tokens, then where its next one goes
+  int32_t* const end = lds + kSortWaves * nk;     // [key]
+  int32_t* const slot = end + nk;                 // [key]
+  __shared__ int32_t below[kSortWaves];
+  __shared__ int64_t scan[kSortWaves];
+  for (int i = tid; i < kSortWaves * nk; i += kSortThreads) cnt[i] = 0;
+  __syncthreads();
+
+  // A wave's tokens are one run of the batch, so that (wave, lane, time) order is position order.
+  const I* const tokens = static_cast<const I*>(A.tokens);
+  const int each = (A.n + kSortThreads - 1) / kSortThreads * 64;
+  const int beg = min(A.n, wave * each), fin = min(A.n, beg + each);
+  volatile int32_t* const mine = cnt + wave * nk;  // read by lanes other than the one that wrote it
+  constexpr int U = 8;  // loads in flight
+  int under = 0;
+  for (int i0 = beg; i0 < fin; i0 += 64 * U) {
+    int32_t t[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * 64 + lane;
+      t[u] = i < fin ? token(tokens, i, A.vocab) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      under += __popcll(__ballot(t[u] >= 0 && t[u] < lo));
+      const int k = t[u] - lo;
+      if (k >= 0 && k < nk) atomicAdd(cnt + wave * nk + k, 1);
+    }
+  }
+  if (lane == 0) below[wave] = under;
+  __syncthreads();
+
+  // Starts of the tokens: a scan over the keys of (count, is there any) in one 64-bit sum.
+  int64_t carry = 0;
+  for (int w = 0; w < kSortWaves; ++w) carry += below[w];
+  const int first = static_cast<int>(carry);
+  for (int k0 = 0; k0 < nk; k0 += kSortThreads) {
+    const int k = k0 + tid;
+    int total = 0;
+    if (k < nk)
+      for (int w = 0; w < kSortWaves; ++w) total += cnt[w * nk + k];
+    const int64_t own = int64_t(total) + (total > 0 ? int64_t(1) << 32 : 0);
+    int64_t x = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t y = __shfl_up(x, o, 64);
+      if (lane >= o) x += y;
+    }
+    if (lane == 63) scan[wave] = x;
+    __syncthreads();
+    int64_t base = carry;
+    for (int w = 0; w < kSortWaves; ++w) {
+      if (w < wave) base += scan[w];
+      carry += scan[w];
+    }
+    if (k < nk) {
+      const int64_t at = base + x - own;
+      int start = static_cast<int>(at);
+      end[k] = start + total;
+      slot[k] = static_cast<int>(at >> 32);
+      for (int w = 0; w < kSortWaves; ++w) {
+        const int c = cnt[w * nk + k];
+        cnt[w * nk + k] = start;
+        start += c;
+      }
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    A.distinct[blockIdx.x] = static_cast<int>(carry >> 32);
+    if (blockIdx.x == gridDim.x - 1) *A.live = static_cast<int>(carry);
+  }
+
+  if (static_cast<int>(carry) > first) {
+    for (int i0 = beg; i0 < fin; i0 += 64 * U) {
+      int32_t t[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * 64 + lane;
+        t[u] = i < fin ? token(tokens, i, A.vocab) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = t[u] - lo;
+        const bool in = k >= 0 && k < nk;
+        uint64_t todo = __ballot(in);
+        while (todo) {  // one of the wave's tokens at a time, its lanes in order
+          const int lead = __builtin_ctzll(todo);
+          const int key = __builtin_amdgcn_readlane(k, lead);
+          const uint64_t same = __ballot(in && k == key);
+          if (in && k == key) {
+            const int at = mine[key];
+            A.recs[at + lanes_below(same, lane)] = {i0 + u * 64 + lane, key + lo, slot[key], end[key]};
+            if (lane == lead) mine[key] = at + __popcll(same);
+          }
+          todo &= ~same;
+        }
+      }
+    }
+  }
+
+  if (A.grad == nullptr) return;
+  // Rows without a token, a wave each (all of a token's records end behind
+  // its first one, so an empty token's end is where the next one starts).
+  for (int k = wave; k < nk; k += kSortWaves) {
+    const int before = k > 0 ? end[k - 1] : first;
+    if (end[k] != before) continue;
+    const float zero[8] = {};
+    if (A.grad_f32) {
+      float* const row = static_cast<float*>(A.grad) + int64_t(lo + k) * A.grad_ld;
+      for (int c = lane * 8; c < A.cols; c += 512) store8(row + c, A.cols - c, zero);
+    } else {
+      uint16_t* const row = static_cast<uint16_t*>(A.grad) + int64_t(lo + k) * A.grad_ld;
+      for (int c = lane * 8; c < A.cols; c += 512) store8(row + c, A.cols - c, zero);
+    }
+  }
+}
+
+// -------------------------------------------------------------------- sum
+
+enum Mode { kDense = 0, kAdd = 1, kRows = 2 };
+
+struct SumArgs {
+  const Rec* recs;
+  const int32_t* distinct;
+  const int32_t* live;
+  const void* dout;
+  int64_t dout_ld;
+  void* grad;       // dense and add: the table's gradient; rows: the values
+  int64_t grad_ld;
+  int32_t* rows;    // rows: the tokens
+  int32_t* count;   // rows: how many
+  float* head;      // [chunk][ld_part]: the part of a token that began in an earlier chunk
+  float* tail;      // [chunk][ld_part]: the first part of a token that goes on in the next chunk
+  int64_t ld_part;
+  int32_t cols, slabs, chunks, chunk, range, blocks;
+  float scale;
+};
+
+// Where a wave is: its chunk's records and its columns.
+struct Place {
+  int c0, len;   // first record, number of records
+  int col, nc;   // the lane's first column and how many of its four exist
+};
+
+__device__ __forceinline__ int wave_sum(int x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+  return x;
+}
+
+// Distinct tokens in sort blocks [b0, b1): the same for every lane.
+__device__ __forceinline__ int distinct_in(const int32_t* distinct, int b0, int b1, int lane) {
+  int s = 0;
+  for (int b = b0 + lane; b < b1; b += 64) s += distinct[b];
+  return __builtin_amdgcn_readfirstlane(wave_sum(s));
+}
+
+// A finished sum goes out. row: the token, or its place among the rows.
+template <typename G, int MODE>
+__device__ __forceinline__ void put(const SumArgs& A, int64_t row, int col, int nc, float (&x)[kVec]) {
+  if (nc <= 0) return;
+  G* const p = static_cast<G*>(A.grad) + row * A.grad_ld + col;
+  if constexpr (MODE == kAdd) {
+    float old[kVec];
+    load4_of(p, nc, old);
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) x[q] = old[q] + x[q] * A.scale;
+  } else {
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) x[q] *= A.scale;
+  }
+  store4_of(p, nc, x);
+}
+
+template <typename D, typename G, int MODE>
+__global__ __launch_bounds__(kThreads) void embed_sum_kernel(SumArgs A) {
+  const int lane = threadIdx.x & 63;
+  const int64_t id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + int64_t(blockIdx.x) * (kThreads / 64);
+  if (MODE == kRows && id == 0) {
+    const int total = distinct_in(A.distinct, 0, A.blocks, lane);
+    if (lane == 0) *A.count = total;
+  }
+  const int64_t chunk = id / A.slabs;
+  const int slab = static_cast<int>(id - chunk * A.slabs);
+  const int live = __builtin_amdgcn_readfirstlane(*A.live);
+  const int64_t c0 = chunk * A.chunk;
+  if (c0 >= live) return;
+  const int len = static_cast<int>(min(int64_t(A.chunk), live - c0));
+  const int c1 = static_cast<int>(c0) + len;
+  const int col = slab * kSlab + lane * kVec, nc = A.cols - col;
+  const Rec mine = lane < len ? A.recs[c0 + lane] : Rec{0, -1, 0, 0};  // a chunk has at most 64 records
+  const int prev = c0 > 0 ? __builtin_amdgcn_readfirstlane(A.recs[c0 - 1].key) : -1;
+  int key = __builtin_amdgcn_readfirstlane(mine.key);
+  int block = key / A.range, base = 0;
+  if (MODE == kRows) base = distinct_in(A.distinct, 0, block, lane);
+  float acc[kVec] = {};
+  int last = 0;  // the lane that holds a record of the current token
+
+  auto flush = [&]() {
+    const int end = __builtin_amdgcn_readlane(mine.end, last);
+    float* part = nullptr;
+    if (key == prev && __builtin_amdgcn_readfirstlane(mine.key) == key) part = A.head;
+    else if (end > c1) part = A.tail;
+    int64_t row = key;
+    if (MODE == kRows) {
+      const int b = key / A.range;
+      if (b != block) {
+        base += distinct_in(A.distinct, block, b, lane);
+        block = b;
+      }
+      row = base + __builtin_amdgcn_readlane(mine.slot, last);
+    }
+    if (part != nullptr) {
+      if (nc > 0) *reinterpret_cast<float4*>(part + chunk * A.ld_part + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    } else {
+      put<G, MODE>(A, row, col, nc, acc);
+      if (MODE == kRows && slab == 0 && lane == 0) A.rows[row] = key;
+    }
+  };
+
+  const D* const dout = static_cast<const D*>(A.dout) + col;
+  constexpr int U = 8;  // rows in flight
+  for (int i0 = 0; i0 < len; i0 += U) {
+    float x[U][kVec];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u < len && nc > 0) {
+        const int64_t pos = __builtin_amdgcn_readlane(mine.pos, i0 + u);
+        load4_of(dout + pos * A.dout_ld, nc, x[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= len) break;
+      const int k = __builtin_amdgcn_readlane(mine.key, i0 + u);
+      if (k != key) {
+        flush();
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) acc[q] = 0.f;
+        key = k;
+        last = i0 + u;
+      }
+#pragma unroll
+      for (int q = 0; q < kVec; ++q) acc[q] += x[u][q];
+    }
+  }
+  flush();
+}
+
+// A token that crosses chunks: its first part, then one part of every later
+// chunk it reaches. Block (chunk, slab); the waves take the later parts in
+// turn, and their sums are added in order.
+template <typename G, int MODE>
+__global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs A) {
+  __shared__ float4 red[kThreads / 64 - 1][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t chunk = blockIdx.x / A.slabs;
+  const int slab = static_cast<int>(blockIdx.x - chunk * A.slabs);
+  const int live = __builtin_amdgcn_readfirstlane(*A.live);
+  const int64_t c0 = chunk * A.chunk, c1 = c0 + A.chunk;
+  if (c1 >= live) return;  // the last chunk: nothing goes on behind it
+  const Rec r = A.recs[c1 - 1];
+  if (r.end <= c1) return;
+  // began before this chunk: another block's
+  if (c0 > 0 && A.recs[c0 - 1].key == r.key) return;
+  const int col = slab * kSlab + lane * kVec, nc = A.cols - col;
+  const int64_t stop = (r.end - 1) / A.chunk;  // the last chunk it reaches
+  float acc[kVec] = {};
+  constexpr int W = kThreads / 64, U = 8;
+  if (nc > 0) {
+    if (wave == 0) {
+      const float4 t = *reinterpret_cast<const float4*>(A.tail + chunk * A.ld_part + col);
+      acc[0] = t.x, acc[1] = t.y, acc[2] = t.z, acc[3] = t.w;
+    }
+    for (int64_t j0 = chunk + 1 + wave; j0 <= stop; j0 += W * U) {
+      float4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        x[u] = j0 + u * W <= stop ? *reinterpret_cast<const float4*>(A.head + (j0 + u * W) * A.ld_part + col)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) acc[0] += x[u].x, acc[1] += x[u].y, acc[2] += x[u].z, acc[3] += x[u].w;
+    }
+  }
+  if (wave > 0) red[wave - 1][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int w = 0; w < W - 1; ++w) {
+    const float4 t = red[w][lane];
+    acc[0] += t.x, acc[1] += t.y, acc[2] += t.z, acc[3] += t.w;
+  }
+  int64_t row = r.key;
+  if (MODE == kRows) {
+    row = distinct_in(A.distinct, 0, r.key / A.range, lane) + r.slot;
+    if (slab == 0 && lane == 0) A.rows[row] = r.key;
+  }
+  put<G, MODE>(A, row, col, nc, acc);
+}
+
+// ------------------------------------------------------------ Adam on rows
+
+struct RowArgs {
+  void* table;
+  float* m;
+  float* v;
+  int64_t ld;
+  const int32_t* rows;
+  const void* values;
+  const int32_t* count;
+  const float* gscale;
+  int64_t capacity;
+  int32_t vocab, cols;
+  int32_t vpr;      // vectors of four in a row
+  uint32_t magic;   // for divisions by vpr
+  int32_t per;      // rows of a block's turn
+  muon_adam::Consts k;
+};
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void embed_adam_kernel(RowArgs A) {
+  muon_adam::Consts k = A.k;
+  k.gs = A.gscale ? *A.gscale : 1.f;
+  const int64_t count = min(int64_t(*A.count), A.capacity);
+  const uint32_t vpr = static_cast<uint32_t>(A.vpr);
+  for (int64_t r0 = int64_t(blockIdx.x) * A.per; r0 < count; r0 += int64_t(gridDim.x) * A.per) {
+    const uint32_t nv = vpr * static_cast<uint32_t>(min(count - r0, int64_t(A.per)));
+    for (uint32_t i = threadIdx.x; i < nv; i += kThreads) {
+      const uint32_t r = div_by(i, vpr, A.magic);
+      const int c = static_cast<int>(i - r * vpr) * kVec, nc = A.cols - c;
+      const int32_t id = A.rows[r0 + r];
+      if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(A.vocab)) continue;
+      T* const p = static_cast<T*>(A.table) + int64_t(id) * A.ld + c;
+      float* const m = A.m + int64_t(id) * A.cols + c;
+      float* const v = A.v + int64_t(id) * A.cols + c;
+      muon_adam::Vec4 x;
+      load4_of(p, nc, x.p);
+      load4_of(static_cast<const T*>(A.values) + (r0 + r) * A.cols + c, nc, x.g);
+      load4_of(m, nc, x.m);
+      load4_of(v, nc, x.v);
+#pragma unroll
+      for (int q = 0; q < kVec; ++q) x.p[q] = muon_adam::adam_elem(x.p[q], x.g[q], x.m[q], x.v[q], k);
+      store4_of(m, nc, x.m);
+      store4_of(v, nc, x.v);
+      store4_of(p, nc, x.p);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+int64_t size_of(int32_t dtype) { return dtype == MUON_F32 ? 4 : 2; }
+
+struct Sizes {
+  int32_t range, blocks;  // sort: entries of a block, blocks
+  int32_t chunk, chunks;  // sum: records of a chunk, chunks
+  int32_t slabs;
+  int64_t ld_part;
+  size_t recs, distinct, live, head, tail, total;  // byte offsets, and the whole
+};
+
+// Sort: one block per CU, as long as its counters fit. Sum: chunks short
+// enough that chunks and slabs give every CU a few waves, of at least 4 and at
+// most 64 records (a lane each).
+Sizes sizes_of(int64_t vocab, int64_t cols, int64_t n) {
+  Sizes s{};
+  s.range = static_cast<int32_t>(std::min<int64_t>(kMaxRange, (vocab + kSortBlocks - 1) / kSortBlocks));
+  s.blocks = static_cast<int32_t>((vocab + s.range - 1) / s.range);
+  s.slabs = static_cast<int32_t>((cols + kSlab - 1) / kSlab);
+  int64_t chunk = 4;
+  while (chunk < 64 && (n + chunk - 1) / chunk * s.slabs > kSumWaves) chunk *= 2;
+  s.chunk = static_cast<int32_t>(chunk);
+  s.chunks = static_cast<int32_t>((n + chunk - 1) / chunk);
+  s.ld_part = (cols + kVec - 1) / kVec * kVec;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  // room for the chunks of any batch up to n (shorter batches may have more of them)
+  const int64_t most = std::min((n + 3) / 4, std::max((n + 63) / 64, kSumWaves / s.slabs + int64_t(1)));
+  const size_t part = up(size_t(most) * size_t(s.ld_part) * sizeof(float));
+  s.recs = 0;
+  s.distinct = s.recs + up(size_t(n) * sizeof(Rec));
+  s.live = s.distinct + up(size_t(s.blocks) * sizeof(int32_t));
+  s.head = s.live + 256;
+  s.tail = s.head + part;
+  s.total = s.tail + part;
+  return s;
+}
+
+uint32_t magic_of(int64_t d) { return static_cast<uint32_t>(UINT32_MAX / static_cast<uint64_t>(d)); }
+
+// Byte ranges of a call; true if a written one meets another.
+struct Spans {
+  struct Span {
+    uintptr_t lo, hi;
+    bool write;
+  } s[10];
+  int n = 0;
+  bool wraps = false;
+  void add(const void* p, int64_t bytes, bool write) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    if (bytes <= 0 || p == nullptr) return;
+    if (lo > UINTPTR_MAX - static_cast<uintptr_t>(bytes)) wraps = true;
+    s[n++] = {lo, lo + static_cast<uintptr_t>(bytes), write};
+  }
+  bool meet() const {
+    if (wraps) return true;
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < i; ++j)
+        if ((s[i].write || s[j].write) && s[i].lo < s[j].hi && s[j].lo < s[i].hi) return true;
+    return false;
+  }
+};
+
+int64_t span_of(int64_t rows, int64_t ld, int64_t cols, int64_t es) { return rows > 0 ? ((rows - 1) * ld + cols) * es : 0; }
+
+muon_status check_sizes(int64_t vocab, int64_t cols, int64_t max_tokens) {
+  if (vocab < 1 || vocab > MUON_EMBED_MAX_VOCAB || cols < 1 || cols > MUON_EMBED_MAX_COLS || max_tokens < 0 ||
+      max_tokens > MUON_EMBED_MAX_TOKENS)
+    return MUON_E_SHAPE;
+  if ((max_tokens + 63) / 64 * ((cols + kSlab - 1) / kSlab) > kMaxWaves) return MUON_E_SHAPE;
+  return MUON_OK;
+}
+
+}  // namespace muon_embed
+
+struct muon_embed_plan_s {
+  int device = -1;
+  muon_dtype dtype = MUON_BF16;
+  muon_embed_table t{};
+  int64_t max_tokens = 0;
+  const float* gscale = nullptr;
+};
+
+namespace {
+
+using namespace muon_embed;
+
+bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+muon_status check_tokens(const muon_embed_plan* p, const muon_embed_tokens* t) {
+  if (t == nullptr) return MUON_E_INVALID;
+  if (t->reserved != 0 || (t->wide != 0 && t->wide != 1)) return MUON_E_INVALID;
+  if (t->n < 0 || t->n > p->max_tokens) return MUON_E_SHAPE;
+  if (t->n > 0 && t->data == nullptr) return MUON_E_INVALID;
+  return misaligned(t->data, t->wide ? 8 : 4) ? MUON_E_ALIGN : MUON_OK;
+}
+
+muon_status check_acts(const muon_embed_plan* p, const muon_embed_acts* a, int64_t n) {
+  if (a == nullptr || a->reserved != 0) return MUON_E_INVALID;
+  if (a->dtype != MUON_F32 && a->dtype != MUON_BF16) return MUON_E_DTYPE;
+  if (n == 0) return MUON_OK;
+  if (a->ld < p->t.cols || a->ld > MUON_EMBED_MAX_LD) return MUON_E_SHAPE;
+  if (a->data == nullptr) return MUON_E_INVALID;
+  return misaligned(a->data, size_t(size_of(a->dtype))) ? MUON_E_ALIGN : MUON_OK;
+}
+
+void add_table(const muon_embed_plan* p, Spans* s) {
+  s->add(p->t.table, span_of(p->t.vocab, p->t.ld, p->t.cols, size_of(p->dtype)), false);
+  s->add(p->t.exp_avg, p->t.vocab * p->t.cols * 4, false);
+  s->add(p->t.exp_avg_sq, p->t.vocab * p->t.cols * 4, false);
+}
+
+bool on_device(const muon_embed_plan* p) {
+  int dev = -1;
+  return hipGetDevice(&dev) == hipSuccess && dev == p->device;
+}
+
+muon_status launched() { return hipGetLastError() == hipSuccess ? MUON_OK : MUON_E_LAUNCH; }
+
+template <typename E, typename O>
+void launch_lookup(const LookArgs& a, bool wide, unsigned grid, hipStream_t s) {
+  if (wide) hipLaunchKernelGGL((embed_lookup_kernel<E, O, int64_t>), dim3(grid), dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((embed_lookup_kernel<E, O, int32_t>), dim3(grid), dim3(kThreads), 0, s, a);
+}
+
+template <typename D, typename G, int MODE>
+muon_status launch_sum(const SumArgs& a, hipStream_t s) {
+  const int64_t waves = int64_t(a.chunks) * a.slabs;
+  hipLaunchKernelGGL((embed_sum_kernel<D, G, MODE>), dim3(unsigned((waves + 3) / 4)), dim3(kThreads), 0, s, a);
+  muon_status st = launched();
+  if (st != MUON_OK || a.chunks < 2) return st;
+  hipLaunchKernelGGL((embed_join_kernel<G, MODE>), dim3(unsigned(waves)), dim3(kThreads), 0, s, a);
+  return launched();
+}
+
+template <int MODE>
+muon_status launch_sum(const SumArgs& a, int32_t dout, muon_dtype grad, hipStream_t s) {
+  if (dout == MUON_F32) return grad == MUON_F32 ? launch_sum<float, float, MODE>(a, s) : launch_sum<float, uint16_t, MODE>(a, s);
+  return grad == MUON_F32 ? launch_sum<uint16_t, float, MODE>(a, s) : launch_sum<uint16_t, uint16_t, MODE>(a, s);
+}
+
+muon_status run_gradient(muon_embed_plan* p, const muon_embed_tokens* tokens, const muon_embed_acts* dout, float scale,
+                         void* grad, int64_t grad_ld, int mode, int32_t* rows, int32_t* count, void* ws, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const Sizes z = sizes_of(p->t.vocab, p->t.cols, tokens->n);
+  char* const w = static_cast<char*>(ws);
+  SortArgs a{};
+  a.tokens = tokens->data;
+  a.recs = reinterpret_cast<Rec*>(w + z.recs);
+  a.distinct = reinterpret_cast<int32_t*>(w + z.distinct);
+  a.live = reinterpret_cast<int32_t*>(w + z.live);
+  a.grad = mode == kDense ? grad : nullptr;
+  a.grad_ld = grad_ld;
+  a.grad_f32 = p->dtype == MUON_F32;
+  a.n = static_cast<int32_t>(tokens->n);
+  a.vocab = static_cast<int32_t>(p->t.vocab);
+  a.cols = static_cast<int32_t>(p->t.cols);
+  a.range = z.range;
+  const size_t lds = size_t(kSortWaves + 2) * size_t(z.range) * sizeof(int32_t);
+  if (tokens->wide)
+    hipLaunchKernelGGL(embed_sort_kernel<int64_t>, dim3(unsigned(z.blocks)), dim3(kSortThreads), lds, s, a);
+  else
+    hipLaunchKernelGGL(embed_sort_kernel<int32_t>, dim3(unsigned(z.blocks)), dim3(kSortThreads), lds, s, a);
+  muon_status st = launched();
+  if (st != MUON_OK) return st;
+  SumArgs b{};
+  b.recs = a.recs;
+  b.distinct = a.distinct;
+  b.live = a.live;
+  b.dout = dout->data;
+  b.dout_ld = dout->ld;
+  b.grad = grad;
+  b.grad_ld = grad_ld;
+  b.rows = rows;
+  b.count = count;
+  b.head = reinterpret_cast<float*>(w + z.head);
+  b.tail = reinterpret_cast<float*>(w + z.tail);
+  b.ld_part = z.ld_part;
+  b.cols = a.cols;
+  b.slabs = z.slabs;
+  b.chunk = z.chunk;
+  b.chunks = std::max(1, z.chunks);  // no token: one wave that leaves the count
+  b.range = z.range;
+  b.blocks = z.blocks;
+  b.scale = scale;
+  if (mode != kRows && tokens->n == 0) return MUON_OK;
+  if (mode == kDense) return launch_sum<kDense>(b, dout->dtype, p->dtype, s);
+  if (mode == kAdd) return launch_sum<kAdd>(b, dout->dtype, p->dtype, s);
+  return launch_sum<kRows>(b, dout->dtype, p->dtype, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_embed_workspace_bytes(int64_t vocab, int64_t cols, int64_t max_tokens, size_t* bytes) {
+  if (bytes == nullptr) return MUON_E_INVALID;
+  const muon_status st = check_sizes(vocab, cols, max_tokens);
+  if (st != MUON_OK) return st;
+  *bytes = sizes_of(vocab, cols, max_tokens).total;
+  return MUON_OK;
+}
+
+muon_status muon_embed_plan_create(const muon_embed_table* table, muon_dtype dtype, int64_t max_tokens,
+                                   muon_embed_plan** plan) {
+  if (plan == nullptr) return MUON_E_INVALID;
+  *plan = nullptr;
+  if (table == nullptr) return MUON_E_INVALID;
+  if (dtype != MUON_F32 && dtype != MUON_BF16) return MUON_E_DTYPE;
+  muon_status st = check_sizes(table->vocab, table->cols, max_tokens);
+  if (st != MUON_OK) return st;
+  if (table->ld < table->cols || table->ld > MUON_EMBED_MAX_LD) return MUON_E_SHAPE;
+  if (table->table == nullptr || (table->exp_avg == nullptr) != (table->exp_avg_sq == nullptr)) return MUON_E_INVALID;
+  if (!std::isfinite(table->lr_mul) || !std::isfinite(table->wd_mul)) return MUON_E_INVALID;
+  if (misaligned(table->table, size_t(size_of(dtype))) || misaligned(table->exp_avg, 4) ||
+      misaligned(table->exp_avg_sq, 4))
+    return MUON_E_ALIGN;
+  Spans sp;
+  sp.add(table->table, span_of(table->vocab, table->ld, table->cols, size_of(dtype)), true);
+  sp.add(table->exp_avg, table->vocab * table->cols * 4, true);
+  sp.add(table->exp_avg_sq, table->vocab * table->cols * 4, true);
+  if (sp.meet()) return MUON_E_INVALID;
+  int dev = 0;
+  hipDeviceProp_t prop;
+  if (hipGetDevice(&dev) != hipSuccess || hipGetDeviceProperties(&prop, dev) != hipSuccess ||
+      std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
+    return MUON_E_DEVICE;
+  muon_embed_plan_s* p = new (std::nothrow) muon_embed_plan_s();
+  if (!p) return MUON_E_ALLOC;
+  p->device = dev;
+  p->dtype = dtype;
+  p->t = *table;
+  p->max_tokens = max_tokens;
+  *plan = p;
+  return MUON_OK;
+}
+
+muon_status muon_embed_plan_lookup(muon_embed_plan* plan, const muon_embed_tokens* tokens, float scale,
+                                   const muon_embed_acts* out, void* stream) {
+  if (plan == nullptr || !std::isfinite(scale)) return MUON_E_INVALID;
+  muon_status st = check_tokens(plan, tokens);
+  if (st != MUON_OK) return st;
+  const int64_t n = tokens->n;
+  if ((st = check_acts(plan, out, n)) != MUON_OK) return st;
+  if (n == 0) return MUON_OK;
+  Spans sp;
+  add_table(plan, &sp);
+  sp.add(tokens->data, n * (tokens->wide ? 8 : 4), false);
+  sp.add(out->data, span_of(n, out->ld, plan->t.cols, size_of(out->dtype)), true);
+  if (sp.meet()) return MUON_E_INVALID;
+  if (!on_device(plan)) return MUON_E_DEVICE;
+  LookArgs a{};
+  a.table = plan->t.table;
+  a.tokens = tokens->data;
+  a.out = out->data;
+  a.ld = plan->t.ld;
+  a.out_ld = out->ld;
+  a.n = n;
+  a.vocab = static_cast<int32_t>(plan->t.vocab);
+  a.cols = static_cast<int32_t>(plan->t.cols);
+  a.vpr = static_cast<int32_t>((plan->t.cols + kLookVec - 1) / kLookVec);
+  a.magic = magic_of(a.vpr);
+  a.per = std::max(1, kThreads * kLookRuns / a.vpr);
+  a.scale = scale;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const unsigned grid = unsigned((n + a.per - 1) / a.per);
+  const bool w = tokens->wide != 0, f = plan->dtype == MUON_F32, of = out->dtype == MUON_F32;
+  if (f && of) launch_lookup<float, float>(a, w, grid, s);
+  else if (f) launch_lookup<float, uint16_t>(a, w, grid, s);
+  else if (of) launch_lookup<uint16_t, float>(a, w, grid, s);
+  else launch_lookup<uint16_t, uint16_t>(a, w, grid, s);
+  return launched();
+}
+
+muon_status muon_embed_plan_gradient(muon_embed_plan* plan, const muon_embed_tokens* tokens, const muon_embed_acts* dout,
+                                     float scale, void* grad, int64_t grad_ld, int32_t accumulate, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (plan == nullptr || !std::isfinite(scale) || grad == nullptr || (accumulate != 0 && accumulate != 1))
+    return MUON_E_INVALID;
+  muon_status st = check_tokens(plan, tokens);
+  if (st != MUON_OK) return st;
+  const int64_t n = tokens->n, es = size_of(plan->dtype);
+  if ((st = check_acts(plan, dout, n)) != MUON_OK) return st;
+  if (grad_ld < plan->t.cols || grad_ld > MUON_EMBED_MAX_LD) return MUON_E_SHAPE;
+  if (misaligned(grad, size_t(es))) return MUON_E_ALIGN;
+  if (workspace == nullptr || misaligned(workspace, 256) ||
+      workspace_bytes < sizes_of(plan->t.vocab, plan->t.cols, n).total)
+    return MUON_E_WORKSPACE;
+  Spans sp;
+  add_table(plan, &sp);
+  sp.add(tokens->data, n * (tokens->wide ? 8 : 4), false);
+  sp.add(dout->data, span_of(n, dout->ld, plan->t.cols, size_of(dout->dtype)), false);
+  sp.add(grad, span_of(plan->t.vocab, grad_ld, plan->t.cols, es), true);
+  sp.add(workspace, int64_t(sizes_of(plan->t.vocab, plan->t.cols, n).total), true);
+  if (sp.meet()) return MUON_E_INVALID;
+  if (n == 0 && accumulate) return MUON_OK;
+  if (!on_device(plan)) return MUON_E_DEVICE;
+  return run_gradient(plan, tokens, dout, scale, grad, grad_ld, accumulate ? kAdd : kDense, nullptr, nullptr, workspace, stream);
+}
+
+muon_status muon_embed_plan_gradient_rows(muon_embed_plan* plan, const muon_embed_tokens* tokens,
+                                          const muon_embed_acts* dout, float scale, int32_t* rows, void* values,
+                                          int32_t* count, void* workspace, size_t workspace_bytes, void* stream) {
+  if (plan == nullptr || !std::isfinite(scale) || count == nullptr) return MUON_E_INVALID;
+  muon_status st = check_tokens(plan, tokens);
+  if (st != MUON_OK) return st;
+  const int64_t n = tokens->n, es = size_of(plan->dtype), cap = std::min(n, plan->t.vocab);
+  if ((st = check_acts(plan, dout, n)) != MUON_OK) return st;
+  if (n > 0 && (rows == nullptr || values == nullptr)) return MUON_E_INVALID;
+  if (misaligned(rows, 4) || misaligned(count, 4) || misaligned(values, size_t(es))) return MUON_E_ALIGN;
+  if (workspace == nullptr || misaligned(workspace, 256) ||
+      workspace_bytes < sizes_of(plan->t.vocab, plan->t.cols, n).total)
+    return MUON_E_WORKSPACE;
+  Spans sp;
+  add_table(plan, &sp);
+  sp.add(tokens->data, n * (tokens->wide ? 8 : 4), false);
+  sp.add(dout->data, span_of(n, dout->ld, plan->t.cols, size_of(dout->dtype)), false);
+  sp.add(rows, cap * 4, true);
+  sp.add(values, cap * plan->t.cols * es, true);
+  sp.add(count, 4, true);
+  sp.add(workspace, int64_t(sizes_of(plan->t.vocab, plan->t.cols, n).total), true);
+  if (sp.meet()) return MUON_E_INVALID;
+  if (!on_device(plan)) return MUON_E_DEVICE;
+  return run_gradient(plan, tokens, dout, scale, values, plan->t.cols, kRows, rows, count, workspace, stream);
+}
+
+muon_status muon_embed_plan_adam_rows(muon_embed_plan* plan, const muon_adam_config* cfg, const int32_t* rows,
+                                      const void* values, const int32_t* count, int64_t capacity, void* stream) {
+  if (plan == nullptr || cfg == nullptr || count == nullptr) return MUON_E_INVALID;
+  if (!std::isfinite(cfg->lr) || !std::isfinite(cfg->beta1) || !std::isfinite(cfg->beta2) || !std::isfinite(cfg->eps) ||
+      !std::isfinite(cfg->wd))
+    return MUON_E_INVALID;
+  if (cfg->beta1 < 0.f || cfg->beta1 >= 1.f || cfg->beta2 < 0.f || cfg->beta2 >= 1.f || cfg->eps < 0.f || cfg->step < 1)
+    return MUON_E_INVALID;
+  if (plan->t.exp_avg == nullptr) return MUON_E_INVALID;
+  if (capacity < 0 || capacity > plan->t.vocab) return MUON_E_SHAPE;
+  const int64_t es = size_of(plan->dtype);
+  if (capacity > 0 && (rows == nullptr || values == nullptr)) return MUON_E_INVALID;
+  if (misaligned(rows, 4) || misaligned(count, 4) || misaligned(values, size_t(es))) return MUON_E_ALIGN;
+  Spans sp;
+  const muon_embed_table& t = plan->t;
+  sp.add(t.table, span_of(t.vocab, t.ld, t.cols, es), true);
+  sp.add(t.exp_avg, t.vocab * t.cols * 4, true);
+  sp.add(t.exp_avg_sq, t.vocab * t.cols * 4, true);
+  sp.add(rows, capacity * 4, false);
+  sp.add(values, capacity * t.cols * es, false);
+  sp.add(count, 4, false);
+  if (sp.meet()) return MUON_E_INVALID;
+  if (capacity == 0) return MUON_OK;
+  if (!on_device(plan)) return MUON_E_DEVICE;
+  RowArgs a{};
+  a.table = t.table;
+  a.m = t.exp_avg;
+  a.v = t.exp_avg_sq;
+  a.ld = t.ld;
+  a.rows = rows;
+  a.values = values;
+  a.count = count;
+  a.gscale = plan->gscale;
+  a.capacity = capacity;
+  a.vocab = static_cast<int32_t>(t.vocab);
+  a.cols = static_cast<int32_t>(t.cols);
+  a.vpr = static_cast<int32_t>((t.cols + kVec - 1) / kVec);
+  a.magic = magic_of(a.vpr);
+  a.per = std::max(1, 2 * kThreads / a.vpr);
+  // the scalars of muon_adam_plan_step
+  const float lr = cfg->lr * t.lr_mul;
+  a.k.b1 = cfg->beta1;
+  a.k.c1 = 1.f - cfg->beta1;
+  a.k.b2 = cfg->beta2;
+  a.k.c2 = 1.f - cfg->beta2;
+  a.k.eps = cfg->eps;
+  a.k.keep = 1.f - lr * (cfg->wd * t.wd_mul);
+  a.k.step = lr * static_cast<float>(1.0 / (1.0 - std::pow(double(cfg->beta1), double(cfg->step))));
+  a.k.isb2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(double(cfg->beta2), double(cfg->step))));
+  a.k.gs = 1.f;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const unsigned grid = unsigned(std::min<int64_t>((capacity + a.per - 1) / a.per, 8192));
+  if (plan->dtype == MUON_F32) hipLaunchKernelGGL(embed_adam_kernel<float>, dim3(grid), dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL(embed_adam_kernel<uint16_t>, dim3(grid), dim3(kThreads), 0, s, a);
+  return launched();
+}
+
+muon_status muon_embed_plan_set_grad_scale(muon_embed_plan* plan, const float* scale) {
+  if (plan == nullptr) return MUON_E_INVALID;
+  if (misaligned(scale, 4)) return MUON_E_ALIGN;
+  plan->gscale = scale;
+  return MUON_OK;
+}
+
+void muon_embed_plan_destroy(muon_embed_plan* plan) { delete plan; }
+
+}  // extern "C"

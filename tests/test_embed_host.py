@@ -1,0 +1,88 @@
+"""The embedding table's entry points (include/muon_embed.h) without a GPU:
+sizes and arguments that are refused before any device call, workspace sizes,
+and how the binding checks and lays out tensors."""
+import ctypes
+
+import pytest
+import torch
+
+import muon_newton_schulz_04_amd as mu
+
+OK, INVALID, DTYPE, SHAPE, ALIGN = 0, 1, 2, 3, 4
+B = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return mu.load_library()
+
+
+def create(lib, dtype=mu.MUON_BF16, max_tokens=64, **kw):
+    f = dict(vocab=100, cols=8, ld=8, table=B, exp_avg=2 * B, exp_avg_sq=3 * B, lr_mul=1.0, wd_mul=1.0)
+    f.update(kw)
+    t = mu.MuonEmbedTable(*f.values())
+    h = ctypes.c_void_p(7)
+    code = lib.muon_embed_plan_create(ctypes.byref(t), dtype, max_tokens, ctypes.byref(h))
+    if code in (INVALID, DTYPE, SHAPE, ALIGN):
+        assert h.value is None  # NULL on error
+    return code
+
+
+@pytest.mark.parametrize("want,kw", [
+    (SHAPE, dict(vocab=0)), (SHAPE, dict(vocab=(1 << 24) + 1)), (SHAPE, dict(cols=0)), (SHAPE, dict(cols=65537, ld=65537)),
+    (SHAPE, dict(ld=7)), (SHAPE, dict(ld=(1 << 40) + 1)), (SHAPE, dict(max_tokens=-1)), (SHAPE, dict(max_tokens=(1 << 24) + 1)),
+    (SHAPE, dict(max_tokens=1 << 24, cols=8193, ld=8193)),
+    (DTYPE, dict(dtype=2)), (INVALID, dict(table=None)), (INVALID, dict(exp_avg=None)), (INVALID, dict(exp_avg_sq=None)),
+    (INVALID, dict(lr_mul=float("nan"))), (INVALID, dict(wd_mul=float("inf"))),
+    (ALIGN, dict(table=B + 1)), (ALIGN, dict(dtype=mu.MUON_F32, table=B + 2)), (ALIGN, dict(exp_avg=2 * B + 2)),
+    (INVALID, dict(exp_avg=B + 100 * 8 * 2 - 4)),                    # moments inside the table
+    (INVALID, dict(exp_avg=2 * B, exp_avg_sq=2 * B + 100 * 8 * 4 - 4)),
+    (INVALID, dict(table=(1 << 64) - 16)),                           # past the end of the address space
+])
+def test_plan_refusals(lib, want, kw):
+    assert create(lib, **kw) == want
+
+
+def test_plan_accepts_what_only_a_device_can_refuse(lib):
+    if torch.cuda.is_available():
+        pytest.skip("checks the order of the tests where there is no device")
+    for kw in ({}, dict(exp_avg=None, exp_avg_sq=None), dict(ld=11), dict(vocab=1, cols=1, ld=1), dict(max_tokens=0),
+               dict(table=B + 2), dict(exp_avg=B + 100 * 8 * 2)):
+        assert create(lib, **kw) == 6  # MUON_E_DEVICE: everything else was fine
+
+
+def test_null_arguments(lib):
+    n = ctypes.c_void_p(None)
+    t = mu.MuonEmbedTokens(None, 0, 0, 0)
+    a = mu.MuonEmbedActs(None, 8, 0, 0)
+    assert lib.muon_embed_plan_create(None, 0, 1, ctypes.byref(ctypes.c_void_p())) == INVALID
+    assert lib.muon_embed_plan_create(ctypes.byref(mu.MuonEmbedTable()), 0, 1, None) == INVALID
+    assert lib.muon_embed_plan_lookup(n, ctypes.byref(t), 1.0, ctypes.byref(a), None) == INVALID
+    assert lib.muon_embed_plan_gradient(n, ctypes.byref(t), ctypes.byref(a), 1.0, None, 8, 0, None, 0, None) == INVALID
+    assert lib.muon_embed_plan_gradient_rows(n, ctypes.byref(t), ctypes.byref(a), 1.0, None, None, None, None, 0, None) == INVALID
+    assert lib.muon_embed_plan_adam_rows(n, None, None, None, None, 0, None) == INVALID
+    assert lib.muon_embed_plan_set_grad_scale(n, None) == INVALID
+    assert lib.muon_embed_workspace_bytes(1, 1, 1, None) == INVALID
+    assert lib.muon_clip_plan_set_live_rows(n, 0, None, 1) == INVALID
+    lib.muon_embed_plan_destroy(n)
+
+
+def test_workspace_grows_with_the_batch(lib):
+    """A plan's workspace serves every smaller batch: sizes never fall as the batch grows."""
+    for vocab, cols in ((1, 1), (50257, 768), (100, 65536), (1 << 24, 8)):
+        last = 0
+        for n in sorted({0, 1, 2, 3, 4, 5, 63, 64, 65, 1000, 4096, 5461, 5462, 16383, 16384, 16385, 65536, 100000}):
+            size = mu.muon_embed_workspace_bytes(vocab, cols, n)
+            assert size >= last and size > 0
+            last = size
+    # the records (16 bytes a token) and the partial sums (two rows a chunk)
+    n = mu.muon_embed_workspace_bytes(50257, 768, 32768)
+    assert 32768 * 16 <= n <= 32768 * 16 + 2 * 1366 * 768 * 4 + 4096
+    for bad in ((0, 1, 1), (1, 0, 1), (1, 1, -1), ((1 << 24) + 1, 1, 1), (1, 65537, 1), (1, 1, (1 << 24) + 1)):
+        with pytest.raises(mu.MuonError):
+            mu.muon_embed_workspace_bytes(*bad)
+
+
+def test_binding_refuses_host_tensors_and_wrong_types():
+    with pytest.raises(ValueError):
+        mu.EmbeddingPlan(torch.zeros(4, 4), 8)  # host memory
