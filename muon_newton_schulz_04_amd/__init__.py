@@ -33,6 +33,9 @@ __all__ = [
     "muon_embed_workspace_bytes", "muon_embed_plan_create", "muon_embed_plan_lookup",
     "muon_embed_plan_gradient", "muon_embed_plan_gradient_rows", "muon_embed_plan_adam_rows",
     "muon_embed_plan_set_grad_scale", "muon_embed_plan_destroy",
+    "MuonStack", "MuonStackWeight", "StackPlan", "muon_stack_workspace_bytes",
+    "muon_stack_plan_create", "muon_stack_plan_step", "muon_stack_plan_set_weights",
+    "muon_stack_plan_step_apply", "muon_stack_plan_set_grad_scale", "muon_stack_plan_destroy",
     "MUON_F32", "MUON_BF16", "MUON_PRECISION_DEFAULT",
 ]
 
@@ -109,6 +112,17 @@ class MuonEmbedActs(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class MuonStack(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("stride", ctypes.c_int64), ("grad", ctypes.c_void_p),
+                ("momentum", ctypes.c_void_p), ("out", ctypes.c_void_p)]
+
+
+class MuonStackWeight(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("ld", ctypes.c_int64), ("stride", ctypes.c_int64),
+                ("lr_mul", ctypes.c_float), ("wd_mul", ctypes.c_float)]
+
+
 class MuonBufferInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("m", "n", "mp", "np", "x_lo", "x_op0", "x_op1", "gram", "poly", "x0_scale")]
@@ -169,6 +183,13 @@ def load_library(path: str = LIB_PATH):
         "muon_embed_plan_adam_rows": (i32, [vp, P(MuonAdamConfig), vp, vp, vp, i64, vp]),
         "muon_embed_plan_set_grad_scale": (i32, [vp, vp]),
         "muon_embed_plan_destroy": (None, [vp]),
+        "muon_stack_workspace_bytes": (i32, [P(MuonStack), i32, i32, P(sz)]),
+        "muon_stack_plan_create": (i32, [P(MuonStack), i32, i32, P(vp)]),
+        "muon_stack_plan_step": (i32, [vp, P(MuonConfig), vp, sz, vp]),
+        "muon_stack_plan_set_weights": (i32, [vp, P(MuonStackWeight), i32]),
+        "muon_stack_plan_step_apply": (i32, [vp, P(MuonConfig), P(MuonApply), vp, sz, vp]),
+        "muon_stack_plan_set_grad_scale": (i32, [vp, vp]),
+        "muon_stack_plan_destroy": (None, [vp]),
         "muon_adam_work_items": (i32, [P(MuonAdamTensor), i32, i32, P(i64)]),
     }
     for name, (res, args) in sig.items():
@@ -1013,4 +1034,172 @@ def muon_embed_plan_set_grad_scale(plan: EmbeddingPlan, scale):
 
 
 def muon_embed_plan_destroy(plan: EmbeddingPlan):
+    plan.destroy()
+
+
+# ------------------------------------------------ stacks of short matrices
+
+def _stack_layout(t):
+    """(count, rows, cols, ld, stride) of a 3-D view with a unit column stride (2-D: one matrix)."""
+    if t.dim() == 2:
+        t = t.unsqueeze(0)
+    if t.dim() != 3:
+        raise ValueError("a stack is a 3-D tensor (count, rows, cols), or one matrix")
+    count, rows, cols = t.shape
+    if t.numel() and cols > 1 and t.stride(2) != 1:
+        raise ValueError("stacks must be row-major with unit column stride")
+    return count, rows, cols, t.stride(1) if rows > 1 else cols, t.stride(0) if count > 1 else 0
+
+
+def _stacks(grads, momenta, outs):
+    """muon_stack array (and dtype code) from lists of torch tensors."""
+    n = len(grads)
+    if len(outs) != n or (momenta is not None and len(momenta) != n):
+        raise ValueError("grads, momenta and outs must have the same length")
+    arr = (MuonStack * max(n, 1))()
+    dt = None
+    for i in range(n):
+        g, m, o = grads[i], None if momenta is None else momenta[i], outs[i]
+        layout = _stack_layout(g)
+        for t in (g, o) + (() if m is None else (m,)):
+            d = _dtype_code(t)
+            dt = d if dt is None else dt
+            if d != dt:
+                raise TypeError("all tensors of a call must share one dtype")
+            if t.shape != g.shape or t.device != grads[0].device:
+                raise ValueError("grad, momentum and out must have the same shape and device")
+            if g.numel() and _stack_layout(t) != layout:
+                raise ValueError("grad, momentum and out must share their strides")
+        arr[i] = MuonStack(*layout, _ptr(g), _ptr(m), _ptr(o))
+    return arr, n, (MUON_BF16 if dt is None else dt)
+
+
+def muon_stack_workspace_bytes(grads, momenta=None, outs=None) -> int:
+    arr, n, dt = _stacks(grads, momenta, grads if outs is None else outs)
+    out = ctypes.c_size_t(0)
+    _check(load_library().muon_stack_workspace_bytes(arr, n, dt, ctypes.byref(out)), "muon_stack_workspace_bytes")
+    return out.value
+
+
+class StackPlan:
+    """The Muon step on stacks of matrices with a short side (at most 128): 3-D views
+    (count, rows, cols) over bf16 or float32 tensors, every matrix orthogonalised by itself.
+    The heads of a fused projection are ``w.view(heads, head_dim, d)``, those of an output
+    projection ``w.view(d, heads, head_dim).transpose(0, 1)``: no copy is made. grad, momentum
+    and out of a stack share their strides; ``out`` may be the grad itself, and is written by
+    ``step`` only (``step_apply`` writes the weights). A step needs a ``workspace``, allocated per
+    call unless one is given; calls that overlap in time need one each."""
+
+    def __init__(self, grads, momenta, outs):
+        import torch
+        lib = load_library()
+        self.handle = ctypes.c_void_p(None)
+        self._keep = (list(grads), None if momenta is None else list(momenta), list(outs))
+        arr, n, dt = _stacks(*self._keep)
+        self.dtype, self.n = dt, n
+        self.device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        if self.device.type != "cuda":
+            raise ValueError("stacks must be in device memory")
+        ws = ctypes.c_size_t(0)
+        _check(lib.muon_stack_workspace_bytes(arr, n, dt, ctypes.byref(ws)), "muon_stack_workspace_bytes")
+        self.workspace_bytes = ws.value
+        h = ctypes.c_void_p(None)
+        with torch.cuda.device(self.device):
+            _check(lib.muon_stack_plan_create(arr, n, dt, ctypes.byref(h)), "muon_stack_plan_create")
+        self.handle = h
+
+    def set_weights(self, weights, lr_mul=None, wd_mul=None):
+        """Attaches one weight tensor per stack (the grad's shape and dtype, its own strides);
+        lr_mul / wd_mul: per-stack multipliers (default 1)."""
+        import torch
+        n = self.n
+        if len(weights) != n:
+            raise ValueError("one weight per stack")
+        lr_mul = [1.0] * n if lr_mul is None else list(lr_mul)
+        wd_mul = [1.0] * n if wd_mul is None else list(wd_mul)
+        arr = (MuonStackWeight * max(n, 1))()
+        for i, w in enumerate(weights):
+            g = self._keep[0][i]
+            if w is None:
+                arr[i] = MuonStackWeight(None, 0, 0, float(lr_mul[i]), float(wd_mul[i]))
+                continue
+            if w.shape != g.shape or _dtype_code(w) != self.dtype or w.device != self.device:
+                raise ValueError("weight must match its grad's shape, dtype and device")
+            ld, stride = _stack_layout(w)[3:]
+            arr[i] = MuonStackWeight(_ptr(w), ld, stride, float(lr_mul[i]), float(wd_mul[i]))
+        with torch.cuda.device(self.device):
+            _check(load_library().muon_stack_plan_set_weights(self.handle, arr, n), "muon_stack_plan_set_weights")
+        self._weights = list(weights)
+
+    def set_grad_scale(self, scale):
+        """Later steps use grad * scale (see ``MuonPlan.set_grad_scale``)."""
+        p = _scale_ptr(scale, self.device)
+        _check(load_library().muon_stack_plan_set_grad_scale(self.handle, p), "muon_stack_plan_set_grad_scale")
+        self._grad_scale = scale
+
+    def _run(self, entry, args, workspace, stream):
+        import torch
+        if workspace is None and stream is None:
+            workspace = torch.empty(max(1, self.workspace_bytes), dtype=torch.uint8, device=self.device)
+        elif workspace is None:
+            # allocated and, once dropped, reused in the order of the stream that uses it
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), self.device)
+            with torch.cuda.stream(s):
+                workspace = torch.empty(max(1, self.workspace_bytes), dtype=torch.uint8, device=self.device)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {self.device}")
+        index = self.device.index
+        handle = _current_stream(index) if stream is None else _stream_handle(stream)
+        args = (self.handle, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+        fn = getattr(load_library(), entry)
+        if torch.cuda.current_device() == index:
+            _check(fn(*args), entry)
+        else:
+            with torch.cuda.device(index):
+                _check(fn(*args), entry)
+        return workspace
+
+    def step(self, cfg: MuonConfig, workspace=None, stream=None):
+        """One Muon update of every matrix into its out and momentum; returns the workspace."""
+        return self._run("muon_stack_plan_step", (ctypes.byref(cfg),), workspace, stream)
+
+    def step_apply(self, cfg: MuonConfig, lr: float, wd: float, workspace=None, stream=None):
+        """The same with W <- W (1 - lr' wd') - lr' X into the attached weights, lr' = lr lr_mul, wd' = wd wd_mul
+        (``out`` is not written)."""
+        ap = MuonApply(float(lr), float(wd))
+        return self._run("muon_stack_plan_step_apply", (ctypes.byref(cfg), ctypes.byref(ap)), workspace, stream)
+
+    def destroy(self):
+        if self.handle:
+            load_library().muon_stack_plan_destroy(self.handle)
+            self.handle = ctypes.c_void_p(None)
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def muon_stack_plan_create(grads, momenta, outs) -> StackPlan:
+    return StackPlan(grads, momenta, outs)
+
+
+def muon_stack_plan_step(plan: StackPlan, cfg: MuonConfig, workspace=None, stream=None):
+    return plan.step(cfg, workspace, stream)
+
+
+def muon_stack_plan_set_weights(plan: StackPlan, weights, lr_mul=None, wd_mul=None):
+    plan.set_weights(weights, lr_mul, wd_mul)
+
+
+def muon_stack_plan_step_apply(plan: StackPlan, cfg: MuonConfig, lr: float, wd: float, workspace=None, stream=None):
+    return plan.step_apply(cfg, lr, wd, workspace, stream)
+
+
+def muon_stack_plan_set_grad_scale(plan: StackPlan, scale):
+    plan.set_grad_scale(scale)
+
+
+def muon_stack_plan_destroy(plan: StackPlan):
     plan.destroy()

@@ -1,0 +1,1093 @@
+// The Muon step on stacks of matrices with a short side (include/muon_stack.h).
+//
+// With m = min(rows, cols) <= 128 the Newton-Schulz iteration runs on the
+// m x m Gram matrix. Polynomials of one symmetric matrix commute, so from
+// A_0 = X X^T
+//
+//   Q_i = a I + b A_i + c A_i^2,  A_{i+1} = Q_i A_i Q_i,  P = Q_{s-1} .. Q_0
+//
+// and s steps are X <- P X: X (n columns) is read for A_0 and read and
+// written for P X, where the step-by-step form reads it twice and writes it
+// once for each of the s steps. Rounding errors of A along small eigenvalues
+// grow by the map's slope (a^2 at zero) in each of the s - 1 updates of A, so
+// A is formed anew from X after s steps (run_length).
+//
+// Phases of a matrix, each over runs of columns ("parts") or as a whole:
+//   gram    buf' and u from the gradient, A = sum of u u^T over the part
+//   solve   one workgroup: the norm (the trace of A), s steps, P
+//   update  X <- P X for the part's columns, and its sum of X X^T
+//   last    X <- P X for the part's columns, out or the weights
+// A tile of X is mp x kCols (mp = m padded to 32, 64 or 128), in LDS as two
+// fp16 numbers hi + lo per element, rows along the product's inner dimension:
+// [m][k] for X X^T, [k][m] for P X. Products are hi hi + hi lo + lo hi with
+// v_mfma_f32_32x32x16_f16.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "../../include/muon_stack.h"
+#include "overlap.hpp"
+#include "plan.hpp"
+
+namespace muon_stack_ns {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+// accesses at an element's alignment (the hardware takes any address)
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+
+// A matrix in the rows <= cols orientation.
+struct Mat {
+  const void* g;
+  void* b;
+  void* o;
+  void* w;
+  int64_t ld, wld;
+  int32_t m, n;
+  int32_t tall;        // rows > cols: the long side runs along memory rows
+  int32_t parts;
+  int64_t gram_off;    // workspace: per part an mp x mp partial Gram matrix (fp32, accumulator order)
+  int64_t exp_off;     // per part the exponent its operands were scaled by (int32)
+  int64_t rec_off;     // {sigma, exponent} of the first run of steps
+  int64_t p_off;       // P: mp x mp hi, then lo (fp16, scaled by kPScale)
+  int64_t x_off;       // X between runs of steps: n (padded to tiles) x mp, fp32
+  float lr_mul, wd_mul;
+};
+
+// Columns [beg, end) of a matrix, in tiles.
+struct Part {
+  int32_t mat, beg, end, index;
+};
+
+struct Args {
+  const Mat* mats;
+  const Part* parts;
+  char* ws;
+  const float* gscale;
+  float a, b, c, mu, eps, lr, wd;
+  int32_t nesterov, use_mom, apply;
+  int32_t runs, each, more;  // runs of steps: `each` steps, the first `more` of them one more
+  int32_t run;               // the run this launch belongs to
+};
+
+constexpr int kXExp = 12;             // operands are scaled to at most 2^13 (X) and 2^14 (A)
+constexpr float kAScale = 4096.f;     // A, Q A: entries at most 4
+constexpr float kPScale = 8.f;        // Q, P: entries at most 4096
+
+template <int MT> struct Cfg {
+  static constexpr int mp = 32 * MT;
+  static constexpr int cols = MT == 1 ? 128 : 64;      // kCols
+  static constexpr int threads = MT == 4 ? 512 : 256;
+  static constexpr int waves = threads / 64;
+  static constexpr int tiles = MT == 4 ? 2 : 1;        // 32 x 32 tiles of an mp x mp product per wave
+  static constexpr int ks = cols + 8;                  // row stride of [m][k], in halves: rows 16 bytes
+  static constexpr int ms = mp + 8;                    // of [k][m]; apart modulo the banks
+  static constexpr int lds_m = cols * ms * 4;          // bytes, hi and lo
+  static constexpr int lds_k = mp * ks * 4;
+  static constexpr int lds_stage = 4 * (mp * (cols + 4) > cols * (mp + 4) ? mp * (cols + 4) : cols * (mp + 4));
+  static constexpr int lds_second = lds_k > lds_stage ? lds_k : lds_stage;
+  static constexpr int lds_tile = lds_m + lds_second;
+  static constexpr int lds_solve = 2 * mp * ms * 4;
+  static constexpr int lds_whole = lds_tile > lds_solve ? lds_tile : lds_solve;
+};
+
+// ------------------------------------------------------------- elementwise
+
+__device__ __forceinline__ float bf2f(uint32_t h) { return __uint_as_float(h << 16); }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // round to nearest even
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
+}
+__device__ __forceinline__ float round_bf16(float a) { return __uint_as_float(pack_bf16(a, 0.f) << 16); }
+
+// Eight consecutive elements, the first n of them if fewer are left (zeros behind).
+__device__ __forceinline__ void load8(const uint16_t* p, int n, float (&x)[8]) {
+  if (n >= 8) {
+    const u32x4_u w = *reinterpret_cast<const u32x4_u*>(p);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      x[2 * q] = __uint_as_float(w[q] << 16);
+      x[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = q < n ? bf2f(p[q]) : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const float* p, int n, float (&x)[8]) {
+  if (n >= 8) {
+    const f32x4_u a = *reinterpret_cast<const f32x4_u*>(p), b = *reinterpret_cast<const f32x4_u*>(p + 4);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      x[q] = a[q];
+      x[q + 4] = b[q];
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = q < n ? p[q] : 0.f;
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, int n, const float (&x)[8]) {
+  if (n >= 8) {
+    const u32x4_u w = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+    *reinterpret_cast<u32x4_u*>(p) = w;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) p[q] = static_cast<uint16_t>(pack_bf16(x[q], 0.f));
+  }
+}
+__device__ __forceinline__ void store8(float* p, int n, const float (&x)[8]) {
+  if (n >= 8) {
+    *reinterpret_cast<f32x4_u*>(p) = f32x4_u{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4_u*>(p + 4) = f32x4_u{x[4], x[5], x[6], x[7]};
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) p[q] = x[q];
+  }
+}
+
+// mu b + g rounded once to the buffer's type. fp32: the fused multiply-add.
+// bf16: s = fma(mu, b, g) is the float32 nearest to the exact value; rounding
+// it again is the nearest bf16 unless s lies half way between two of them and
+// the exact value does not. Then the sign of the exact remainder (float64:
+// the product is exact, the sum splits exactly into S + E, and so does S - s)
+// moves s off the halfway point.
+__device__ __forceinline__ float momentum(float mu, float b, float g, const float*) { return __fmaf_rn(mu, b, g); }
+__device__ __forceinline__ float momentum(float mu, float b, float g, const uint16_t*) {
+  const float s = __fmaf_rn(mu, b, g);
+  const uint32_t bits = __float_as_uint(s);
+  if ((bits & 0xffffu) == 0x8000u) {
+    const double p = __dmul_rn(double(mu), double(b)), big = __dadd_rn(p, double(g)), part = __dsub_rn(big, p);
+    const double rest = __dadd_rn(__dsub_rn(p, __dsub_rn(big, part)), __dsub_rn(double(g), part));
+    const double off = __dadd_rn(__dsub_rn(big, double(s)), rest);
+    if (off > 0.0 || off < 0.0) return round_bf16(__uint_as_float((off > 0.0) == (s > 0.0) ? bits + 1u : bits - 1u));
+  }
+  return round_bf16(s);
+}
+
+// The exponent e of |x| in [2^e, 2^(e+1)), in [-126, 127].
+__device__ __forceinline__ int exponent(float x) {
+  const int e = static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127;
+  return min(max(e, -126), 127);
+}
+
+// x = hi + lo, two of them at once, as packed pairs.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const f16x2 h = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
+  const f16x2 l = {static_cast<_Float16>(x - static_cast<float>(h[0])), static_cast<_Float16>(y - static_cast<float>(h[1]))};
+  hi = __builtin_bit_cast(uint32_t, h);
+  lo = __builtin_bit_cast(uint32_t, l);
+}
+
+// ---------------------------------------------------------- tiles in memory
+
+// The two vectors of eight consecutive elements a thread moves of a tile:
+// vector c8 of rows ra and rb. Rows run along memory: the m rows of a wide
+// matrix (eight columns each), the columns of a tall one (eight of its m).
+struct Spot {
+  int ra, rb, c;
+};
+template <int MT, bool ALONG_K, bool PAIRS>
+__device__ __forceinline__ Spot spot(int tid) {
+  typedef Cfg<MT> C;
+  constexpr int vpr = (ALONG_K ? C::cols : C::mp) / 8;
+  const int r = tid / vpr, c = tid % vpr * 8;
+  if (PAIRS) return {2 * r, 2 * r + 1, c};
+  return {r, r + C::threads / vpr, c};
+}
+
+// Elements of the tile's row r from c on that exist (0 .. 8), and where they are.
+template <bool TALL>
+__device__ __forceinline__ int extent(const Mat& M, int k0, int r, int c) {
+  const int row = TALL ? k0 + r : r, rows = TALL ? M.n : M.m, left = TALL ? M.m - c : M.n - (k0 + c);
+  return row < rows ? left : 0;
+}
+template <bool TALL>
+__device__ __forceinline__ int64_t place(int64_t ld, int k0, int r, int c) {
+  return TALL ? int64_t(k0 + r) * ld + c : int64_t(r) * ld + (k0 + c);
+}
+
+// Writes a thread's 2 x 8 values (scaled to fp16's range) as hi and lo.
+// SAME: the tile's rows are memory rows, eight consecutive halves each; else
+// the memory rows ra, rb = ra + 1 are columns of the tile, in pairs.
+template <bool SAME>
+__device__ __forceinline__ void put_tile(_Float16* hi, _Float16* lo, int stride, const Spot& s, const float (&x)[2][8]) {
+  if constexpr (SAME) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint4 h, l;
+      split2(x[j][0], x[j][1], h.x, l.x);
+      split2(x[j][2], x[j][3], h.y, l.y);
+      split2(x[j][4], x[j][5], h.z, l.z);
+      split2(x[j][6], x[j][7], h.w, l.w);
+      const int at = (j ? s.rb : s.ra) * stride + s.c;
+      *reinterpret_cast<uint4*>(hi + at) = h;
+      *reinterpret_cast<uint4*>(lo + at) = l;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      uint32_t h, l;
+      split2(x[0][q], x[1][q], h, l);
+      const int at = (s.c + q) * stride + s.ra;
+      *reinterpret_cast<uint32_t*>(hi + at) = h;
+      *reinterpret_cast<uint32_t*>(lo + at) = l;
+    }
+  }
+}
+
+// acc += X Y^T over K of the inner dimension, from K0: 32 rows of X from row
+// xr, 32 of Y from row yr (rows `stride` halves apart). Accumulator i of a
+// lane: row 8 (i / 4) + 4 (lane / 32) + i % 4, column lane % 32.
+__device__ __forceinline__ f32x16 mul3(const f16x8& xh, const f16x8& xl, const f16x8& yh, const f16x8& yl, f32x16 acc) {
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh, yh, acc, 0, 0, 0);
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh, yl, acc, 0, 0, 0);
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(xl, yh, acc, 0, 0, 0);
+  return acc;
+}
+__device__ __forceinline__ f16x8 frag(const _Float16* p, int row, int stride, int k, int lane) {
+  return *reinterpret_cast<const f16x8*>(p + (row + (lane & 31)) * stride + k + (lane >> 5) * 8);
+}
+
+// The rows (of 4) and column of a lane's accumulators 4 g .. 4 g + 3.
+__device__ __forceinline__ int acc_row(int g, int lane) { return 8 * g + 4 * (lane >> 5); }
+
+// Writes the transpose of a 32 x 32 accumulator tile: element (row, col) goes
+// to [c0 + col][r0 + row], four consecutive halves at a time.
+__device__ __forceinline__ void put_acc(_Float16* hi, _Float16* lo, int stride, int r0, int c0, const f32x16& x, float scale, int lane) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint2 h, l;
+    split2(x[4 * g] * scale, x[4 * g + 1] * scale, h.x, l.x);
+    split2(x[4 * g + 2] * scale, x[4 * g + 3] * scale, h.y, l.y);
+    const int at = (c0 + (lane & 31)) * stride + r0 + acc_row(g, lane);
+    *reinterpret_cast<uint2*>(hi + at) = h;
+    *reinterpret_cast<uint2*>(lo + at) = l;
+  }
+}
+
+// Which 32 x 32 tiles of an mp x mp product a wave has: rows ti, columns tj + t.
+template <int MT>
+__device__ __forceinline__ void tile_of(int wave, int& ti, int& tj) {
+  if (MT == 4) ti = wave >> 1, tj = 2 * (wave & 1);
+  else if (MT == 2) ti = wave >> 1, tj = wave & 1;
+  else ti = 0, tj = 0;
+}
+
+// acc += the tile's K K^T. MT = 1 has one tile of the product: each wave takes
+// every fourth step of the inner dimension, and the sums are added at the end.
+template <int MT>
+__device__ __forceinline__ void gram_tile(const _Float16* hi, const _Float16* lo, f32x16 (&acc)[Cfg<MT>::tiles], int wave, int lane) {
+  typedef Cfg<MT> C;
+  int ti, tj;
+  tile_of<MT>(wave, ti, tj);
+  constexpr int step = MT == 1 ? C::waves : 1;
+#pragma unroll
+  for (int k = 0; k < C::cols / 16; k += step) {
+    const int kk = 16 * (MT == 1 ? k + wave : k);
+    const f16x8 xh = frag(hi, 32 * ti, C::ks, kk, lane), xl = frag(lo, 32 * ti, C::ks, kk, lane);
+#pragma unroll
+    for (int t = 0; t < C::tiles; ++t) {
+      const f16x8 yh = frag(hi, 32 * (tj + t), C::ks, kk, lane), yl = frag(lo, 32 * (tj + t), C::ks, kk, lane);
+      acc[t] = mul3(xh, xl, yh, yl, acc[t]);
+    }
+  }
+}
+
+// The part's sum of X X^T goes to the workspace, in accumulator order.
+template <int MT>
+__device__ __forceinline__ void put_gram(const Args& A, const Mat& M, int part, f32x16 (&acc)[Cfg<MT>::tiles], char* lds, int wave, int lane) {
+  typedef Cfg<MT> C;
+  float4* const out = reinterpret_cast<float4*>(A.ws + M.gram_off) + int64_t(part) * (C::mp * C::mp / 4);
+  if constexpr (MT == 1) {
+    float4* const red = reinterpret_cast<float4*>(lds);
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < 4; ++g) red[(wave * 4 + g) * 64 + lane] = make_float4(acc[0][4 * g], acc[0][4 * g + 1], acc[0][4 * g + 2], acc[0][4 * g + 3]);
+    __syncthreads();
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < C::waves; ++w) {
+      const float4 t = red[(w * 4 + wave) * 64 + lane];
+      s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
+    }
+    out[wave * 64 + lane] = s;
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int t = 0; t < C::tiles; ++t)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        out[((wave * C::tiles + t) * 4 + g) * 64 + lane] = make_float4(acc[t][4 * g], acc[t][4 * g + 1], acc[t][4 * g + 2], acc[t][4 * g + 3]);
+  }
+}
+
+// ------------------------------------------------------------------ phases
+
+// G times the plan's factor, and u from it; FIRST: the momentum is read,
+// updated and written, else it has been.
+template <typename T, bool TALL, bool FIRST>
+__device__ __forceinline__ void load_u(const Args& A, const Mat& M, int k0, int r, int c, float gs, float (&u)[8]) {
+  const int n = extent<TALL>(M, k0, r, c);
+  if (n <= 0) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) u[q] = 0.f;
+    return;
+  }
+  const int64_t at = place<TALL>(M.ld, k0, r, c);
+  load8(static_cast<const T*>(M.g) + at, n, u);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) u[q] *= gs;
+  if (!A.use_mom) return;
+  float b[8];
+  T* const buf = static_cast<T*>(M.b) + at;
+  load8(buf, n, b);
+  if constexpr (FIRST) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) b[q] = momentum(A.mu, b[q], u[q], buf);
+    store8(buf, n, b);
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) u[q] = A.nesterov ? __fmaf_rn(A.mu, b[q], u[q]) : b[q];
+}
+
+// Phase gram over the part's columns. The operands are scaled by a power of
+// two that puts the largest |u| so far into [2^12, 2^13): when a tile raises
+// it, the sums so far are rescaled, which is exact.
+template <typename T, int MT, bool TALL>
+__device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Part& p, char* lds) {
+  typedef Cfg<MT> C;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  _Float16* const hi = reinterpret_cast<_Float16*>(lds);
+  _Float16* const lo = hi + C::mp * C::ks;
+  __shared__ int top[C::waves];
+  const float gs = A.gscale ? *A.gscale : 1.f;
+  // a wide matrix's rows are the tile's; of a tall one they are its columns
+  const Spot s = spot<MT, !TALL, TALL>(tid);
+  f32x16 acc[C::tiles] = {};
+  int e = -126;
+  for (int t = p.beg; t < p.end; ++t) {
+    const int k0 = t * C::cols;
+    float u[2][8];
+    load_u<T, TALL, true>(A, M, k0, s.ra, s.c, gs, u[0]);
+    load_u<T, TALL, true>(A, M, k0, s.rb, s.c, gs, u[1]);
+    float big = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) big = fmaxf(big, fmaxf(fabsf(u[0][q]), fabsf(u[1][q])));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
+    if (lane == 0) top[wave] = exponent(big);
+    __syncthreads();  // the tile of the pass before has been read, too
+    int now = e;
+#pragma unroll
+    for (int w = 0; w < C::waves; ++w) now = max(now, top[w]);
+    now = __builtin_amdgcn_readfirstlane(now);
+    if (now > e) {
+#pragma unroll
+      for (int i = 0; i < C::tiles; ++i)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][q] = ldexpf(acc[i][q], 2 * (e - now));
+      e = now;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) u[j][q] = ldexpf(u[j][q], kXExp - e);
+    put_tile<!TALL>(hi, lo, C::ks, s, u);
+    __syncthreads();
+    gram_tile<MT>(hi, lo, acc, wave, lane);
+  }
+  put_gram<MT>(A, M, p.index, acc, lds, wave, lane);
+  if (tid == 0) reinterpret_cast<int32_t*>(A.ws + M.exp_off)[p.index] = e;
+}
+
+template <int MT>
+__device__ __forceinline__ void mul_lds(const _Float16* x, const _Float16* y, f32x16 (&acc)[Cfg<MT>::tiles], float scale, int wave, int lane) {
+  typedef Cfg<MT> C;
+  int ti, tj;
+  tile_of<MT>(wave, ti, tj);
+#pragma unroll
+  for (int t = 0; t < C::tiles; ++t) acc[t] = f32x16{};
+  if (MT == 1 && wave > 0) return;
+#pragma unroll 2
+  for (int k = 0; k < C::mp; k += 16) {
+    const f16x8 xh = frag(x, 32 * ti, C::ms, k, lane), xl = frag(x + C::mp * C::ms, 32 * ti, C::ms, k, lane);
+#pragma unroll
+    for (int t = 0; t < C::tiles; ++t) {
+      const f16x8 yh = frag(y, 32 * (tj + t), C::ms, k, lane), yl = frag(y + C::mp * C::ms, 32 * (tj + t), C::ms, k, lane);
+      acc[t] = mul3(xh, xl, yh, yl, acc[t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < C::tiles; ++t)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) acc[t][q] *= scale;
+}
+
+template <int MT>
+__device__ __forceinline__ void put_lds(_Float16* x, const f32x16 (&v)[Cfg<MT>::tiles], float scale, int wave, int lane) {
+  typedef Cfg<MT> C;
+  int ti, tj;
+  tile_of<MT>(wave, ti, tj);
+  if (MT == 1 && wave > 0) return;
+#pragma unroll
+  for (int t = 0; t < C::tiles; ++t) put_acc(x, x + C::mp * C::ms, C::ms, 32 * ti, 32 * (tj + t), v[t], scale, lane);
+}
+
+// Phase solve: A from its parts, the norm (first run), the run's steps on A
+// and P. All matrices are symmetric, so a product X Y is X Y^T, and a tile
+// may be stored transposed.
+template <int MT>
+__device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run, char* lds) {
+  typedef Cfg<MT> C;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  _Float16* const l1 = reinterpret_cast<_Float16*>(lds);
+  _Float16* const l2 = l1 + 2 * C::mp * C::ms;
+  __shared__ float red[C::waves];
+  int ti, tj;
+  tile_of<MT>(wave, ti, tj);
+  const bool mine = MT != 1 || wave == 0;
+  const int32_t* const exps = reinterpret_cast<const int32_t*>(A.ws + M.exp_off);
+  int e = kXExp;
+  if (run == 0) {
+    e = -126;
+    for (int p = 0; p < M.parts; ++p) e = max(e, exps[p]);
+  }
+  f32x16 a[C::tiles] = {}, pr[C::tiles] = {}, q[C::tiles], acc[C::tiles];
+  const float4* in = reinterpret_cast<const float4*>(A.ws + M.gram_off);
+  if (mine)
+    for (int p = 0; p < M.parts; ++p, in += C::mp * C::mp / 4) {
+      const int shift = run == 0 ? 2 * (exps[p] - e) : 0;
+#pragma unroll
+      for (int t = 0; t < C::tiles; ++t)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float4 x = in[((wave * C::tiles + t) * 4 + g) * 64 + lane];
+          a[t][4 * g] += ldexpf(x.x, shift);
+          a[t][4 * g + 1] += ldexpf(x.y, shift);
+          a[t][4 * g + 2] += ldexpf(x.z, shift);
+          a[t][4 * g + 3] += ldexpf(x.w, shift);
+        }
+    }
+  float scale = 1.f / (kAScale * kAScale);  // X was scaled by 2^kXExp
+  if (run == 0) {
+    // the trace is the sum of squares
+    float d = 0.f;
+#pragma unroll
+    for (int t = 0; t < C::tiles; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (mine && ti == tj + t && acc_row(i >> 2, lane) + (i & 3) == (lane & 31)) d += a[t][i];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) d += __shfl_xor(d, o, 64);
+    if (lane == 0) red[wave] = d;
+    __syncthreads();
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < C::waves; ++w) sum += red[w];
+    // sigma = 1 / ((norm + eps) 2^(kXExp - e)), whatever float32 makes of the norm; zeros give zeros
+    const double norm = ldexp(sqrt(double(sum)), e - kXExp);
+    float sigma = static_cast<float>(1.0 / ldexp(norm + double(A.eps), kXExp - e));
+    if (sum == 0.f) sigma = 0.f;
+    scale = sigma * sigma;
+    if (tid == 0) {
+      reinterpret_cast<float*>(A.ws + M.rec_off)[0] = sigma;
+      reinterpret_cast<int32_t*>(A.ws + M.rec_off)[1] = e;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < C::tiles; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a[t][i] *= scale;
+  // the identity's elements of this lane, for a I
+  auto diag = [&](int t, int i) { return ti == tj + t && acc_row(i >> 2, lane) + (i & 3) == (lane & 31); };
+  const int steps = A.each + (run < A.more ? 1 : 0);
+  if (steps == 0) {
+#pragma unroll
+    for (int t = 0; t < C::tiles; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pr[t][i] = diag(t, i) ? 1.f : 0.f;
+  }
+  if (steps > 0) put_lds<MT>(l1, a, kAScale, wave, lane);
+  __syncthreads();
+  for (int i = 0; i < steps; ++i) {
+    const bool more = i + 1 < steps;
+    mul_lds<MT>(l1, l1, acc, 1.f / (kAScale * kAScale), wave, lane);
+#pragma unroll
+    for (int t = 0; t < C::tiles; ++t)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) q[t][j] = __fmaf_rn(A.c, acc[t][j], __fmaf_rn(A.b, a[t][j], diag(t, j) ? A.a : 0.f));
+    if (i == 0) {
+#pragma unroll
+      for (int t = 0; t < C::tiles; ++t) pr[t] = q[t];
+      if (!more) break;
+    }
+    put_lds<MT>(l2, q, kPScale, wave, lane);
+    __syncthreads();
+    if (more) {
+      mul_lds<MT>(l2, l1, acc, 1.f / (kAScale * kPScale), wave, lane);
+      __syncthreads();
+      put_lds<MT>(l1, acc, kAScale, wave, lane);
+      __syncthreads();
+      mul_lds<MT>(l1, l2, a, 1.f / (kAScale * kPScale), wave, lane);
+    }
+    if (i > 0) {
+      __syncthreads();
+      put_lds<MT>(l1, pr, kPScale, wave, lane);
+      __syncthreads();
+      mul_lds<MT>(l2, l1, pr, 1.f / (kPScale * kPScale), wave, lane);
+    }
+    __syncthreads();
+    if (more) {
+      put_lds<MT>(l1, a, kAScale, wave, lane);
+      __syncthreads();
+    }
+  }
+  if (mine) {
+    _Float16* const out = reinterpret_cast<_Float16*>(A.ws + M.p_off);
+#pragma unroll
+    for (int t = 0; t < C::tiles; ++t) put_acc(out, out + C::mp * C::mp, C::mp, 32 * ti, 32 * (tj + t), pr[t], kPScale, lane);
+  }
+}
+
+// P X for the part's columns: GRAD: X is sigma u, from the gradients, else what
+// the run before left. LAST: out or the weights, else X and its X X^T.
+template <typename T, int MT, bool TALL, bool GRAD, bool LAST>
+__device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const Part& p, char* lds) {
+  typedef Cfg<MT> C;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  _Float16* const mh = reinterpret_cast<_Float16*>(lds);        // [k][m]
+  _Float16* const ml = mh + C::cols * C::ms;
+  _Float16* const kh = reinterpret_cast<_Float16*>(lds + C::lds_m);  // [m][k]
+  _Float16* const kl = kh + C::mp * C::ks;
+  float* const stage = reinterpret_cast<float*>(lds + C::lds_m);
+  const int mi = wave % MT, ki = wave / MT;  // the wave's rows of X and columns of the tile, in 32s
+  const float gs = A.gscale ? *A.gscale : 1.f;
+  float f = 1.f / (kAScale * kPScale);
+  int e = 0;
+  if (GRAD) {
+    f = reinterpret_cast<const float*>(A.ws + M.rec_off)[0] * (1.f / kPScale);
+    e = reinterpret_cast<const int32_t*>(A.ws + M.rec_off)[1];
+  }
+  f16x8 ph[C::mp / 16], pl[C::mp / 16];
+  const _Float16* const pm = reinterpret_cast<const _Float16*>(A.ws + M.p_off);
+#pragma unroll
+  for (int k = 0; k < C::mp / 16; ++k) {
+    ph[k] = frag(pm, 32 * mi, C::mp, 16 * k, lane);
+    pl[k] = frag(pm + C::mp * C::mp, 32 * mi, C::mp, 16 * k, lane);
+  }
+  float* const xs = reinterpret_cast<float*>(A.ws + M.x_off);
+  constexpr bool kRowsAreK = TALL || !GRAD;  // memory rows are columns of X
+  const Spot s = spot<MT, !kRowsAreK, !kRowsAreK>(tid);
+  f32x16 acc2[C::tiles] = {};
+  for (int t = p.beg; t < p.end; ++t) {
+    const int k0 = t * C::cols;
+    float u[2][8];
+    if constexpr (GRAD) {
+      load_u<T, TALL, false>(A, M, k0, s.ra, s.c, gs, u[0]);
+      load_u<T, TALL, false>(A, M, k0, s.rb, s.c, gs, u[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) u[j][q] = ldexpf(u[j][q], kXExp - e);
+    } else {
+      load8(xs + int64_t(k0 + s.ra) * C::mp + s.c, 8, u[0]);
+      load8(xs + int64_t(k0 + s.rb) * C::mp + s.c, 8, u[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) u[j][q] *= kAScale;
+    }
+    put_tile<kRowsAreK>(mh, ml, C::ms, s, u);
+    __syncthreads();
+    f32x16 acc = {};
+#pragma unroll
+    for (int k = 0; k < C::mp / 16; ++k)
+      acc = mul3(frag(mh, 32 * ki, C::ms, 16 * k, lane), frag(ml, 32 * ki, C::ms, 16 * k, lane), ph[k], pl[k], acc);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] *= f;
+    const int col = 32 * mi + (lane & 31);
+    if constexpr (!LAST) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        xs[int64_t(k0 + 32 * ki + acc_row(i >> 2, lane) + (i & 3)) * C::mp + col] = acc[i];
+      put_acc(kh, kl, C::ks, 32 * ki, 32 * mi, acc, kAScale, lane);
+      __syncthreads();
+      gram_tile<MT>(kh, kl, acc2, wave, lane);
+    } else {
+      // through LDS, so that memory rows are written whole
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int row = 32 * ki + acc_row(g, lane);
+        if constexpr (TALL) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) stage[(row + i) * (C::mp + 4) + col] = acc[4 * g + i];
+        } else {
+          *reinterpret_cast<f32x4*>(stage + col * (C::cols + 4) + row) = f32x4{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+        }
+      }
+      __syncthreads();
+      const Spot o = spot<MT, !TALL, false>(tid);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = j ? o.rb : o.ra, n = extent<TALL>(M, k0, r, o.c);
+        if (n <= 0) continue;
+        const float* const in = stage + r * ((TALL ? C::mp : C::cols) + 4) + o.c;
+        float x[8];
+        load8(in, 8, x);
+        if (A.apply) {
+          const float keep = 1.f - (A.lr * M.lr_mul) * (A.wd * M.wd_mul), step = A.lr * M.lr_mul;
+          T* const w = static_cast<T*>(M.w) + place<TALL>(M.wld, k0, r, o.c);
+          float y[8];
+          load8(w, n, y);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) x[q] = __fmaf_rn(-step, x[q], y[q] * keep);
+          store8(w, n, x);
+        } else {
+          store8(static_cast<T*>(M.o) + place<TALL>(M.ld, k0, r, o.c), n, x);
+        }
+      }
+    }
+  }
+  if constexpr (!LAST) put_gram<MT>(A, M, p.index, acc2, lds, wave, lane);
+}
+
+template <typename T, int MT, bool GRAD, bool LAST>
+__device__ __forceinline__ void apply_any(const Args& A, const Mat& M, const Part& p, char* lds) {
+  if (M.tall) phase_apply<T, MT, true, GRAD, LAST>(A, M, p, lds);
+  else phase_apply<T, MT, false, GRAD, LAST>(A, M, p, lds);
+}
+template <typename T, int MT>
+__device__ __forceinline__ void gram_any(const Args& A, const Mat& M, const Part& p, char* lds) {
+  if (M.tall) phase_gram<T, MT, true>(A, M, p, lds);
+  else phase_gram<T, MT, false>(A, M, p, lds);
+}
+
+// ----------------------------------------------------------------- kernels
+
+template <typename T, int MT>
+__global__ __launch_bounds__(Cfg<MT>::threads) void stack_gram_kernel(Args A) {
+  extern __shared__ __align__(16) char lds[];
+  const Part p = A.parts[blockIdx.x];
+  gram_any<T, MT>(A, A.mats[p.mat], p, lds);
+}
+
+template <int MT>
+__global__ __launch_bounds__(Cfg<MT>::threads) void stack_solve_kernel(Args A, int first) {
+  extern __shared__ __align__(16) char lds[];
+  phase_solve<MT>(A, A.mats[first + blockIdx.x], A.run, lds);
+}
+
+template <typename T, int MT, bool GRAD, bool LAST>
+__global__ __launch_bounds__(Cfg<MT>::threads) void stack_apply_kernel(Args A) {
+  extern __shared__ __align__(16) char lds[];
+  const Part p = A.parts[blockIdx.x];
+  apply_any<T, MT, GRAD, LAST>(A, A.mats[p.mat], p, lds);
+}
+
+// A matrix a workgroup: all phases in one launch.
+template <typename T, int MT>
+__global__ __launch_bounds__(Cfg<MT>::threads) void stack_whole_kernel(Args A) {
+  extern __shared__ __align__(16) char lds[];
+  const Part p = A.parts[blockIdx.x];
+  const Mat& M = A.mats[p.mat];
+  gram_any<T, MT>(A, M, p, lds);
+  for (int run = 0; run < A.runs; ++run) {
+    __syncthreads();  // what the phase before wrote to the workspace is read by other waves
+    phase_solve<MT>(A, M, run, lds);
+    __syncthreads();
+    const bool last = run + 1 == A.runs;
+    if (run == 0 && last) apply_any<T, MT, true, true>(A, M, p, lds);
+    else if (run == 0) apply_any<T, MT, true, false>(A, M, p, lds);
+    else if (!last) phase_apply<T, MT, false, false, false>(A, M, p, lds);
+    else apply_any<T, MT, false, true>(A, M, p, lds);
+  }
+}
+
+// -------------------------------------------------------------------- host
+
+constexpr int kClasses = 3;  // mp = 32, 64, 128
+int class_of(int64_t m) { return m <= 32 ? 0 : m <= 64 ? 1 : 2; }
+int mp_of(int cls) { return 32 << cls; }
+int cols_of(int cls) { return cls == 0 ? 128 : 64; }
+
+struct Host {
+  muon_dtype dtype = MUON_BF16;
+  std::vector<muon_stack> stacks;
+  std::vector<Mat> mats;               // by class, then in the caller's order
+  std::vector<int32_t> owner;          // the stack of each
+  std::vector<int64_t> index;          // its place in it
+  std::vector<Part> parts;             // by class
+  int32_t mat_beg[kClasses + 1] = {}, part_beg[kClasses + 1] = {};
+  bool whole[kClasses] = {};
+  size_t ws_bytes = 0;
+};
+
+bool empty(const muon_stack& s) { return s.count == 0 || s.rows == 0 || s.cols == 0; }
+
+// Whether a stack's matrices are apart, and the place of all of them in memory.
+bool apart(const muon_stack& s, int64_t ld, int64_t stride, const void* p, bool write, int64_t es,
+           std::vector<muon::tensor_overlap::Interval>* iv) {
+  const int64_t span = (s.rows - 1) * ld + s.cols, all = (s.count - 1) * stride + span;
+  const bool blocks = s.count == 1 || stride >= span;
+  const bool side = s.count > 1 && !blocks && stride >= s.cols && (s.count - 1) * stride + s.cols <= ld;
+  if (!blocks && !side) return false;
+  int64_t width = all, step = 0;  // one solid run
+  if (side) width = (s.count - 1) * stride + s.cols, step = s.rows > 1 ? ld : 0;
+  else if (ld > s.cols && (s.count == 1 || stride % ld == 0) && all > s.cols) width = s.cols, step = ld;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  if (lo > UINTPTR_MAX - static_cast<uintptr_t>(all * es)) return false;
+  iv->push_back({lo, lo + static_cast<uintptr_t>(all * es), static_cast<uintptr_t>(width * es), static_cast<uintptr_t>(step * es), write});
+  return true;
+}
+
+constexpr int64_t kMaxStep = int64_t(1) << 40;  // elements of a stride
+
+muon_status validate(const muon_stack* st, int32_t n, muon_dtype dtype, const muon_stack_weight* w, int64_t* total) {
+  if (dtype != MUON_F32 && dtype != MUON_BF16) return MUON_E_DTYPE;
+  if (n < 0 || n > MUON_STACK_MAX_MATRICES) return MUON_E_SHAPE;
+  if (n > 0 && st == nullptr) return MUON_E_INVALID;
+  const int64_t es = dtype == MUON_F32 ? 4 : 2;
+  std::vector<muon::tensor_overlap::Interval> iv;
+  *total = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const muon_stack& s = st[i];
+    if (s.count < 0 || s.rows < 0 || s.cols < 0 || s.count > MUON_STACK_MAX_MATRICES || s.rows > MUON_STACK_MAX_LONG ||
+        s.cols > MUON_STACK_MAX_LONG)
+      return MUON_E_SHAPE;
+    if (empty(s)) continue;
+    if (std::min(s.rows, s.cols) > MUON_STACK_MAX_SHORT) return MUON_E_SHAPE;
+    *total += s.count;
+    if (*total > MUON_STACK_MAX_MATRICES) return MUON_E_SHAPE;
+    if (s.ld < s.cols || s.ld > kMaxStep || s.stride < 0 || s.stride > kMaxStep) return MUON_E_SHAPE;
+    if (s.grad == nullptr || s.out == nullptr) return MUON_E_INVALID;
+    for (const void* p : {s.grad, static_cast<const void*>(s.momentum), static_cast<const void*>(s.out)})
+      if (reinterpret_cast<uintptr_t>(p) % es != 0) return MUON_E_ALIGN;
+    if (!apart(s, s.ld, s.stride, s.out, true, es, &iv)) return MUON_E_INVALID;
+    if (s.momentum && !apart(s, s.ld, s.stride, s.momentum, true, es, &iv)) return MUON_E_INVALID;
+    if (s.grad != s.out && !apart(s, s.ld, s.stride, s.grad, false, es, &iv)) return MUON_E_INVALID;
+    if (w == nullptr) continue;
+    const muon_stack_weight& v = w[i];
+    if (v.weight == nullptr || !std::isfinite(v.lr_mul) || !std::isfinite(v.wd_mul)) return MUON_E_INVALID;
+    if (v.ld < s.cols || v.ld > kMaxStep || v.stride < 0 || v.stride > kMaxStep) return MUON_E_SHAPE;
+    if (reinterpret_cast<uintptr_t>(v.weight) % es != 0) return MUON_E_ALIGN;
+    if (!apart(s, v.ld, v.stride, v.weight, true, es, &iv)) return MUON_E_INVALID;
+  }
+  return muon::tensor_overlap::overlaps(iv) ? MUON_E_INVALID : MUON_OK;
+}
+
+// One launch with a matrix a workgroup where there are enough of them to fill
+// the CUs; otherwise the columns are split into parts.
+constexpr int64_t kWholeMats = 256;
+constexpr int64_t kMaxParts = 64;
+constexpr int64_t kTargetParts = 1024;
+
+muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
+  int64_t total = 0;
+  const muon_status status = validate(st, n, dtype, nullptr, &total);
+  if (status != MUON_OK) return status;
+  H->dtype = dtype;
+  H->stacks.assign(st, st + n);
+  const int64_t es = dtype == MUON_F32 ? 4 : 2;
+  size_t off = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t at = off;
+    off += (static_cast<size_t>(bytes) + 255) / 256 * 256;
+    return static_cast<int64_t>(at);
+  };
+  for (int cls = 0; cls < kClasses; ++cls) {
+    H->mat_beg[cls] = static_cast<int32_t>(H->mats.size());
+    H->part_beg[cls] = static_cast<int32_t>(H->parts.size());
+    int64_t count = 0, tiles = 0;
+    const int64_t cols = cols_of(cls), mp = mp_of(cls);
+    for (int32_t i = 0; i < n; ++i)
+      if (!empty(st[i]) && class_of(std::min(st[i].rows, st[i].cols)) == cls) {
+        count += st[i].count;
+        tiles += st[i].count * ((std::max(st[i].rows, st[i].cols) + cols - 1) / cols);
+      }
+    H->whole[cls] = count >= kWholeMats;
+    const int64_t each = std::max<int64_t>(1, (tiles + kTargetParts - 1) / kTargetParts);
+    for (int32_t i = 0; i < n; ++i) {
+      const muon_stack& s = st[i];
+      if (empty(s) || class_of(std::min(s.rows, s.cols)) != cls) continue;
+      for (int64_t t = 0; t < s.count; ++t) {
+        Mat M{};
+        M.g = static_cast<const char*>(s.grad) + t * s.stride * es;
+        M.b = s.momentum ? static_cast<char*>(s.momentum) + t * s.stride * es : nullptr;
+        M.o = static_cast<char*>(s.out) + t * s.stride * es;
+        M.ld = s.ld;
+        M.m = static_cast<int32_t>(std::min(s.rows, s.cols));
+        M.n = static_cast<int32_t>(std::max(s.rows, s.cols));
+        M.tall = s.rows > s.cols;
+        const int64_t nt = (M.n + cols - 1) / cols;
+        const int64_t per = H->whole[cls] ? nt : std::max(each, (nt + kMaxParts - 1) / kMaxParts);
+        M.parts = static_cast<int32_t>((nt + per - 1) / per);
+        M.gram_off = take(M.parts * mp * mp * 4);
+        M.exp_off = take(M.parts * 4);
+        M.rec_off = take(8);
+        M.p_off = take(mp * mp * 4);
+        M.x_off = take(nt * cols * mp * 4);
+        for (int32_t p = 0; p < M.parts; ++p)
+          H->parts.push_back({static_cast<int32_t>(H->mats.size()), static_cast<int32_t>(p * per),
+                              static_cast<int32_t>(std::min(nt, (p + 1) * per)), p});
+        H->mats.push_back(M);
+        H->owner.push_back(i);
+        H->index.push_back(t);
+      }
+    }
+  }
+  H->mat_beg[kClasses] = static_cast<int32_t>(H->mats.size());
+  H->part_beg[kClasses] = static_cast<int32_t>(H->parts.size());
+  H->ws_bytes = off;
+  return MUON_OK;
+}
+
+// The largest number of steps from one Gram matrix. Errors of A grow by at
+// most the slope of lambda -> lambda q(lambda)^2 in each update of A; the
+// slope and |q| are taken over the values that 4097 points of X0's range pass
+// through. P's entries have to stay in fp16's range, too.
+int run_length(const muon_config& c, muon_dtype dtype) {
+  double slope = 0.0, top = 0.0;
+  for (int i = 0; i <= 4096; ++i) {
+    double x = i / 4096.0;
+    for (int32_t t = 0; t < c.steps; ++t) {
+      const double l = x * x, q = c.a + l * (c.b + c.c * l), dq = c.b + 2.0 * c.c * l;
+      slope = std::max(slope, std::fabs(q * q + 2.0 * l * q * dq));
+      top = std::max(top, std::fabs(q));
+      x *= q;
+    }
+  }
+  const double limit = dtype == MUON_F32 ? 8.0 : 256.0;
+  int s = 1;
+  double grown = slope, size = top * top;
+  while (s < c.steps && grown <= limit && size <= 4096.0) {
+    ++s;
+    grown *= slope;
+    size *= top;
+  }
+  return s;
+}
+
+}  // namespace muon_stack_ns
+
+struct muon_stack_plan_s {
+  muon_stack_ns::Host host;
+  int device = -1;
+  void* dmem = nullptr;
+  const muon_stack_ns::Mat* d_mats = nullptr;
+  const muon_stack_ns::Part* d_parts = nullptr;
+  bool has_weights = false;
+  const float* gscale = nullptr;
+};
+
+namespace {
+
+using namespace muon_stack_ns;
+
+template <typename K>
+muon_status go(K kernel, unsigned grid, int threads, int lds, hipStream_t s, const Args& a) {
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(unsigned(threads)), size_t(lds), s, a);
+  return hipGetLastError() == hipSuccess ? MUON_OK : MUON_E_LAUNCH;
+}
+
+template <typename T, int MT>
+muon_status run_class(const muon_stack_plan_s* p, int cls, Args a, hipStream_t s) {
+  typedef Cfg<MT> C;
+  const Host& H = p->host;
+  const int mats = H.mat_beg[cls + 1] - H.mat_beg[cls];
+  if (mats == 0) return MUON_OK;
+  const unsigned parts = unsigned(H.part_beg[cls + 1] - H.part_beg[cls]);
+  a.parts = p->d_parts + H.part_beg[cls];
+  if (H.whole[cls]) return go(stack_whole_kernel<T, MT>, parts, C::threads, C::lds_whole, s, a);
+  muon_status st = go(stack_gram_kernel<T, MT>, parts, C::threads, C::lds_tile, s, a);
+  for (int run = 0; run < a.runs && st == MUON_OK; ++run) {
+    a.run = run;
+    hipLaunchKernelGGL(stack_solve_kernel<MT>, dim3(unsigned(mats)), dim3(C::threads), C::lds_solve, s, a, H.mat_beg[cls]);
+    if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
+    const bool last = run + 1 == a.runs;
+    if (run == 0)
+      st = last ? go(stack_apply_kernel<T, MT, true, true>, parts, C::threads, C::lds_tile, s, a)
+                : go(stack_apply_kernel<T, MT, true, false>, parts, C::threads, C::lds_tile, s, a);
+    else
+      st = last ? go(stack_apply_kernel<T, MT, false, true>, parts, C::threads, C::lds_tile, s, a)
+                : go(stack_apply_kernel<T, MT, false, false>, parts, C::threads, C::lds_tile, s, a);
+  }
+  return st;
+}
+
+template <typename T>
+muon_status run_all(const muon_stack_plan_s* p, const Args& a, hipStream_t s) {
+  muon_status st = run_class<T, 1>(p, 0, a, s);
+  if (st == MUON_OK) st = run_class<T, 2>(p, 1, a, s);
+  if (st == MUON_OK) st = run_class<T, 4>(p, 2, a, s);
+  return st;
+}
+
+muon_status step(muon_stack_plan_s* p, const muon_config* cfg, const muon_apply* ap, void* ws, size_t bytes, void* stream) {
+  if (p == nullptr) return MUON_E_INVALID;
+  const Host& H = p->host;
+  // the range check of the 16-bit operands holds for both dtypes
+  muon_status st = muon::validate_config(cfg, MUON_BF16);
+  if (st != MUON_OK) return st;
+  if (H.mats.empty()) return MUON_OK;
+  if (ap != nullptr && !p->has_weights) return MUON_E_INVALID;
+  if (ws == nullptr || bytes < H.ws_bytes || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MUON_E_WORKSPACE;
+  if (cfg->momentum != 0.f)
+    for (const Mat& M : H.mats)
+      if (M.b == nullptr) return MUON_E_INVALID;
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess || dev != p->device) return MUON_E_DEVICE;
+  Args a{};
+  a.mats = p->d_mats;
+  a.ws = static_cast<char*>(ws);
+  a.gscale = p->gscale;
+  a.a = cfg->a;
+  a.b = cfg->b;
+  a.c = cfg->c;
+  a.mu = cfg->momentum;
+  a.eps = cfg->eps;
+  a.nesterov = cfg->nesterov;
+  a.use_mom = cfg->momentum != 0.f;
+  a.apply = ap != nullptr;
+  if (ap != nullptr) {
+    a.lr = ap->lr;
+    a.wd = ap->wd;
+  }
+  const int len = run_length(*cfg, H.dtype);
+  a.runs = std::max(1, (cfg->steps + len - 1) / len);
+  a.each = cfg->steps / a.runs;
+  a.more = cfg->steps % a.runs;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return H.dtype == MUON_F32 ? run_all<float>(p, a, s) : run_all<uint16_t>(p, a, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_stack_workspace_bytes(const muon_stack* stacks, int32_t n, muon_dtype dtype, size_t* bytes) {
+  if (bytes == nullptr) return MUON_E_INVALID;
+  try {
+    Host H;
+    const muon_status st = build(stacks, n, dtype, &H);
+    if (st == MUON_OK) *bytes = H.ws_bytes;
+    return st;
+  } catch (...) {
+    return MUON_E_ALLOC;
+  }
+}
+
+muon_status muon_stack_plan_create(const muon_stack* stacks, int32_t n, muon_dtype dtype, muon_stack_plan** plan) {
+  if (plan == nullptr) return MUON_E_INVALID;
+  *plan = nullptr;
+  muon_stack_plan_s* p = nullptr;
+  try {
+    p = new muon_stack_plan_s();
+    muon_status st = build(stacks, n, dtype, &p->host);
+    if (st == MUON_OK) {
+      hipDeviceProp_t prop;
+      if (hipGetDevice(&p->device) != hipSuccess || hipGetDeviceProperties(&prop, p->device) != hipSuccess ||
+          std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
+        st = MUON_E_DEVICE;
+    }
+    if (st != MUON_OK) {
+      delete p;
+      return st;
+    }
+    const Host& H = p->host;
+    const size_t mb = (sizeof(Mat) * H.mats.size() + 255) / 256 * 256;
+    std::vector<char> h(std::max<size_t>(256, mb + sizeof(Part) * H.parts.size()), 0);
+    if (!H.mats.empty()) std::memcpy(h.data(), H.mats.data(), sizeof(Mat) * H.mats.size());
+    if (!H.parts.empty()) std::memcpy(h.data() + mb, H.parts.data(), sizeof(Part) * H.parts.size());
+    if (hipMalloc(&p->dmem, h.size()) != hipSuccess) {
+      (void)hipGetLastError();
+      delete p;
+      return MUON_E_ALLOC;
+    }
+    if (hipMemcpy(p->dmem, h.data(), h.size(), hipMemcpyHostToDevice) != hipSuccess) {
+      (void)hipGetLastError();
+      (void)hipFree(p->dmem);
+      delete p;
+      return MUON_E_DEVICE;
+    }
+    p->d_mats = static_cast<const Mat*>(p->dmem);
+    p->d_parts = reinterpret_cast<const Part*>(static_cast<char*>(p->dmem) + mb);
+    *plan = p;
+    return MUON_OK;
+  } catch (...) {
+    if (p != nullptr && p->dmem != nullptr) (void)hipFree(p->dmem);
+    delete p;
+    return MUON_E_ALLOC;
+  }
+}
+
+muon_status muon_stack_plan_step(muon_stack_plan* plan, const muon_config* cfg, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  return step(plan, cfg, nullptr, workspace, workspace_bytes, stream);
+}
+
+muon_status muon_stack_plan_set_weights(muon_stack_plan* plan, const muon_stack_weight* w, int32_t n) {
+  if (plan == nullptr) return MUON_E_INVALID;
+  Host& H = plan->host;
+  if (n != static_cast<int32_t>(H.stacks.size())) return MUON_E_SHAPE;
+  if (n > 0 && w == nullptr) return MUON_E_INVALID;
+  try {
+    int64_t total = 0;
+    muon_status st = validate(H.stacks.data(), n, H.dtype, w, &total);
+    if (st != MUON_OK) return st;
+    std::vector<Mat> mats = H.mats;
+    const int64_t es = H.dtype == MUON_F32 ? 4 : 2;
+    for (size_t i = 0; i < mats.size(); ++i) {
+      const muon_stack_weight& v = w[H.owner[i]];
+      mats[i].w = static_cast<char*>(v.weight) + H.index[i] * v.stride * es;
+      mats[i].wld = v.ld;
+      mats[i].lr_mul = v.lr_mul;
+      mats[i].wd_mul = v.wd_mul;
+    }
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess || dev != plan->device) return MUON_E_DEVICE;
+    if (hipDeviceSynchronize() != hipSuccess) return MUON_E_DEVICE;
+    if (!mats.empty() && hipMemcpy(plan->dmem, mats.data(), sizeof(Mat) * mats.size(), hipMemcpyHostToDevice) != hipSuccess)
+      return MUON_E_DEVICE;
+    H.mats = std::move(mats);
+    plan->has_weights = true;
+    return MUON_OK;
+  } catch (...) {
+    return MUON_E_ALLOC;
+  }
+}
+
+muon_status muon_stack_plan_step_apply(muon_stack_plan* plan, const muon_config* cfg, const muon_apply* ap, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  const muon_status st = muon::validate_apply(ap);
+  if (st != MUON_OK) return st;
+  return step(plan, cfg, ap, workspace, workspace_bytes, stream);
+}
+
+muon_status muon_stack_plan_set_grad_scale(muon_stack_plan* plan, const float* scale) {
+  if (plan == nullptr) return MUON_E_INVALID;
+  if (reinterpret_cast<uintptr_t>(scale) % 4 != 0) return MUON_E_ALIGN;
+  plan->gscale = scale;
+  return MUON_OK;
+}
+
+void muon_stack_plan_destroy(muon_stack_plan* plan) {
+  if (!plan) return;
+  (void)hipDeviceSynchronize();
+  if (plan->dmem) (void)hipFree(plan->dmem);
+  delete plan;
+}
+
+}  // extern "C"

@@ -1,0 +1,125 @@
+"""The Muon step on stacks of short matrices (include/muon_stack.h) without a
+GPU: what is refused before any device call, workspace sizes, and the
+binding's views."""
+import ctypes
+
+import pytest
+import torch
+
+import muon_newton_schulz_04_amd as mu
+
+OK, INVALID, DTYPE, SHAPE, ALIGN = 0, 1, 2, 3, 4
+B = 1 << 44
+F32, BF16 = mu.MUON_F32, mu.MUON_BF16
+FIELDS = ("count", "rows", "cols", "ld", "stride", "grad", "momentum", "out")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return mu.load_library()
+
+
+def stack(**kw):
+    f = dict(count=3, rows=8, cols=40, ld=40, stride=320, grad=B, momentum=2 * B, out=3 * B)
+    f.update(kw)
+    return tuple(f[k] for k in FIELDS)
+
+
+def status(lib, stacks, dtype=BF16, n=None):
+    arr = (mu.MuonStack * max(1, len(stacks)))()
+    for i, s in enumerate(stacks):
+        arr[i] = mu.MuonStack(*s)
+    n = len(stacks) if n is None else n
+    out = ctypes.c_size_t(0)
+    code = lib.muon_stack_workspace_bytes(arr, n, dtype, ctypes.byref(out))
+    h = ctypes.c_void_p(5)
+    made = lib.muon_stack_plan_create(arr, n, dtype, ctypes.byref(h))
+    if code != OK:
+        assert made == code and h.value is None
+    elif not torch.cuda.is_available():
+        assert made == 6 and h.value is None
+    else:
+        lib.muon_stack_plan_destroy(h)
+    return code
+
+
+@pytest.mark.parametrize("want,kw", [
+    (OK, {}), (OK, dict(momentum=None)), (OK, dict(grad=3 * B)), (OK, dict(count=0)), (OK, dict(rows=0)), (OK, dict(cols=0, grad=None, out=None)),
+    (OK, dict(rows=128, cols=128, ld=128, stride=128 * 128)), (SHAPE, dict(rows=129, cols=129, ld=129, stride=129 * 129)),
+    (OK, dict(rows=65536, cols=128, ld=128, stride=65536 * 128)), (SHAPE, dict(rows=65537, cols=8, ld=8, stride=65537 * 8)),
+    (OK, dict(rows=1, cols=65536, ld=65536, stride=65536)), (SHAPE, dict(cols=65537, ld=65537, stride=8 * 65537)),
+    (SHAPE, dict(count=-1)), (SHAPE, dict(rows=-1)), (SHAPE, dict(cols=-1)), (SHAPE, dict(count=65537)), (SHAPE, dict(ld=39)),
+    (SHAPE, dict(stride=-1)), (SHAPE, dict(ld=(1 << 40) + 1)), (SHAPE, dict(stride=(1 << 40) + 1)),
+    (OK, dict(stride=(1 << 30))), (OK, dict(ld=41, stride=7 * 41 + 40)), (INVALID, dict(stride=319)), (INVALID, dict(stride=0)), (OK, dict(count=1, stride=0)),
+    (OK, dict(ld=120, stride=40)), (INVALID, dict(ld=119, stride=40)), (INVALID, dict(ld=120, stride=39)), (OK, dict(ld=130, stride=45)),
+    (INVALID, dict(grad=None)), (INVALID, dict(out=None)), (ALIGN, dict(grad=B + 1)), (ALIGN, dict(momentum=2 * B + 1)), (ALIGN, dict(out=3 * B + 1)),
+    (INVALID, dict(out=B + 2)), (INVALID, dict(momentum=B)), (INVALID, dict(momentum=3 * B + 3 * 640 - 2)), (OK, dict(momentum=3 * B + 3 * 640)),
+    (INVALID, dict(out=(1 << 64) - 64)),
+])
+def test_one_stack(lib, want, kw):
+    assert status(lib, [stack(**kw)]) == want
+
+
+def test_types_and_lists(lib):
+    assert status(lib, [stack()], dtype=2) == DTYPE
+    assert status(lib, [stack(grad=B + 2)], dtype=F32) == ALIGN
+    assert status(lib, [], n=0) == OK
+    assert status(lib, [stack()], n=-1) == SHAPE
+    assert status(lib, [stack(), stack()]) == INVALID                               # the same out twice
+    apart = stack(grad=B, momentum=5 * B, out=6 * B)
+    assert status(lib, [stack(), apart]) == OK                                      # grads may be shared
+    assert status(lib, [stack(count=40000), stack(count=40000, grad=4 * B, momentum=5 * B, out=6 * B)]) == SHAPE
+    assert lib.muon_stack_workspace_bytes(None, 1, BF16, ctypes.byref(ctypes.c_size_t())) == INVALID
+    assert lib.muon_stack_workspace_bytes(None, 0, BF16, None) == INVALID
+    assert lib.muon_stack_plan_create(None, 1, BF16, ctypes.byref(ctypes.c_void_p())) == INVALID
+    assert lib.muon_stack_plan_create(None, 0, BF16, None) == INVALID
+    n = ctypes.c_void_p(None)
+    assert lib.muon_stack_plan_step(n, None, None, 0, None) == INVALID
+    assert lib.muon_stack_plan_step_apply(n, None, None, None, 0, None) == INVALID
+    assert lib.muon_stack_plan_set_weights(n, None, 0) == INVALID
+    assert lib.muon_stack_plan_set_grad_scale(n, None) == INVALID
+    lib.muon_stack_plan_destroy(n)
+
+
+def test_column_slices_of_one_matrix(lib):
+    """q, k and v as column blocks of one [d, 3 heads 64] matrix: spans run into each other, columns do not."""
+    def part(j, heads=4, side=64, d=100):
+        off = 2 * j * heads * side
+        return stack(count=heads, rows=d, cols=side, ld=3 * heads * side, stride=side, grad=B + off, momentum=2 * B + off, out=3 * B + off)
+    assert status(lib, [part(0), part(1), part(2)]) == OK
+    assert status(lib, [part(0), part(1), part(1)]) == INVALID
+    off = part(1)
+    assert status(lib, [part(0), (*off[:5], off[5] - 2, off[6] - 2, off[7] - 2)]) == INVALID  # one column into the neighbour
+
+
+def test_workspace_does_not_depend_on_pointers(lib):
+    shapes = [torch.empty(36, 64, 768, dtype=torch.bfloat16), torch.empty(12, 768, 64, dtype=torch.bfloat16)]
+    size = mu.muon_stack_workspace_bytes(shapes)
+    # X between runs (fp32), partial Gram matrices, P
+    assert 48 * 64 * 768 * 4 <= size <= 48 * (64 * 768 * 4 + 64 * 64 * 4 * (12 + 1) + 4 * 256)
+    assert mu.muon_stack_workspace_bytes([]) == 0
+    assert mu.muon_stack_workspace_bytes([torch.empty(0, 4, 4)]) == 0
+
+
+def test_binding_layouts():
+    w = torch.empty(768, 3 * 768)
+    assert mu._stack_layout(w.view(12, 64, 3 * 768)) == (12, 64, 2304, 2304, 64 * 2304)
+    assert mu._stack_layout(w.view(768, 36, 64).transpose(0, 1)) == (36, 768, 64, 2304, 64)
+    assert mu._stack_layout(w[:, :100]) == (1, 768, 100, 2304, 0)
+    assert mu._stack_layout(torch.empty(5, 1, 9)) == (5, 1, 9, 9, 9)
+    for bad in (torch.empty(3), torch.empty(2, 2, 2, 2), w.t(), torch.empty(4, 6, 8).transpose(1, 2)):
+        with pytest.raises(ValueError):
+            mu._stack_layout(bad)
+    a, b = torch.empty(2, 4, 8), torch.empty(2, 4, 16)[:, :, :8]
+    with pytest.raises(ValueError):
+        mu.muon_stack_workspace_bytes([a], [b], [a])                 # other strides
+    with pytest.raises(ValueError):
+        mu.muon_stack_workspace_bytes([a], [a[:1]], [a])
+    with pytest.raises(TypeError):
+        mu.muon_stack_workspace_bytes([a], [a.bfloat16()], [a])
+    with pytest.raises(TypeError):
+        mu.muon_stack_workspace_bytes([a.half()])
+    with pytest.raises(ValueError):
+        mu.muon_stack_workspace_bytes([a], None, [])
+    with pytest.raises(ValueError):
+        mu.StackPlan([a], None, [a])                                 # host memory
