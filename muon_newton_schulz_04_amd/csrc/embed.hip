@@ -157,39 +157,50 @@ struct LookArgs {
   float scale;
 };
 
+// A row's last vector starts at cols - 8 where the row is no whole number of
+// them: some elements are written twice, with the same value. Loads are
+// without branches, so that all of a thread's are in flight at once: a token
+// outside the vocabulary loads row 0 and stores zeros.
 template <typename E, typename O, typename I>
 __global__ __launch_bounds__(kThreads) void embed_lookup_kernel(LookArgs A) {
   const int64_t first = int64_t(blockIdx.x) * A.per;
   const int64_t left = A.n - first;
   const uint32_t vpr = static_cast<uint32_t>(A.vpr);
   const uint32_t nv = vpr * static_cast<uint32_t>(left < A.per ? left : A.per);
-  const E* table = static_cast<const E*>(A.table);
-  O* out = static_cast<O*>(A.out);
+  const E* const table = static_cast<const E*>(A.table);
+  O* const out = static_cast<O*>(A.out) + first * A.out_ld;
+  const I* const tokens = static_cast<const I*>(A.tokens) + first;
+  if (A.cols < kLookVec) {  // narrow rows: one vector each
+    for (uint32_t k = threadIdx.x; k < nv; k += kThreads) {
+      const int32_t t = token(tokens, k, A.vocab);
+      float x[8];
+      load8(table + int64_t(max(t, 0)) * A.ld, A.cols, x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = t >= 0 ? x[q] * A.scale : 0.f;
+      store8(out + k * A.out_ld, A.cols, x);
+    }
+    return;
+  }
   for (uint32_t k0 = threadIdx.x; k0 < nv; k0 += kThreads * kLookRuns) {
     float x[kLookRuns][8];
+    int32_t t[kLookRuns];
+    int64_t at[kLookRuns];
+    int c[kLookRuns];
 #pragma unroll
     for (int j = 0; j < kLookRuns; ++j) {
-      const uint32_t k = k0 + j * kThreads;
-      if (k >= nv) break;
-      const uint32_t r = div_by(k, vpr, A.magic);
-      const int c = static_cast<int>(k - r * vpr) * kLookVec;
-      const int32_t t = token(static_cast<const I*>(A.tokens), first + r, A.vocab);
-      if (t >= 0) {
-        load8(table + int64_t(t) * A.ld + c, A.cols - c, x[j]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) x[j][q] = 0.f;
-      }
+      const uint32_t k = min(k0 + j * kThreads, nv - 1), r = div_by(k, vpr, A.magic);
+      c[j] = min(static_cast<int>(k - r * vpr) * kLookVec, A.cols - kLookVec);
+      at[j] = int64_t(r) * A.out_ld + c[j];
+      t[j] = token(tokens, r, A.vocab);
     }
 #pragma unroll
-    for (int j = 0; j < kLookRuns; ++j) {
-      const uint32_t k = k0 + j * kThreads;
-      if (k >= nv) break;
-      const uint32_t r = div_by(k, vpr, A.magic);
-      const int c = static_cast<int>(k - r * vpr) * kLookVec;
+    for (int j = 0; j < kLookRuns; ++j) load8(table + int64_t(max(t[j], 0)) * A.ld + c[j], 8, x[j]);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[j][q] *= A.scale;
-      store8(out + (first + r) * A.out_ld + c, A.cols - c, x[j]);
+    for (int j = 0; j < kLookRuns; ++j) {
+      if (k0 + j * kThreads >= nv) break;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[j][q] = t[j] >= 0 ? x[j][q] * A.scale : 0.f;
+      store8(out + at[j], 8, x[j]);
     }
   }
 }
@@ -204,6 +215,7 @@ struct SortArgs {
   void* grad;         // dense form: rows without a token are cleared here (nullptr: not)
   int64_t grad_ld;
   int32_t n, vocab, cols, range;
+  int32_t bits;       // of a token's place in the range
   int32_t grad_f32;
 };
 
@@ -302,17 +314,17 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(SortArgs A) {
       for (int u = 0; u < U; ++u) {
         const int k = t[u] - lo;
         const bool in = k >= 0 && k < nk;
-        uint64_t todo = __ballot(in);
-        while (todo) {  // one of the wave's tokens at a time, its lanes in order
-          const int lead = __builtin_ctzll(todo);
-          const int key = __builtin_amdgcn_readlane(k, lead);
-          const uint64_t same = __ballot(in && k == key);
-          if (in && k == key) {
-            const int at = mine[key];
-            A.recs[at + lanes_below(same, lane)] = {i0 + u * 64 + lane, key + lo, slot[key], end[key]};
-            if (lane == lead) mine[key] = at + __popcll(same);
-          }
-          todo &= ~same;
+        uint64_t same = __ballot(in);
+        if (same == 0) continue;
+        for (int b = 0; b < A.bits; ++b) {  // the lanes with this lane's token
+          const bool set = (k >> b) & 1;
+          const uint64_t with = __ballot(set);
+          same &= set ? with : ~with;
+        }
+        if (in) {
+          const int at = mine[k], before = lanes_below(same, lane);
+          A.recs[at + before] = {i0 + u * 64 + lane, k + lo, slot[k], end[k]};
+          if (before == 0) mine[k] = at + __popcll(same);
         }
       }
     }
@@ -356,12 +368,6 @@ struct SumArgs {
   float scale;
 };
 
-// Where a wave is: its chunk's records and its columns.
-struct Place {
-  int c0, len;   // first record, number of records
-  int col, nc;   // the lane's first column and how many of its four exist
-};
-
 __device__ __forceinline__ int wave_sum(int x) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
@@ -375,9 +381,21 @@ __device__ __forceinline__ int distinct_in(const int32_t* distinct, int b0, int 
   return __builtin_amdgcn_readfirstlane(wave_sum(s));
 }
 
+// A lane has columns [col, col + 4); its loads are those of [from, from + 4),
+// which differs where the row ends (rows of under four columns aside).
+struct Cols {
+  int col, nc;  // nc: how many of them exist, at most zero for none
+  int from;
+};
+__device__ __forceinline__ Cols cols_of(int slab, int lane, int cols) {
+  const int col = slab * kSlab + lane * kVec;
+  return {col, cols - col, cols >= kVec ? min(col, cols - kVec) : 0};
+}
+
 // A finished sum goes out. row: the token, or its place among the rows.
 template <typename G, int MODE>
-__device__ __forceinline__ void put(const SumArgs& A, int64_t row, int col, int nc, float (&x)[kVec]) {
+__device__ __forceinline__ void put(const SumArgs& A, int64_t row, const Cols& l, float (&x)[kVec]) {
+  const int col = l.col, nc = l.nc;
   if (nc <= 0) return;
   G* const p = static_cast<G*>(A.grad) + row * A.grad_ld + col;
   if constexpr (MODE == kAdd) {
@@ -407,7 +425,7 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(SumArgs A) {
   if (c0 >= live) return;
   const int len = static_cast<int>(min(int64_t(A.chunk), live - c0));
   const int c1 = static_cast<int>(c0) + len;
-  const int col = slab * kSlab + lane * kVec, nc = A.cols - col;
+  const Cols l = cols_of(slab, lane, A.cols);
   const Rec mine = lane < len ? A.recs[c0 + lane] : Rec{0, -1, 0, 0};  // a chunk has at most 64 records
   const int prev = c0 > 0 ? __builtin_amdgcn_readfirstlane(A.recs[c0 - 1].key) : -1;
   int key = __builtin_amdgcn_readfirstlane(mine.key);
@@ -430,24 +448,32 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(SumArgs A) {
       }
       row = base + __builtin_amdgcn_readlane(mine.slot, last);
     }
+    // the lane's own columns first: a row's last lane has loaded those before them, too
+    const int shift = l.col - l.from;
+    float x[kVec];
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) x[q] = shift == 1 && q < 3 ? acc[q + 1] : shift == 2 && q < 2 ? acc[q + 2] : shift == 3 && q < 1 ? acc[3] : acc[q];
     if (part != nullptr) {
-      if (nc > 0) *reinterpret_cast<float4*>(part + chunk * A.ld_part + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (l.nc > 0) *reinterpret_cast<float4*>(part + chunk * A.ld_part + l.col) = make_float4(x[0], x[1], x[2], x[3]);
     } else {
-      put<G, MODE>(A, row, col, nc, acc);
+      put<G, MODE>(A, row, l, x);
       if (MODE == kRows && slab == 0 && lane == 0) A.rows[row] = key;
     }
   };
 
-  const D* const dout = static_cast<const D*>(A.dout) + col;
+  const D* const dout = static_cast<const D*>(A.dout) + l.from;
   constexpr int U = 8;  // rows in flight
   for (int i0 = 0; i0 < len; i0 += U) {
     float x[U][kVec];
+    // no branch around a load: they all go out before the first is waited for
+    if (A.cols >= kVec) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i0 + u < len && nc > 0) {
-        const int64_t pos = __builtin_amdgcn_readlane(mine.pos, i0 + u);
-        load4_of(dout + pos * A.dout_ld, nc, x[u]);
-      }
+      for (int u = 0; u < U; ++u)
+        muon_adam::load4<false>(dout + int64_t(__builtin_amdgcn_readlane(mine.pos, min(i0 + u, len - 1))) * A.dout_ld, x[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        load4_of(dout + int64_t(__builtin_amdgcn_readlane(mine.pos, min(i0 + u, len - 1))) * A.dout_ld, A.cols, x[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -483,20 +509,20 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs A) {
   if (r.end <= c1) return;
   // began before this chunk: another block's
   if (c0 > 0 && A.recs[c0 - 1].key == r.key) return;
-  const int col = slab * kSlab + lane * kVec, nc = A.cols - col;
+  const Cols l = cols_of(slab, lane, A.cols);
   const int64_t stop = (r.end - 1) / A.chunk;  // the last chunk it reaches
   float acc[kVec] = {};
   constexpr int W = kThreads / 64, U = 8;
-  if (nc > 0) {
+  if (l.nc > 0) {
     if (wave == 0) {
-      const float4 t = *reinterpret_cast<const float4*>(A.tail + chunk * A.ld_part + col);
+      const float4 t = *reinterpret_cast<const float4*>(A.tail + chunk * A.ld_part + l.col);
       acc[0] = t.x, acc[1] = t.y, acc[2] = t.z, acc[3] = t.w;
     }
     for (int64_t j0 = chunk + 1 + wave; j0 <= stop; j0 += W * U) {
       float4 x[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        x[u] = j0 + u * W <= stop ? *reinterpret_cast<const float4*>(A.head + (j0 + u * W) * A.ld_part + col)
+        x[u] = j0 + u * W <= stop ? *reinterpret_cast<const float4*>(A.head + (j0 + u * W) * A.ld_part + l.col)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int u = 0; u < U; ++u) acc[0] += x[u].x, acc[1] += x[u].y, acc[2] += x[u].z, acc[3] += x[u].w;
@@ -515,7 +541,7 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs A) {
     row = distinct_in(A.distinct, 0, r.key / A.range, lane) + r.slot;
     if (slab == 0 && lane == 0) A.rows[row] = r.key;
   }
-  put<G, MODE>(A, row, col, nc, acc);
+  put<G, MODE>(A, row, l, acc);
 }
 
 // ------------------------------------------------------------ Adam on rows
@@ -725,6 +751,7 @@ muon_status run_gradient(muon_embed_plan* p, const muon_embed_tokens* tokens, co
   a.vocab = static_cast<int32_t>(p->t.vocab);
   a.cols = static_cast<int32_t>(p->t.cols);
   a.range = z.range;
+  while ((1 << a.bits) < z.range) ++a.bits;
   const size_t lds = size_t(kSortWaves + 2) * size_t(z.range) * sizeof(int32_t);
   if (tokens->wide)
     hipLaunchKernelGGL(embed_sort_kernel<int64_t>, dim3(unsigned(z.blocks)), dim3(kSortThreads), lds, s, a);
