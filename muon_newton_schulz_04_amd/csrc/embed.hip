@@ -5,11 +5,12 @@
 //
 // All of it is bound by HBM, or by the launches for small batches. The
 // gradient takes three launches:
-//  - sort: block b owns R consecutive vocabulary entries. It reads all n tokens
-//    twice, counts its own and those below its range (which gives the place of
+//  - sort: a block owns R consecutive vocabulary entries in one segment of the
+//    batch. It reads all n tokens, counts those of its range before, in and
+//    behind its segment and those below its range (which gives the place of
 //    its first token without any other block's word), and writes its tokens'
 //    records ordered by token, then by position. No atomics across blocks, no
-//    dependence on how tokens are spread, any n.
+//    sum that depends on how tokens are spread, any n.
 //  - sum: the sorted records are cut into chunks of equal length, whatever
 //    tokens they hold. A wave takes the columns of a slab through one chunk and
 //    writes the sum of each token that lies within it; a token that crosses a
@@ -37,7 +38,8 @@ constexpr int kLookRuns = 4;       // such vectors per thread, kThreads apart
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxRange = 2048;    // vocabulary entries of a sort block: 16 waves' counters fill 128 KB of LDS
-constexpr int kSortBlocks = 256;   // sort blocks while the range allows: one per CU
+constexpr int kSortBlocks = 256;   // sort blocks: one per CU
+constexpr int kSegment = 4096;     // tokens of a segment of the batch, at least
 constexpr int kSlab = 64 * kVec;   // columns of a wave in the sum
 constexpr int64_t kSumWaves = 4096;  // waves of the sum aimed at: 16 on each CU
 constexpr int64_t kMaxWaves = 1 << 23;  // of one launch (the join has a block for each)
@@ -46,7 +48,7 @@ constexpr int64_t kMaxWaves = 1 << 23;  // of one launch (the join has a block f
 struct Rec {
   int32_t pos;   // its position in the batch
   int32_t key;   // the token
-  int32_t slot;  // the token's rank among the distinct tokens of its sort block
+  int32_t slot;  // the token's rank among the distinct tokens of its range
   int32_t end;   // index behind the token's last record
 };
 
@@ -210,12 +212,13 @@ __global__ __launch_bounds__(kThreads) void embed_lookup_kernel(LookArgs A) {
 struct SortArgs {
   const void* tokens;
   Rec* recs;
-  int32_t* distinct;  // per block: distinct tokens of its range
+  int32_t* distinct;  // per range: its distinct tokens
   int32_t* live;      // tokens inside the vocabulary
   void* grad;         // dense form: rows without a token are cleared here (nullptr: not)
   int64_t grad_ld;
   int32_t n, vocab, cols, range;
-  int32_t bits;       // of a token's place in the range
+  int32_t segments, run;  // of the batch; tokens of a wave in its block's segment, a multiple of 64
+  int32_t bits;           // of a token's place in the range
   int32_t grad_f32;
 };
 
@@ -223,42 +226,52 @@ __device__ __forceinline__ int lanes_below(uint64_t mask, int lane) {
   return __popcll(mask & ((uint64_t(1) << lane) - 1));
 }
 
+// The lookups of a batch's frequent tokens fall into few ranges, whose blocks
+// set the time: with one segment of the batch (256 ranges, one a CU) the
+// gradient of 32768 Zipf-distributed tokens of 50257 spent 47 us here.
 template <typename I>
 __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(SortArgs A) {
   extern __shared__ int32_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int lo = blockIdx.x * A.range;
+  const int part = blockIdx.x / A.segments, segment = blockIdx.x - part * A.segments;
+  const int lo = part * A.range;
   const int nk = min(A.range, A.vocab - lo);
   int32_t* const cnt = lds;                       // [wave][key]: the wave's tokens, then where its next one goes
-  int32_t* const end = lds + kSortWaves * nk;     // [key]
-  int32_t* const slot = end + nk;                 // [key]
+  int32_t* const before = lds + kSortWaves * nk;  // [key]: tokens of earlier segments; then the end of the token's records
+  int32_t* const behind = before + nk;            // [key]: of later segments; then the token's rank in the range
   __shared__ int32_t below[kSortWaves];
   __shared__ int64_t scan[kSortWaves];
-  for (int i = tid; i < kSortWaves * nk; i += kSortThreads) cnt[i] = 0;
+  for (int i = tid; i < (kSortWaves + 2) * nk; i += kSortThreads) lds[i] = 0;
   __syncthreads();
 
-  // A wave's tokens are one run of the batch, so that (wave, lane, time) order is position order.
   const I* const tokens = static_cast<const I*>(A.tokens);
-  const int each = (A.n + kSortThreads - 1) / kSortThreads * 64;
-  const int beg = min(A.n, wave * each), fin = min(A.n, beg + each);
-  volatile int32_t* const mine = cnt + wave * nk;  // read by lanes other than the one that wrote it
   constexpr int U = 8;  // loads in flight
-  int under = 0;
-  for (int i0 = beg; i0 < fin; i0 += 64 * U) {
-    int32_t t[U];
+  const int64_t size = int64_t(A.run) * kSortWaves;  // of a segment
+  const int64_t seg0 = segment * size, seg1 = seg0 + size;
+  {
+    // every wave a run of the whole batch; a step of 64 tokens lies in one wave's run of one segment
+    const int64_t each = (int64_t(A.n) + kSortThreads - 1) / kSortThreads * 64;
+    const int64_t beg = wave * each, fin = min(int64_t(A.n), beg + each);
+    int under = 0;
+    for (int64_t i0 = beg; i0 < fin; i0 += 64 * U) {
+      int32_t t[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * 64 + lane;
-      t[u] = i < fin ? token(tokens, i, A.vocab) : -1;
-    }
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = i0 + u * 64 + lane;
+        t[u] = token(tokens, min(i, int64_t(A.n) - 1), A.vocab);
+        if (i >= fin) t[u] = -1;
+      }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      under += __popcll(__ballot(t[u] >= 0 && t[u] < lo));
-      const int k = t[u] - lo;
-      if (k >= 0 && k < nk) atomicAdd(cnt + wave * nk + k, 1);
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = i0 + u * 64;
+        int32_t* const to = i < seg0 ? before : i >= seg1 ? behind : cnt + static_cast<int>((i - seg0) / A.run) * nk;
+        under += __popcll(__ballot(t[u] >= 0 && t[u] < lo));
+        const int k = t[u] - lo;
+        if (k >= 0 && k < nk) atomicAdd(to + k, 1);
+      }
     }
+    if (lane == 0) below[wave] = under;
   }
-  if (lane == 0) below[wave] = under;
   __syncthreads();
 
   // Starts of the tokens: a scan over the keys of (count, is there any) in one 64-bit sum.
@@ -268,8 +281,10 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(SortArgs A) {
   for (int k0 = 0; k0 < nk; k0 += kSortThreads) {
     const int k = k0 + tid;
     int total = 0;
-    if (k < nk)
+    if (k < nk) {
+      total = before[k] + behind[k];
       for (int w = 0; w < kSortWaves; ++w) total += cnt[w * nk + k];
+    }
     const int64_t own = int64_t(total) + (total > 0 ? int64_t(1) << 32 : 0);
     int64_t x = own;
 #pragma unroll
@@ -286,29 +301,34 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(SortArgs A) {
     }
     if (k < nk) {
       const int64_t at = base + x - own;
-      int start = static_cast<int>(at);
-      end[k] = start + total;
-      slot[k] = static_cast<int>(at >> 32);
+      int start = static_cast<int>(at) + before[k];
       for (int w = 0; w < kSortWaves; ++w) {
         const int c = cnt[w * nk + k];
         cnt[w * nk + k] = start;
         start += c;
       }
+      before[k] = static_cast<int>(at) + total;
+      behind[k] = static_cast<int>(at >> 32);
     }
     __syncthreads();
   }
-  if (tid == 0) {
-    A.distinct[blockIdx.x] = static_cast<int>(carry >> 32);
-    if (blockIdx.x == gridDim.x - 1) *A.live = static_cast<int>(carry);
+  const int32_t* const end = before;
+  const int32_t* const slot = behind;
+  if (tid == 0 && segment == 0) {
+    A.distinct[part] = static_cast<int>(carry >> 32);
+    if (blockIdx.x + A.segments == gridDim.x) *A.live = static_cast<int>(carry);
   }
 
   if (static_cast<int>(carry) > first) {
-    for (int i0 = beg; i0 < fin; i0 += 64 * U) {
+    volatile int32_t* const mine = cnt + wave * nk;  // read by lanes other than the one that wrote it
+    const int64_t beg = min(int64_t(A.n), seg0 + int64_t(wave) * A.run), fin = min(int64_t(A.n), beg + A.run);
+    for (int64_t i0 = beg; i0 < fin; i0 += 64 * U) {
       int32_t t[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * 64 + lane;
-        t[u] = i < fin ? token(tokens, i, A.vocab) : -1;
+        const int64_t i = i0 + u * 64 + lane;
+        t[u] = token(tokens, min(i, int64_t(A.n) - 1), A.vocab);
+        if (i >= fin) t[u] = -1;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -322,20 +342,20 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(SortArgs A) {
           same &= set ? with : ~with;
         }
         if (in) {
-          const int at = mine[k], before = lanes_below(same, lane);
-          A.recs[at + before] = {i0 + u * 64 + lane, k + lo, slot[k], end[k]};
-          if (before == 0) mine[k] = at + __popcll(same);
+          const int at = mine[k], earlier = lanes_below(same, lane);
+          A.recs[at + earlier] = {static_cast<int32_t>(i0) + u * 64 + lane, k + lo, slot[k], end[k]};
+          if (earlier == 0) mine[k] = at + __popcll(same);
         }
       }
     }
   }
 
   if (A.grad == nullptr) return;
-  // Rows without a token, a wave each (all of a token's records end behind
-  // its first one, so an empty token's end is where the next one starts).
-  for (int k = wave; k < nk; k += kSortWaves) {
-    const int before = k > 0 ? end[k - 1] : first;
-    if (end[k] != before) continue;
+  // Rows without a token, a wave each, the segments' blocks in turn (all of a
+  // token's records end behind its first one, so an empty token's end is where
+  // the next one starts).
+  for (int k = wave * A.segments + segment; k < nk; k += kSortWaves * A.segments) {
+    if (end[k] != (k > 0 ? end[k - 1] : first)) continue;
     const float zero[8] = {};
     if (A.grad_f32) {
       float* const row = static_cast<float*>(A.grad) + int64_t(lo + k) * A.grad_ld;
@@ -364,7 +384,7 @@ struct SumArgs {
   float* head;      // [chunk][ld_part]: the part of a token that began in an earlier chunk
   float* tail;      // [chunk][ld_part]: the first part of a token that goes on in the next chunk
   int64_t ld_part;
-  int32_t cols, slabs, chunks, chunk, range, blocks;
+  int32_t cols, slabs, chunks, chunk, range, ranges;
   float scale;
 };
 
@@ -374,15 +394,16 @@ __device__ __forceinline__ int wave_sum(int x) {
   return x;
 }
 
-// Distinct tokens in sort blocks [b0, b1): the same for every lane.
+// Distinct tokens in ranges [b0, b1): the same for every lane.
 __device__ __forceinline__ int distinct_in(const int32_t* distinct, int b0, int b1, int lane) {
   int s = 0;
   for (int b = b0 + lane; b < b1; b += 64) s += distinct[b];
   return __builtin_amdgcn_readfirstlane(wave_sum(s));
 }
 
-// A lane has columns [col, col + 4); its loads are those of [from, from + 4),
-// which differs where the row ends (rows of under four columns aside).
+// A lane has columns [col, col + 4) and works on [from, from + 4), which differs
+// where the row ends: its last lane then does some of the columns before its
+// own once more (rows of under four columns aside).
 struct Cols {
   int col, nc;  // nc: how many of them exist, at most zero for none
   int from;
@@ -392,30 +413,58 @@ __device__ __forceinline__ Cols cols_of(int slab, int lane, int cols) {
   return {col, cols - col, cols >= kVec ? min(col, cols - kVec) : 0};
 }
 
-// A finished sum goes out. row: the token, or its place among the rows.
+// A finished sum goes out. row: the token, or its place among the rows. A
+// column that two lanes have gets the same value twice; an addition to what is
+// there may happen once only, so there each lane keeps to its own columns.
 template <typename G, int MODE>
-__device__ __forceinline__ void put(const SumArgs& A, int64_t row, const Cols& l, float (&x)[kVec]) {
-  const int col = l.col, nc = l.nc;
-  if (nc <= 0) return;
-  G* const p = static_cast<G*>(A.grad) + row * A.grad_ld + col;
-  if constexpr (MODE == kAdd) {
-    float old[kVec];
-    load4_of(p, nc, old);
+__device__ __forceinline__ void put(const SumArgs& A, int64_t row, const Cols& l, const float (&acc)[kVec]) {
+  if (l.nc <= 0) return;
+  G* const p = static_cast<G*>(A.grad) + row * A.grad_ld + l.from;
+  float x[kVec];
+  if (MODE != kAdd) {
 #pragma unroll
-    for (int q = 0; q < kVec; ++q) x[q] = old[q] + x[q] * A.scale;
-  } else {
-#pragma unroll
-    for (int q = 0; q < kVec; ++q) x[q] *= A.scale;
+    for (int q = 0; q < kVec; ++q) x[q] = acc[q] * A.scale;
+    store4_of(p, A.cols, x);
+    return;
   }
-  store4_of(p, nc, x);
+  const int skip = l.col - l.from;
+  if (skip == 0) {
+    load4_of(p, A.cols, x);
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) x[q] += acc[q] * A.scale;
+    store4_of(p, A.cols, x);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < kVec; ++q)
+    if (q >= skip) muon_adam::PElem<G>::store(p, q, muon_adam::PElem<G>::load(p, q) + acc[q] * A.scale);
 }
+
+__device__ __forceinline__ void put_part(float* part, const SumArgs& A, int64_t chunk, const Cols& l, const float (&acc)[kVec]) {
+  if (l.nc > 0) muon_adam::store4<false>(part + chunk * A.ld_part + l.from, acc);
+}
+
+// A row's four elements as they lie in memory.
+template <typename D> struct Raw;
+template <> struct Raw<float> {
+  typedef muon_adam::f32x4 T;
+  static constexpr int rows = 8;  // in one group of loads; two groups are in flight
+  static __device__ __forceinline__ float get(const T& x, int q) { return x[q]; }
+};
+template <> struct Raw<uint16_t> {
+  typedef muon_adam::u32x2 T;
+  static constexpr int rows = 16;
+  static __device__ __forceinline__ float get(const T& x, int q) {
+    return __uint_as_float(q & 1 ? x[q >> 1] & 0xffff0000u : x[q >> 1] << 16);
+  }
+};
 
 template <typename D, typename G, int MODE>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(SumArgs A) {
   const int lane = threadIdx.x & 63;
   const int64_t id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + int64_t(blockIdx.x) * (kThreads / 64);
   if (MODE == kRows && id == 0) {
-    const int total = distinct_in(A.distinct, 0, A.blocks, lane);
+    const int total = distinct_in(A.distinct, 0, A.ranges, lane);
     if (lane == 0) *A.count = total;
   }
   const int64_t chunk = id / A.slabs;
@@ -426,71 +475,81 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(SumArgs A) {
   const int len = static_cast<int>(min(int64_t(A.chunk), live - c0));
   const int c1 = static_cast<int>(c0) + len;
   const Cols l = cols_of(slab, lane, A.cols);
-  const Rec mine = lane < len ? A.recs[c0 + lane] : Rec{0, -1, 0, 0};  // a chunk has at most 64 records
-  const int prev = c0 > 0 ? __builtin_amdgcn_readfirstlane(A.recs[c0 - 1].key) : -1;
+  // a chunk has at most 64 records: lane i has the i-th
+  const Rec mine = A.recs[c0 + min(lane, len - 1)];
   int key = __builtin_amdgcn_readfirstlane(mine.key);
-  int block = key / A.range, base = 0;
-  if (MODE == kRows) base = distinct_in(A.distinct, 0, block, lane);
+  // the first token's sum is a part if it began in an earlier chunk
+  bool head = c0 > 0 && __builtin_amdgcn_readfirstlane(A.recs[c0 - 1].key) == key;
+  int row = mine.key;  // where the lane's token goes
+  if (MODE == kRows) {
+    const int mine_in = mine.key / A.range;
+    int base = 0, from = 0;
+    for (uint64_t todo = ~uint64_t(0); todo;) {  // a range at a time
+      const int r = __builtin_amdgcn_readlane(mine_in, __builtin_ctzll(todo));
+      base += distinct_in(A.distinct, from, r, lane);
+      from = r;
+      if (mine_in == r) row = base + mine.slot;
+      todo &= ~__ballot(mine_in == r);
+    }
+    // (the chunk that a token begins in)
+    const int left = __shfl_up(mine.key, 1, 64);
+    if (slab == 0 && lane < len && (lane > 0 ? left != mine.key : !head)) A.rows[row] = mine.key;
+  }
   float acc[kVec] = {};
-  int last = 0;  // the lane that holds a record of the current token
-
+  int at = 0;  // a record of the current token
   auto flush = [&]() {
-    const int end = __builtin_amdgcn_readlane(mine.end, last);
-    float* part = nullptr;
-    if (key == prev && __builtin_amdgcn_readfirstlane(mine.key) == key) part = A.head;
-    else if (end > c1) part = A.tail;
-    int64_t row = key;
-    if (MODE == kRows) {
-      const int b = key / A.range;
-      if (b != block) {
-        base += distinct_in(A.distinct, block, b, lane);
-        block = b;
-      }
-      row = base + __builtin_amdgcn_readlane(mine.slot, last);
-    }
-    // the lane's own columns first: a row's last lane has loaded those before them, too
-    const int shift = l.col - l.from;
-    float x[kVec];
+    if (head) put_part(A.head, A, chunk, l, acc);
+    else put<G, MODE>(A, __builtin_amdgcn_readlane(row, at), l, acc);
+    head = false;
 #pragma unroll
-    for (int q = 0; q < kVec; ++q) x[q] = shift == 1 && q < 3 ? acc[q + 1] : shift == 2 && q < 2 ? acc[q + 2] : shift == 3 && q < 1 ? acc[3] : acc[q];
-    if (part != nullptr) {
-      if (l.nc > 0) *reinterpret_cast<float4*>(part + chunk * A.ld_part + l.col) = make_float4(x[0], x[1], x[2], x[3]);
-    } else {
-      put<G, MODE>(A, row, l, x);
-      if (MODE == kRows && slab == 0 && lane == 0) A.rows[row] = key;
-    }
+    for (int q = 0; q < kVec; ++q) acc[q] = 0.f;
   };
-
   const D* const dout = static_cast<const D*>(A.dout) + l.from;
-  constexpr int U = 8;  // rows in flight
-  for (int i0 = 0; i0 < len; i0 += U) {
-    float x[U][kVec];
-    // no branch around a load: they all go out before the first is waited for
-    if (A.cols >= kVec) {
+  typedef Raw<D> R;
+  constexpr int U = R::rows;
+  if (A.cols < kVec) {  // narrow rows
+    for (int i = 0; i < len; ++i) {
+      const int k = __builtin_amdgcn_readlane(mine.key, i);
+      if (k != key) flush();
+      key = k;
+      at = i;
+      float x[kVec];
+      load4_of(dout + int64_t(__builtin_amdgcn_readlane(mine.pos, i)) * A.dout_ld, A.cols, x);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        muon_adam::load4<false>(dout + int64_t(__builtin_amdgcn_readlane(mine.pos, min(i0 + u, len - 1))) * A.dout_ld, x[u]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        load4_of(dout + int64_t(__builtin_amdgcn_readlane(mine.pos, min(i0 + u, len - 1))) * A.dout_ld, A.cols, x[u]);
+      for (int q = 0; q < kVec; ++q) acc[q] += x[q];
     }
+  } else {
+    // The next group of rows is fetched before the last one is added up, with
+    // no branch around a load: all of a group's are in flight at once.
+    auto fetch = [&](int i0, typename R::T (&x)[U]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i0 + u >= len) break;
-      const int k = __builtin_amdgcn_readlane(mine.key, i0 + u);
-      if (k != key) {
-        flush();
+      for (int u = 0; u < U; ++u)
+        x[u] = *reinterpret_cast<const typename R::T*>(dout + int64_t(__builtin_amdgcn_readlane(mine.pos, min(i0 + u, len - 1))) * A.dout_ld);
+    };
+    auto add = [&](int i0, const typename R::T (&x)[U]) {
 #pragma unroll
-        for (int q = 0; q < kVec; ++q) acc[q] = 0.f;
+      for (int u = 0; u < U; ++u) {
+        if (i0 + u >= len) break;
+        const int k = __builtin_amdgcn_readlane(mine.key, i0 + u);
+        if (k != key) flush();
         key = k;
-        last = i0 + u;
-      }
+        at = i0 + u;
 #pragma unroll
-      for (int q = 0; q < kVec; ++q) acc[q] += x[u][q];
+        for (int q = 0; q < kVec; ++q) acc[q] += R::get(x[u], q);
+      }
+    };
+    typename R::T x[U], y[U];
+    fetch(0, x);
+    for (int i0 = 0; i0 < len; i0 += 2 * U) {
+      if (i0 + U < len) fetch(i0 + U, y);
+      add(i0, x);
+      if (i0 + U >= len) break;
+      if (i0 + 2 * U < len) fetch(i0 + 2 * U, x);
+      add(i0 + U, y);
     }
   }
-  flush();
+  if (!head && __builtin_amdgcn_readlane(mine.end, at) > c1) put_part(A.tail, A, chunk, l, acc);
+  else flush();
 }
 
 // A token that crosses chunks: its first part, then one part of every later
@@ -515,17 +574,18 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs A) {
   constexpr int W = kThreads / 64, U = 8;
   if (l.nc > 0) {
     if (wave == 0) {
-      const float4 t = *reinterpret_cast<const float4*>(A.tail + chunk * A.ld_part + l.col);
-      acc[0] = t.x, acc[1] = t.y, acc[2] = t.z, acc[3] = t.w;
+      muon_adam::load4<false>(A.tail + chunk * A.ld_part + l.from, acc);
     }
     for (int64_t j0 = chunk + 1 + wave; j0 <= stop; j0 += W * U) {
-      float4 x[U];
+      float x[U][kVec];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        x[u] = j0 + u * W <= stop ? *reinterpret_cast<const float4*>(A.head + (j0 + u * W) * A.ld_part + l.col)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int u = 0; u < U; ++u) muon_adam::load4<false>(A.head + min(j0 + u * W, stop) * A.ld_part + l.from, x[u]);
 #pragma unroll
-      for (int u = 0; u < U; ++u) acc[0] += x[u].x, acc[1] += x[u].y, acc[2] += x[u].z, acc[3] += x[u].w;
+      for (int u = 0; u < U; ++u) {
+        if (j0 + u * W > stop) break;
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) acc[q] += x[u][q];
+      }
     }
   }
   if (wave > 0) red[wave - 1][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -537,10 +597,7 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs A) {
     acc[0] += t.x, acc[1] += t.y, acc[2] += t.z, acc[3] += t.w;
   }
   int64_t row = r.key;
-  if (MODE == kRows) {
-    row = distinct_in(A.distinct, 0, r.key / A.range, lane) + r.slot;
-    if (slab == 0 && lane == 0) A.rows[row] = r.key;
-  }
+  if (MODE == kRows) row = distinct_in(A.distinct, 0, r.key / A.range, lane) + r.slot;
   put<G, MODE>(A, row, l, acc);
 }
 
@@ -598,20 +655,30 @@ __global__ __launch_bounds__(kThreads) void embed_adam_kernel(RowArgs A) {
 int64_t size_of(int32_t dtype) { return dtype == MUON_F32 ? 4 : 2; }
 
 struct Sizes {
-  int32_t range, blocks;  // sort: entries of a block, blocks
+  int32_t range, ranges;  // sort: entries of a range, ranges
+  int32_t segments, run;  // segments of the batch, tokens of a wave in one
   int32_t chunk, chunks;  // sum: records of a chunk, chunks
   int32_t slabs;
   int64_t ld_part;
   size_t recs, distinct, live, head, tail, total;  // byte offsets, and the whole
 };
 
-// Sort: one block per CU, as long as its counters fit. Sum: chunks short
-// enough that chunks and slabs give every CU a few waves, of at least 4 and at
-// most 64 records (a lane each).
+// Sort: a block per CU, ranges times segments of the batch. Segments split the
+// work of ranges with many tokens (but all blocks read all tokens), so there
+// are as many as leave each kSegment tokens and fit beside the ranges, whose
+// length the counters in LDS limit. Sum: chunks short enough that chunks and
+// slabs give every CU a few waves, of at least 4 and at most 64 records (a
+// lane each).
 Sizes sizes_of(int64_t vocab, int64_t cols, int64_t n) {
   Sizes s{};
-  s.range = static_cast<int32_t>(std::min<int64_t>(kMaxRange, (vocab + kSortBlocks - 1) / kSortBlocks));
-  s.blocks = static_cast<int32_t>((vocab + s.range - 1) / s.range);
+  const int64_t least = (vocab + kMaxRange - 1) / kMaxRange;
+  const int64_t segments = std::max<int64_t>(1, std::min(n / kSegment, kSortBlocks / least));
+  const int64_t wanted = std::max<int64_t>(least, kSortBlocks / segments);
+  s.range = static_cast<int32_t>((vocab + wanted - 1) / wanted);
+  s.ranges = static_cast<int32_t>((vocab + s.range - 1) / s.range);
+  const int64_t unit = segments * kSortThreads;  // a multiple of 64 tokens for every wave
+  s.run = static_cast<int32_t>((n + unit - 1) / unit * 64);
+  s.segments = static_cast<int32_t>(segments);
   s.slabs = static_cast<int32_t>((cols + kSlab - 1) / kSlab);
   int64_t chunk = 4;
   while (chunk < 64 && (n + chunk - 1) / chunk * s.slabs > kSumWaves) chunk *= 2;
@@ -624,7 +691,7 @@ Sizes sizes_of(int64_t vocab, int64_t cols, int64_t n) {
   const size_t part = up(size_t(most) * size_t(s.ld_part) * sizeof(float));
   s.recs = 0;
   s.distinct = s.recs + up(size_t(n) * sizeof(Rec));
-  s.live = s.distinct + up(size_t(s.blocks) * sizeof(int32_t));
+  s.live = s.distinct + up(size_t(s.ranges) * sizeof(int32_t));
   s.head = s.live + 256;
   s.tail = s.head + part;
   s.total = s.tail + part;
@@ -751,12 +818,14 @@ muon_status run_gradient(muon_embed_plan* p, const muon_embed_tokens* tokens, co
   a.vocab = static_cast<int32_t>(p->t.vocab);
   a.cols = static_cast<int32_t>(p->t.cols);
   a.range = z.range;
+  a.segments = z.segments;
+  a.run = z.run;
   while ((1 << a.bits) < z.range) ++a.bits;
   const size_t lds = size_t(kSortWaves + 2) * size_t(z.range) * sizeof(int32_t);
   if (tokens->wide)
-    hipLaunchKernelGGL(embed_sort_kernel<int64_t>, dim3(unsigned(z.blocks)), dim3(kSortThreads), lds, s, a);
+    hipLaunchKernelGGL(embed_sort_kernel<int64_t>, dim3(unsigned(z.ranges * z.segments)), dim3(kSortThreads), lds, s, a);
   else
-    hipLaunchKernelGGL(embed_sort_kernel<int32_t>, dim3(unsigned(z.blocks)), dim3(kSortThreads), lds, s, a);
+    hipLaunchKernelGGL(embed_sort_kernel<int32_t>, dim3(unsigned(z.ranges * z.segments)), dim3(kSortThreads), lds, s, a);
   muon_status st = launched();
   if (st != MUON_OK) return st;
   SumArgs b{};
@@ -777,7 +846,7 @@ muon_status run_gradient(muon_embed_plan* p, const muon_embed_tokens* tokens, co
   b.chunk = z.chunk;
   b.chunks = std::max(1, z.chunks);  // no token: one wave that leaves the count
   b.range = z.range;
-  b.blocks = z.blocks;
+  b.ranges = z.ranges;
   b.scale = scale;
   if (mode != kRows && tokens->n == 0) return MUON_OK;
   if (mode == kDense) return launch_sum<kDense>(b, dout->dtype, p->dtype, s);
