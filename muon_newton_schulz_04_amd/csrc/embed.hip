@@ -384,6 +384,7 @@ struct SumArgs {
   float* head;      // [chunk][ld_part]: the part of a token that began in an earlier chunk
   float* tail;      // [chunk][ld_part]: the first part of a token that goes on in the next chunk
   int64_t ld_part;
+  int64_t n;        // records, live and not
   int32_t cols, slabs, chunks, chunk, range, ranges;
   float scale;
 };
@@ -469,17 +470,25 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(SumArgs A) {
   }
   const int64_t chunk = id / A.slabs;
   const int slab = static_cast<int>(id - chunk * A.slabs);
-  const int live = __builtin_amdgcn_readfirstlane(*A.live);
   const int64_t c0 = chunk * A.chunk;
+  if (c0 >= A.n) return;
+  // a chunk has at most 64 records: lane i has the i-th (those behind *live
+  // are not set and not used; all are loaded at once)
+  Rec mine = A.recs[min(c0 + lane, A.n - 1)];
+  const int before = A.recs[c0 > 0 ? c0 - 1 : 0].key;
+  const int live = __builtin_amdgcn_readfirstlane(*A.live);
   if (c0 >= live) return;
   const int len = static_cast<int>(min(int64_t(A.chunk), live - c0));
   const int c1 = static_cast<int>(c0) + len;
   const Cols l = cols_of(slab, lane, A.cols);
-  // a chunk has at most 64 records: lane i has the i-th
-  const Rec mine = A.recs[c0 + min(lane, len - 1)];
+  if (lane >= len) {  // the last record again
+    mine.pos = __builtin_amdgcn_readlane(mine.pos, len - 1);
+    mine.key = __builtin_amdgcn_readlane(mine.key, len - 1);
+    mine.slot = __builtin_amdgcn_readlane(mine.slot, len - 1);
+  }
   int key = __builtin_amdgcn_readfirstlane(mine.key);
   // the first token's sum is a part if it began in an earlier chunk
-  bool head = c0 > 0 && __builtin_amdgcn_readfirstlane(A.recs[c0 - 1].key) == key;
+  bool head = c0 > 0 && __builtin_amdgcn_readfirstlane(before) == key;
   int row = mine.key;  // where the lane's token goes
   if (MODE == kRows) {
     const int mine_in = mine.key / A.range;
@@ -520,11 +529,12 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(SumArgs A) {
     }
   } else {
     // The next group of rows is fetched before the last one is added up, with
-    // no branch around a load: all of a group's are in flight at once.
+    // no branch around a load (behind the chunk's end the last row again), so
+    // that the waits for a group need not count those of the next.
     auto fetch = [&](int i0, typename R::T (&x)[U]) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        x[u] = *reinterpret_cast<const typename R::T*>(dout + int64_t(__builtin_amdgcn_readlane(mine.pos, min(i0 + u, len - 1))) * A.dout_ld);
+        x[u] = __builtin_nontemporal_load(reinterpret_cast<const typename R::T*>(dout + int64_t(__builtin_amdgcn_readlane(mine.pos, min(i0 + u, len - 1))) * A.dout_ld));
     };
     auto add = [&](int i0, const typename R::T (&x)[U]) {
 #pragma unroll
@@ -540,11 +550,12 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(SumArgs A) {
     };
     typename R::T x[U], y[U];
     fetch(0, x);
-    for (int i0 = 0; i0 < len; i0 += 2 * U) {
-      if (i0 + U < len) fetch(i0 + U, y);
+    if (A.chunk <= U) {
+      add(0, x);
+    } else for (int i0 = 0; i0 < len; i0 += 2 * U) {
+      fetch(i0 + U, y);
       add(i0, x);
-      if (i0 + U >= len) break;
-      if (i0 + 2 * U < len) fetch(i0 + 2 * U, x);
+      fetch(i0 + 2 * U, x);
       add(i0 + U, y);
     }
   }
@@ -561,13 +572,13 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs A) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t chunk = blockIdx.x / A.slabs;
   const int slab = static_cast<int>(blockIdx.x - chunk * A.slabs);
-  const int live = __builtin_amdgcn_readfirstlane(*A.live);
   const int64_t c0 = chunk * A.chunk, c1 = c0 + A.chunk;
-  if (c1 >= live) return;  // the last chunk: nothing goes on behind it
+  if (c1 >= A.n) return;
   const Rec r = A.recs[c1 - 1];
+  const int before = A.recs[c0 > 0 ? c0 - 1 : 0].key;
+  if (c1 >= *A.live) return;  // the last chunk: nothing goes on behind it
   if (r.end <= c1) return;
-  // began before this chunk: another block's
-  if (c0 > 0 && A.recs[c0 - 1].key == r.key) return;
+  if (c0 > 0 && before == r.key) return;  // began before this chunk: another block's
   const Cols l = cols_of(slab, lane, A.cols);
   const int64_t stop = (r.end - 1) / A.chunk;  // the last chunk it reaches
   float acc[kVec] = {};
@@ -841,6 +852,7 @@ muon_status run_gradient(muon_embed_plan* p, const muon_embed_tokens* tokens, co
   b.head = reinterpret_cast<float*>(w + z.head);
   b.tail = reinterpret_cast<float*>(w + z.tail);
   b.ld_part = z.ld_part;
+  b.n = tokens->n;
   b.cols = a.cols;
   b.slabs = z.slabs;
   b.chunk = z.chunk;
