@@ -35,9 +35,11 @@ using muon_adam::kVec;
 constexpr int kThreads = 256;
 constexpr int kLookVec = 8;        // consecutive elements per thread of the lookup
 constexpr int kLookRuns = 4;       // such vectors per thread, kThreads apart
-constexpr int kSortThreads = 1024;
+constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kMaxRange = 2048;    // vocabulary entries of a sort block: 16 waves' counters fill 128 KB of LDS
+constexpr int kSortLoads = 8;      // tokens a lane has in flight
+constexpr int kQueue = 64 * (kSortLoads + 1);  // of a wave: tokens found, not yet placed
+constexpr int kMaxRange = 3000;    // vocabulary entries of a sort block: ten counters each, 117 of the 160 KB of LDS
 constexpr int kSortBlocks = 256;   // sort blocks: one per CU
 constexpr int kSegment = 4096;     // tokens of a segment of the batch, at least
 constexpr int kSlab = 64 * kVec;   // columns of a wave in the sum
@@ -130,12 +132,32 @@ __device__ __forceinline__ void store4_of(T* p, int n, const float (&x)[kVec]) {
   }
 }
 
-// The token at i, or -1 where it is outside the vocabulary.
+// A token as it was given, -1 where it is outside the vocabulary.
+__device__ __forceinline__ int32_t narrow(int32_t t, int32_t vocab) {
+  return static_cast<uint32_t>(t) < static_cast<uint32_t>(vocab) ? t : -1;
+}
+__device__ __forceinline__ int32_t narrow(int64_t t, int32_t vocab) {
+  return (t >> 32) == 0 ? narrow(static_cast<int32_t>(t), vocab) : -1;
+}
 template <typename I>
 __device__ __forceinline__ int32_t token(const I* tokens, int64_t i, int32_t vocab) {
-  const I t = tokens[i];
-  return t >= 0 && t < static_cast<I>(vocab) ? static_cast<int32_t>(t) : -1;
+  return narrow(tokens[i], vocab);
 }
+
+// A wave's tokens i0 + 64 u + lane, u < U; behind fin the last one again, so
+// that no load is behind a branch.
+template <int U, typename I>
+__device__ __forceinline__ void load_tokens(const I* tokens, int64_t i0, int64_t fin, int lane, I (&t)[U]) {
+  if (i0 + 64 * U <= fin) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) t[u] = tokens[i0 + 64 * u + lane];
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u) t[u] = tokens[min(i0 + 64 * u + lane, fin - 1)];
+  }
+}
+__device__ __forceinline__ uint32_t unsigned_of(int32_t t) { return static_cast<uint32_t>(t); }
+__device__ __forceinline__ uint64_t unsigned_of(int64_t t) { return static_cast<uint64_t>(t); }
 
 // k / d for magic = (2^32 - 1) / d: 2^32 - magic d lies in [1, d], so the
 // product's high word is the quotient or one less.
@@ -214,76 +236,92 @@ struct SortArgs {
   Rec* recs;
   int32_t* distinct;  // per range: its distinct tokens
   int32_t* live;      // tokens inside the vocabulary
-  void* grad;         // dense form: rows without a token are cleared here (nullptr: not)
-  int64_t grad_ld;
-  int32_t n, vocab, cols, range;
+  uint8_t* present;   // dense form: whether a token occurs (nullptr: not wanted)
+  int32_t n, vocab, range;
   int32_t segments, run;  // of the batch; tokens of a wave in its block's segment, a multiple of 64
   int32_t bits;           // of a token's place in the range
-  int32_t grad_f32;
 };
 
 __device__ __forceinline__ int lanes_below(uint64_t mask, int lane) {
   return __popcll(mask & ((uint64_t(1) << lane) - 1));
 }
 
-// The lookups of a batch's frequent tokens fall into few ranges, whose blocks
-// set the time: with one segment of the batch (256 ranges, one a CU) the
-// gradient of 32768 Zipf-distributed tokens of 50257 spent 47 us here.
+// A batch's frequent tokens fall into few ranges, whose blocks set the time:
+// hence the segments. What else counts is the number of instructions a token
+// takes in the blocks that it does not belong to, and their size (a long
+// unrolled body takes as long to fetch as to run): tokens are compared as they
+// are (one outside the vocabulary is in no range), and those of the range are
+// queued and placed 64 at a time.
 template <typename I>
 __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(SortArgs A) {
-  extern __shared__ int32_t lds[];
+  extern __shared__ __align__(16) int32_t lds[];
+  constexpr int W = kSortWaves, U = kSortLoads;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int part = blockIdx.x / A.segments, segment = blockIdx.x - part * A.segments;
   const int lo = part * A.range;
   const int nk = min(A.range, A.vocab - lo);
-  int32_t* const cnt = lds;                       // [wave][key]: the wave's tokens, then where its next one goes
-  int32_t* const before = lds + kSortWaves * nk;  // [key]: tokens of earlier segments; then the end of the token's records
-  int32_t* const behind = before + nk;            // [key]: of later segments; then the token's rank in the range
-  __shared__ int32_t below[kSortWaves];
-  __shared__ int64_t scan[kSortWaves];
-  for (int i = tid; i < (kSortWaves + 2) * nk; i += kSortThreads) lds[i] = 0;
+  int32_t* const cnt = lds;              // [key][wave]: the wave's tokens, then where its next one goes
+  int32_t* const before = lds + W * nk;  // [key]: tokens of earlier segments; then the end of the token's records
+  int32_t* const behind = before + nk;   // [key]: of later segments; then the token's rank in the range
+  __shared__ uint2 queues[W][kQueue];
+  __shared__ int32_t below[W];
+  __shared__ int64_t scan[W];
+  for (int i = tid * 4; i < (W + 2) * nk; i += kSortThreads * 4) *reinterpret_cast<int4*>(lds + i) = int4{0, 0, 0, 0};
   __syncthreads();
 
   const I* const tokens = static_cast<const I*>(A.tokens);
-  constexpr int U = 8;  // loads in flight
-  const int64_t size = int64_t(A.run) * kSortWaves;  // of a segment
-  const int64_t seg0 = segment * size, seg1 = seg0 + size;
-  {
-    // every wave a run of the whole batch; a step of 64 tokens lies in one wave's run of one segment
-    const int64_t each = (int64_t(A.n) + kSortThreads - 1) / kSortThreads * 64;
-    const int64_t beg = wave * each, fin = min(int64_t(A.n), beg + each);
-    int under = 0;
+  const int64_t seg0 = min(int64_t(A.n), segment * int64_t(A.run) * W), seg1 = min(int64_t(A.n), seg0 + int64_t(A.run) * W);
+  const int64_t run0 = min(seg1, seg0 + int64_t(wave) * A.run), run1 = min(seg1, run0 + A.run);  // the wave's own
+  int under = 0;
+#pragma unroll 1
+  for (int stage = 0; stage < 3; ++stage) {  // earlier segments, the block's, later ones
+    int64_t beg = run0, fin = run1;
+    int32_t* to = cnt + wave;
+    if (stage != 1) {  // a share for every wave
+      const int64_t from = stage == 0 ? 0 : seg1, till = stage == 0 ? seg0 : int64_t(A.n);
+      const int64_t each = ((till - from + kSortThreads - 1) / kSortThreads) * 64;
+      beg = min(till, from + wave * each);
+      fin = min(till, beg + each);
+      to = stage == 0 ? before : behind;
+    }
+    const int pitch = stage == 1 ? W : 1;
+    I t[U], next[U];
+    if (beg < fin) load_tokens(tokens, beg, fin, lane, next);
+#pragma unroll 1
     for (int64_t i0 = beg; i0 < fin; i0 += 64 * U) {
-      int32_t t[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) t[u] = next[u];
+      load_tokens(tokens, min(i0 + 64 * U, fin - 1), fin, lane, next);  // in flight meanwhile
+      const int left = static_cast<int>(min(fin - i0, int64_t(64 * U)));
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t i = i0 + u * 64 + lane;
-        t[u] = token(tokens, min(i, int64_t(A.n) - 1), A.vocab);
-        if (i >= fin) t[u] = -1;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t i = i0 + u * 64;
-        int32_t* const to = i < seg0 ? before : i >= seg1 ? behind : cnt + static_cast<int>((i - seg0) / A.run) * nk;
-        under += __popcll(__ballot(t[u] >= 0 && t[u] < lo));
-        const int k = t[u] - lo;
-        if (k >= 0 && k < nk) atomicAdd(to + k, 1);
+        // (a negative token is above all others as an unsigned number)
+        const bool there = 64 * u + lane < left;
+        under += __popcll(__ballot(there && unsigned_of(t[u]) < unsigned_of(I(lo))));
+        const auto k = unsigned_of(t[u]) - unsigned_of(I(lo));
+        if (there && k < unsigned_of(I(nk))) atomicAdd(to + static_cast<uint32_t>(k) * pitch, 1);
       }
     }
-    if (lane == 0) below[wave] = under;
   }
+  if (lane == 0) below[wave] = under;
   __syncthreads();
 
   // Starts of the tokens: a scan over the keys of (count, is there any) in one 64-bit sum.
   int64_t carry = 0;
-  for (int w = 0; w < kSortWaves; ++w) carry += below[w];
+  for (int w = 0; w < W; ++w) carry += below[w];
   const int first = static_cast<int>(carry);
+#pragma unroll 1
   for (int k0 = 0; k0 < nk; k0 += kSortThreads) {
     const int k = k0 + tid;
-    int total = 0;
+    int total = 0, early = 0, c[W] = {};
     if (k < nk) {
-      total = before[k] + behind[k];
-      for (int w = 0; w < kSortWaves; ++w) total += cnt[w * nk + k];
+      static_assert(W == 8, "two vectors of four counters");
+      const int4 x = *reinterpret_cast<const int4*>(cnt + W * k), y = *reinterpret_cast<const int4*>(cnt + W * k + 4);
+      c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w, c[4] = y.x, c[5] = y.y, c[6] = y.z, c[7] = y.w;
+      early = before[k];
+      total = early + behind[k];
+#pragma unroll
+      for (int w = 0; w < W; ++w) total += c[w];
     }
     const int64_t own = int64_t(total) + (total > 0 ? int64_t(1) << 32 : 0);
     int64_t x = own;
@@ -295,18 +333,21 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(SortArgs A) {
     if (lane == 63) scan[wave] = x;
     __syncthreads();
     int64_t base = carry;
-    for (int w = 0; w < kSortWaves; ++w) {
+    for (int w = 0; w < W; ++w) {
       if (w < wave) base += scan[w];
       carry += scan[w];
     }
     if (k < nk) {
       const int64_t at = base + x - own;
-      int start = static_cast<int>(at) + before[k];
-      for (int w = 0; w < kSortWaves; ++w) {
-        const int c = cnt[w * nk + k];
-        cnt[w * nk + k] = start;
-        start += c;
+      int start = static_cast<int>(at) + early;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const int n = c[w];
+        c[w] = start;
+        start += n;
       }
+      *reinterpret_cast<int4*>(cnt + W * k) = int4{c[0], c[1], c[2], c[3]};
+      *reinterpret_cast<int4*>(cnt + W * k + 4) = int4{c[4], c[5], c[6], c[7]};
       before[k] = static_cast<int>(at) + total;
       behind[k] = static_cast<int>(at >> 32);
     }
@@ -319,52 +360,65 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(SortArgs A) {
     if (blockIdx.x + A.segments == gridDim.x) *A.live = static_cast<int>(carry);
   }
 
-  if (static_cast<int>(carry) > first) {
-    volatile int32_t* const mine = cnt + wave * nk;  // read by lanes other than the one that wrote it
-    const int64_t beg = min(int64_t(A.n), seg0 + int64_t(wave) * A.run), fin = min(int64_t(A.n), beg + A.run);
-    for (int64_t i0 = beg; i0 < fin; i0 += 64 * U) {
-      int32_t t[U];
+  if (static_cast<int>(carry) > first && run0 < run1) {
+    // read by lanes other than the ones that wrote it
+    volatile int32_t* const mine = cnt + wave;
+    volatile uint2* const queue = queues[wave];
+    int have = 0;
+#pragma unroll 1
+    for (int64_t i0 = run0; i0 < run1; i0 += 64 * U) {
+      I t[U];
+      load_tokens(tokens, i0, run1, lane, t);
+      const int left = static_cast<int>(min(run1 - i0, int64_t(64 * U)));
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t i = i0 + u * 64 + lane;
-        t[u] = token(tokens, min(i, int64_t(A.n) - 1), A.vocab);
-        if (i >= fin) t[u] = -1;
+        const auto k = unsigned_of(t[u]) - unsigned_of(I(lo));
+        const bool in = 64 * u + lane < left && k < unsigned_of(I(nk));
+        const uint64_t found = __ballot(in);
+        if (in) {
+          const int at = have + lanes_below(found, lane);
+          queue[at].x = static_cast<uint32_t>(k);
+          queue[at].y = static_cast<uint32_t>(i0) + 64 * u + lane;
+        }
+        have += __popcll(found);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = t[u] - lo;
-        const bool in = k >= 0 && k < nk;
+      const bool last = i0 + 64 * U >= run1;
+      int taken = 0;
+#pragma unroll 1
+      for (; have - taken >= 64 || (last && taken < have); taken += 64) {
+        const bool in = lane < have - taken;
+        const uint32_t k = queue[taken + (in ? lane : 0)].x, pos = queue[taken + (in ? lane : 0)].y;
         uint64_t same = __ballot(in);
-        if (same == 0) continue;
+        uint32_t same0 = static_cast<uint32_t>(same), same1 = static_cast<uint32_t>(same >> 32);
+#pragma unroll 1
         for (int b = 0; b < A.bits; ++b) {  // the lanes with this lane's token
-          const bool set = (k >> b) & 1;
-          const uint64_t with = __ballot(set);
-          same &= set ? with : ~with;
+          const uint64_t with = __ballot((k >> b) & 1);
+          const uint32_t flip = ((k >> b) & 1) - 1;  // lanes with the bit keep `with`, those without its complement
+          same0 &= static_cast<uint32_t>(with) ^ flip;
+          same1 &= static_cast<uint32_t>(with >> 32) ^ flip;
         }
         if (in) {
-          const int at = mine[k], earlier = lanes_below(same, lane);
-          A.recs[at + earlier] = {static_cast<int32_t>(i0) + u * 64 + lane, k + lo, slot[k], end[k]};
-          if (earlier == 0) mine[k] = at + __popcll(same);
+          same = static_cast<uint64_t>(same1) << 32 | same0;
+          const int at = mine[W * k], earlier = lanes_below(same, lane);
+          A.recs[at + earlier] = {static_cast<int32_t>(pos), lo + static_cast<int32_t>(k), slot[k], end[k]};
+          if (earlier == 0) mine[W * k] = at + __popcll(same);
         }
       }
+      if (taken < have && taken > 0) {  // fewer than 64 are left: to the front
+        const bool in = lane < have - taken;
+        const uint32_t k = queue[taken + (in ? lane : 0)].x, pos = queue[taken + (in ? lane : 0)].y;
+        if (in) {
+          queue[lane].x = k;
+          queue[lane].y = pos;
+        }
+      }
+      have = max(0, have - taken);
     }
   }
 
-  if (A.grad == nullptr) return;
-  // Rows without a token, a wave each, the segments' blocks in turn (all of a
-  // token's records end behind its first one, so an empty token's end is where
-  // the next one starts).
-  for (int k = wave * A.segments + segment; k < nk; k += kSortWaves * A.segments) {
-    if (end[k] != (k > 0 ? end[k - 1] : first)) continue;
-    const float zero[8] = {};
-    if (A.grad_f32) {
-      float* const row = static_cast<float*>(A.grad) + int64_t(lo + k) * A.grad_ld;
-      for (int c = lane * 8; c < A.cols; c += 512) store8(row + c, A.cols - c, zero);
-    } else {
-      uint16_t* const row = static_cast<uint16_t*>(A.grad) + int64_t(lo + k) * A.grad_ld;
-      for (int c = lane * 8; c < A.cols; c += 512) store8(row + c, A.cols - c, zero);
-    }
-  }
+  if (A.present == nullptr || segment != 0) return;
+  // all of a token's records end behind its first one, so an empty token's end is where the next one starts
+  for (int k = tid; k < nk; k += kSortThreads) A.present[lo + k] = end[k] != (k > 0 ? end[k - 1] : first);
 }
 
 // -------------------------------------------------------------------- sum
@@ -385,9 +439,13 @@ struct SumArgs {
   float* tail;      // [chunk][ld_part]: the first part of a token that goes on in the next chunk
   int64_t ld_part;
   int64_t n;        // records, live and not
-  int32_t cols, slabs, chunks, chunk, range, ranges;
+  const uint8_t* present;  // dense form
+  int32_t cols, slabs, chunks, chunk, range, ranges, vocab;
+  int32_t sum_blocks;      // the blocks behind them clear rows
   float scale;
 };
+
+constexpr int kClearRows = 16;  // of a wave
 
 __device__ __forceinline__ int wave_sum(int x) {
 #pragma unroll
@@ -460,11 +518,31 @@ template <> struct Raw<uint16_t> {
   }
 };
 
+// Clears the rows of tokens that do not occur. They run beside the sums, not
+// in the sort (which has the time that the batch's frequent tokens take, and
+// no use for HBM).
+template <typename G>
+__device__ __forceinline__ void clear_rows(const SumArgs& A, int block, int lane) {
+  const int r0 = (block * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kClearRows;
+  if (r0 >= A.vocab) return;
+  const int r = min(r0 + lane, A.vocab - 1);
+  const bool clear = lane < kClearRows && r0 + lane < A.vocab && A.present[r] == 0;
+  const float zero[8] = {};
+  for (uint64_t todo = __ballot(clear); todo; todo &= todo - 1) {
+    G* const row = static_cast<G*>(A.grad) + int64_t(r0 + __builtin_ctzll(todo)) * A.grad_ld;
+    for (int c = lane * 8; c < A.cols; c += 512) store8(row + c, A.cols - c, zero);
+  }
+}
+
 template <typename D, typename G, int MODE>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(SumArgs A) {
   const int lane = threadIdx.x & 63;
+  if (MODE == kDense && int(blockIdx.x) >= A.sum_blocks) {
+    clear_rows<G>(A, blockIdx.x - A.sum_blocks, lane);
+    return;
+  }
   const int64_t id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + int64_t(blockIdx.x) * (kThreads / 64);
-  if (MODE == kRows && id == 0) {
+  if (MODE == kRows && id == 0) {  // (there is a block without tokens, too)
     const int total = distinct_in(A.distinct, 0, A.ranges, lane);
     if (lane == 0) *A.count = total;
   }
@@ -671,7 +749,7 @@ struct Sizes {
   int32_t chunk, chunks;  // sum: records of a chunk, chunks
   int32_t slabs;
   int64_t ld_part;
-  size_t recs, distinct, live, head, tail, total;  // byte offsets, and the whole
+  size_t recs, distinct, live, present, head, tail, total;  // byte offsets, and the whole
 };
 
 // Sort: a block per CU, ranges times segments of the batch. Segments split the
@@ -702,8 +780,9 @@ Sizes sizes_of(int64_t vocab, int64_t cols, int64_t n) {
   const size_t part = up(size_t(most) * size_t(s.ld_part) * sizeof(float));
   s.recs = 0;
   s.distinct = s.recs + up(size_t(n) * sizeof(Rec));
-  s.live = s.distinct + up(size_t(s.ranges) * sizeof(int32_t));
-  s.head = s.live + 256;
+  s.live = s.distinct + up(size_t(std::max<int64_t>(least, kSortBlocks)) * sizeof(int32_t));
+  s.present = s.live + 256;
+  s.head = s.present + up(size_t(vocab));
   s.tail = s.head + part;
   s.total = s.tail + part;
   return s;
@@ -799,7 +878,11 @@ void launch_lookup(const LookArgs& a, bool wide, unsigned grid, hipStream_t s) {
 template <typename D, typename G, int MODE>
 muon_status launch_sum(const SumArgs& a, hipStream_t s) {
   const int64_t waves = int64_t(a.chunks) * a.slabs;
-  hipLaunchKernelGGL((embed_sum_kernel<D, G, MODE>), dim3(unsigned((waves + 3) / 4)), dim3(kThreads), 0, s, a);
+  constexpr int each = kThreads / 64, rows = each * kClearRows;
+  SumArgs b = a;
+  b.sum_blocks = static_cast<int32_t>(std::max<int64_t>(MODE == kRows ? 1 : 0, (waves + each - 1) / each));
+  const int64_t clear = MODE == kDense ? (int64_t(a.vocab) + rows - 1) / rows : 0;
+  hipLaunchKernelGGL((embed_sum_kernel<D, G, MODE>), dim3(unsigned(b.sum_blocks + clear)), dim3(kThreads), 0, s, b);
   muon_status st = launched();
   if (st != MUON_OK || a.chunks < 2) return st;
   hipLaunchKernelGGL((embed_join_kernel<G, MODE>), dim3(unsigned(waves)), dim3(kThreads), 0, s, a);
@@ -822,17 +905,14 @@ muon_status run_gradient(muon_embed_plan* p, const muon_embed_tokens* tokens, co
   a.recs = reinterpret_cast<Rec*>(w + z.recs);
   a.distinct = reinterpret_cast<int32_t*>(w + z.distinct);
   a.live = reinterpret_cast<int32_t*>(w + z.live);
-  a.grad = mode == kDense ? grad : nullptr;
-  a.grad_ld = grad_ld;
-  a.grad_f32 = p->dtype == MUON_F32;
+  a.present = mode == kDense ? reinterpret_cast<uint8_t*>(w + z.present) : nullptr;
   a.n = static_cast<int32_t>(tokens->n);
   a.vocab = static_cast<int32_t>(p->t.vocab);
-  a.cols = static_cast<int32_t>(p->t.cols);
   a.range = z.range;
   a.segments = z.segments;
   a.run = z.run;
   while ((1 << a.bits) < z.range) ++a.bits;
-  const size_t lds = size_t(kSortWaves + 2) * size_t(z.range) * sizeof(int32_t);
+  const size_t lds = (size_t(kSortWaves + 2) * size_t(z.range) + 3) / 4 * 16;  // cleared 16 bytes at a time
   if (tokens->wide)
     hipLaunchKernelGGL(embed_sort_kernel<int64_t>, dim3(unsigned(z.ranges * z.segments)), dim3(kSortThreads), lds, s, a);
   else
@@ -853,14 +933,16 @@ muon_status run_gradient(muon_embed_plan* p, const muon_embed_tokens* tokens, co
   b.tail = reinterpret_cast<float*>(w + z.tail);
   b.ld_part = z.ld_part;
   b.n = tokens->n;
-  b.cols = a.cols;
+  b.present = a.present;
+  b.vocab = a.vocab;
+  b.cols = static_cast<int32_t>(p->t.cols);
   b.slabs = z.slabs;
   b.chunk = z.chunk;
-  b.chunks = std::max(1, z.chunks);  // no token: one wave that leaves the count
+  b.chunks = z.chunks;
   b.range = z.range;
   b.ranges = z.ranges;
   b.scale = scale;
-  if (mode != kRows && tokens->n == 0) return MUON_OK;
+  if (mode == kAdd && tokens->n == 0) return MUON_OK;
   if (mode == kDense) return launch_sum<kDense>(b, dout->dtype, p->dtype, s);
   if (mode == kAdd) return launch_sum<kAdd>(b, dout->dtype, p->dtype, s);
   return launch_sum<kRows>(b, dout->dtype, p->dtype, s);

@@ -75,9 +75,9 @@ def test_workspace_grows_with_the_batch(lib):
             size = mu.muon_embed_workspace_bytes(vocab, cols, n)
             assert size >= last and size > 0
             last = size
-    # the records (16 bytes a token) and the partial sums (two rows a chunk)
+    # the records (16 bytes a token), the partial sums (two rows a chunk) and a byte for every table row
     n = mu.muon_embed_workspace_bytes(50257, 768, 32768)
-    assert 32768 * 16 <= n <= 32768 * 16 + 2 * 1366 * 768 * 4 + 4096
+    assert 32768 * 16 <= n <= 32768 * 16 + 2 * 1366 * 768 * 4 + 50257 + 8192
     for bad in ((0, 1, 1), (1, 0, 1), (1, 1, -1), ((1 << 24) + 1, 1, 1), (1, 65537, 1), (1, 1, (1 << 24) + 1)):
         with pytest.raises(mu.MuonError):
             mu.muon_embed_workspace_bytes(*bad)
