@@ -24,8 +24,8 @@
  * become X <- (Q_s .. Q_1) X, Q_i = a I + b A_i + c A_i^2, A_{i+1} = Q_i A_i Q_i,
  * so that X is read and written once per s steps instead of once per product.
  * After s steps A is formed anew from X: s is chosen from the polynomial so
- * that rounding errors of A grow by less than 2^8 (bf16 sets) or 2^3 (fp32
- * sets) within a run of s (three and one steps for the usual quintic, seven
+ * that rounding errors of A grow by less than 2^15 (bf16 sets) or 2^3 (fp32
+ * sets) within a run of s (five and one steps for the usual quintic, thirteen
  * and three for the cubic).
  *
  * Arithmetic: buf' is the exact mu * buf + G rounded once to the set's dtype,

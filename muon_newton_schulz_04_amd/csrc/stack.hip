@@ -74,7 +74,7 @@ struct Args {
   char* ws;
   const float* gscale;
   float a, b, c, mu, eps, lr, wd;
-  int32_t nesterov, use_mom, apply;
+  int32_t nesterov, use_mom;
   int32_t runs, each, more;  // runs of steps: `each` steps, the first `more` of them one more
   int32_t run;               // the run this launch belongs to
 };
@@ -95,9 +95,10 @@ template <int MT> struct Cfg {
   static constexpr int lds_k = mp * ks * 4;
   static constexpr int lds_stage = 4 * (mp * (cols + 4) > cols * (mp + 4) ? mp * (cols + 4) : cols * (mp + 4));
   static constexpr int lds_second = lds_k > lds_stage ? lds_k : lds_stage;
+  static constexpr int lds_gram = MT == 1 && lds_k < waves * 4096 ? waves * 4096 : lds_k;
   static constexpr int lds_tile = lds_m + lds_second;
-  static constexpr int lds_solve = 2 * mp * ms * 4;
-  static constexpr int lds_whole = lds_tile > lds_solve ? lds_tile : lds_solve;
+  static constexpr int square = 2 * mp * mp;           // halves of an mp x mp matrix in the solve, hi and lo
+  static constexpr int lds_solve = (MT == 4 ? 2 : 3) * square * 2;
 };
 
 // ------------------------------------------------------------- elementwise
@@ -110,52 +111,32 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // round to n
 }
 __device__ __forceinline__ float round_bf16(float a) { return __uint_as_float(pack_bf16(a, 0.f) << 16); }
 
-// Eight consecutive elements, the first n of them if fewer are left (zeros behind).
-__device__ __forceinline__ void load8(const uint16_t* p, int n, float (&x)[8]) {
-  if (n >= 8) {
-    const u32x4_u w = *reinterpret_cast<const u32x4_u*>(p);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      x[2 * q] = __uint_as_float(w[q] << 16);
-      x[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = q < n ? bf2f(p[q]) : 0.f;
+// Eight consecutive elements as they lie in memory.
+template <typename T> struct Raw;
+template <> struct Raw<uint16_t> {
+  u32x4_u v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_u*>(p); }
+  __device__ __forceinline__ float get(int q) const { return __uint_as_float(q & 1 ? v[q >> 1] & 0xffff0000u : v[q >> 1] << 16); }
+};
+template <> struct Raw<float> {
+  f32x4_u v, w;
+  __device__ __forceinline__ void load(const float* p) {
+    v = *reinterpret_cast<const f32x4_u*>(p);
+    w = *reinterpret_cast<const f32x4_u*>(p + 4);
   }
+  __device__ __forceinline__ float get(int q) const { return q < 4 ? v[q] : w[q - 4]; }
+};
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf2f(*p); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ void store1(uint16_t* p, float x) { *p = static_cast<uint16_t>(pack_bf16(x, 0.f)); }
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+  const u32x4_u w = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+  *reinterpret_cast<u32x4_u*>(p) = w;
 }
-__device__ __forceinline__ void load8(const float* p, int n, float (&x)[8]) {
-  if (n >= 8) {
-    const f32x4_u a = *reinterpret_cast<const f32x4_u*>(p), b = *reinterpret_cast<const f32x4_u*>(p + 4);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      x[q] = a[q];
-      x[q + 4] = b[q];
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = q < n ? p[q] : 0.f;
-  }
-}
-__device__ __forceinline__ void store8(uint16_t* p, int n, const float (&x)[8]) {
-  if (n >= 8) {
-    const u32x4_u w = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
-    *reinterpret_cast<u32x4_u*>(p) = w;
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q < n) p[q] = static_cast<uint16_t>(pack_bf16(x[q], 0.f));
-  }
-}
-__device__ __forceinline__ void store8(float* p, int n, const float (&x)[8]) {
-  if (n >= 8) {
-    *reinterpret_cast<f32x4_u*>(p) = f32x4_u{x[0], x[1], x[2], x[3]};
-    *reinterpret_cast<f32x4_u*>(p + 4) = f32x4_u{x[4], x[5], x[6], x[7]};
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q < n) p[q] = x[q];
-  }
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  *reinterpret_cast<f32x4_u*>(p) = f32x4_u{x[0], x[1], x[2], x[3]};
+  *reinterpret_cast<f32x4_u*>(p + 4) = f32x4_u{x[4], x[5], x[6], x[7]};
 }
 
 // mu b + g rounded once to the buffer's type. fp32: the fused multiply-add.
@@ -177,16 +158,25 @@ __device__ __forceinline__ float momentum(float mu, float b, float g, const uint
   return round_bf16(s);
 }
 
-// The exponent e of |x| in [2^e, 2^(e+1)), in [-126, 127].
-__device__ __forceinline__ int exponent(float x) {
-  const int e = static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127;
-  return min(max(e, -126), 127);
+// The exponent e of x >= 0 (its bits) in [2^e, 2^(e+1)), in [-126, 127].
+__device__ __forceinline__ int exponent(int bits) { return min(max((bits >> 23) - 127, -126), 127); }
+
+// The largest of the lanes' numbers (none negative), for all of them.
+__device__ __forceinline__ int wave_max(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true));  // row_shr:1, 2, 4, 8
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xf, 0xf, true));  // row_bcast:15, 31
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xf, 0xf, true));
+  return __builtin_amdgcn_readlane(v, 63);
 }
 
 // x = hi + lo, two of them at once, as packed pairs.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const f16x2 h = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
-  const f16x2 l = {static_cast<_Float16>(x - static_cast<float>(h[0])), static_cast<_Float16>(y - static_cast<float>(h[1]))};
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const f16x2 h = __builtin_convertvector((f2{x, y}), f16x2);
+  const f16x2 l = __builtin_convertvector((f2{x - static_cast<float>(h[0]), y - static_cast<float>(h[1])}), f16x2);
   hi = __builtin_bit_cast(uint32_t, h);
   lo = __builtin_bit_cast(uint32_t, l);
 }
@@ -208,15 +198,94 @@ __device__ __forceinline__ Spot spot(int tid) {
   return {r, r + C::threads / vpr, c};
 }
 
-// Elements of the tile's row r from c on that exist (0 .. 8), and where they are.
-template <bool TALL>
-__device__ __forceinline__ int extent(const Mat& M, int k0, int r, int c) {
-  const int row = TALL ? k0 + r : r, rows = TALL ? M.n : M.m, left = TALL ? M.m - c : M.n - (k0 + c);
-  return row < rows ? left : 0;
+// Where a thread's two vectors are in memory. A vector that would reach over a
+// row's end is moved back to end with it (`back` elements, eight or more: it
+// has none of its own), a row that does not exist is the last one: the loads
+// need no branch, and fix() puts the values in their places. NARROW: memory
+// rows of under eight elements, which are loaded one by one.
+template <bool TALL, bool NARROW>
+struct Frame {
+  int64_t ra, rb;  // elements from the matrix's first, without the row's part
+  int c, back;
+  bool oka, okb;
+  __device__ __forceinline__ Frame(const Mat& M, int k0, const Spot& s) {
+    const int rows = TALL ? M.n : M.m, len = TALL ? M.m : M.n, r0 = TALL ? k0 : 0, at = TALL ? s.c : k0 + s.c;
+    c = NARROW ? min(at, len - 1) : min(at, len - 8);
+    back = at - c;
+    oka = r0 + s.ra < rows;
+    okb = r0 + s.rb < rows;
+    ra = min(r0 + s.ra, rows - 1);
+    rb = min(r0 + s.rb, rows - 1);
+  }
+};
+// Whether a tile reaches over the matrix's sides.
+template <int MT>
+__device__ __forceinline__ bool at_edge(const Mat& M, int k0) {
+  return M.m < Cfg<MT>::mp || k0 + Cfg<MT>::cols > M.n;
 }
-template <bool TALL>
-__device__ __forceinline__ int64_t place(int64_t ld, int k0, int r, int c) {
-  return TALL ? int64_t(k0 + r) * ld + c : int64_t(r) * ld + (k0 + c);
+
+template <typename T, bool TALL, bool NARROW>
+__device__ __forceinline__ void fetch(const void* base, int64_t ld, const Mat& M, const Frame<TALL, NARROW>& f, Raw<T> (&x)[2]) {
+  const T* const a = static_cast<const T*>(base) + f.ra * ld + f.c;
+  const T* const b = static_cast<const T*>(base) + f.rb * ld + f.c;
+  if constexpr (!NARROW) {
+    x[0].load(a);
+    x[1].load(b);
+  } else {
+    // the row's elements from c on, the last of them again behind its end
+    const int left = (TALL ? M.m : M.n) - 1 - f.c;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int at = min(q, left);
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t u = uint32_t(a[at]), v = uint32_t(b[at]);
+        x[0].v[q >> 1] = q & 1 ? x[0].v[q >> 1] | u << 16 : u;
+        x[1].v[q >> 1] = q & 1 ? x[1].v[q >> 1] | v << 16 : v;
+      } else if (q < 4) {
+        x[0].v[q] = a[at];
+        x[1].v[q] = b[at];
+      } else {
+        x[0].w[q - 4] = a[at];
+        x[1].w[q - 4] = b[at];
+      }
+    }
+  }
+}
+
+// How many elements of the vector are the thread's own: [0, mine) once they
+// are in their places (NARROW: they already are).
+template <bool TALL, bool NARROW>
+__device__ __forceinline__ int own(const Mat& M, const Frame<TALL, NARROW>& f, bool ok) {
+  if (!ok) return 0;
+  if (NARROW) return f.back > 0 ? 0 : min(8, (TALL ? M.m : M.n) - f.c);
+  return max(0, 8 - f.back);
+}
+// Moves a vector's values `back` places to the front; zeros where nothing is the thread's own.
+template <bool TALL, bool NARROW>
+__device__ __forceinline__ void fix(const Mat& M, const Frame<TALL, NARROW>& f, bool ok, float (&x)[8]) {
+  const int n = own(M, f, ok);
+  if constexpr (!NARROW) {
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = f.back & s ? (q + s < 8 ? x[q + s] : 0.f) : x[q];
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) x[q] = q < n ? x[q] : 0.f;
+}
+// Stores the thread's own elements of a row; the values are in their places.
+template <typename T, bool TALL, bool NARROW>
+__device__ __forceinline__ void put_row(void* base, int64_t ld, const Mat& M, const Frame<TALL, NARROW>& f, int64_t row, bool ok, bool edge, const float (&x)[8]) {
+  T* const p = static_cast<T*>(base) + row * ld + f.c + f.back;
+  if (!NARROW && !edge) {
+    store8(p, x);
+    return;
+  }
+  const int n = own(M, f, ok);
+  if (n == 8) store8(p, x);
+  else
+    for (int q = 0; q < 7; ++q)
+      if (q < n) store1(p + q, x[q]);
 }
 
 // Writes a thread's 2 x 8 values (scaled to fp16's range) as hi and lo.
@@ -336,59 +405,82 @@ __device__ __forceinline__ void put_gram(const Args& A, const Mat& M, int part, 
 
 // ------------------------------------------------------------------ phases
 
-// G times the plan's factor, and u from it; FIRST: the momentum is read,
-// updated and written, else it has been.
-template <typename T, bool TALL, bool FIRST>
-__device__ __forceinline__ void load_u(const Args& A, const Mat& M, int k0, int r, int c, float gs, float (&u)[8]) {
-  const int n = extent<TALL>(M, k0, r, c);
-  if (n <= 0) {
+// What a launch's u depends on.
+struct Step {
+  float gs, mu;
+  bool use_mom, nesterov;
+  __device__ __forceinline__ Step(const Args& A) : gs(A.gscale ? *A.gscale : 1.f), mu(A.mu), use_mom(A.use_mom), nesterov(A.nesterov) {}
+};
+// u of a vector from the gradient and the momentum as loaded; FIRST: the
+// momentum's new value is left in nb. (Without momentum the second operand is
+// the gradient again: it is loaded, and not used.)
+template <typename T, bool FIRST>
+__device__ __forceinline__ void form_u(const Step& S, const Raw<T>& g, const Raw<T>& b, float (&u)[8], float (&nb)[8]) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) u[q] = 0.f;
-    return;
+  for (int q = 0; q < 8; ++q) u[q] = g.get(q) * S.gs;
+  if (!S.use_mom) return;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    nb[q] = FIRST ? momentum(S.mu, b.get(q), u[q], static_cast<const T*>(nullptr)) : b.get(q);
+    u[q] = S.nesterov ? __fmaf_rn(S.mu, nb[q], u[q]) : nb[q];
   }
-  const int64_t at = place<TALL>(M.ld, k0, r, c);
-  load8(static_cast<const T*>(M.g) + at, n, u);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) u[q] *= gs;
-  if (!A.use_mom) return;
-  float b[8];
-  T* const buf = static_cast<T*>(M.b) + at;
-  load8(buf, n, b);
-  if constexpr (FIRST) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) b[q] = momentum(A.mu, b[q], u[q], buf);
-    store8(buf, n, b);
-  }
-#pragma unroll
-  for (int q = 0; q < 8; ++q) u[q] = A.nesterov ? __fmaf_rn(A.mu, b[q], u[q]) : b[q];
 }
+
+// A tile's gradient and momentum on their way.
+template <typename T, bool TALL, bool NARROW>
+struct Load {
+  Raw<T> g[2], b[2];
+  __device__ __forceinline__ void start(const Mat& M, const void* b2, int k0, const Spot& s) {
+    const Frame<TALL, NARROW> f(M, k0, s);
+    fetch<T>(M.g, M.ld, M, f, g);
+    fetch<T>(b2, M.ld, M, f, b);
+  }
+};
 
 // Phase gram over the part's columns. The operands are scaled by a power of
 // two that puts the largest |u| so far into [2^12, 2^13): when a tile raises
-// it, the sums so far are rescaled, which is exact.
-template <typename T, int MT, bool TALL>
+// it, the sums so far are rescaled, which is exact. Two tiles are on their way
+// while one is worked on.
+template <typename T, int MT, bool TALL, bool NARROW>
 __device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Part& p, char* lds) {
   typedef Cfg<MT> C;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   _Float16* const hi = reinterpret_cast<_Float16*>(lds);
   _Float16* const lo = hi + C::mp * C::ks;
   __shared__ int top[C::waves];
-  const float gs = A.gscale ? *A.gscale : 1.f;
+  const Step S(A);
+  const void* const b2 = S.use_mom ? M.b : M.g;
   // a wide matrix's rows are the tile's; of a tall one they are its columns
   const Spot s = spot<MT, !TALL, TALL>(tid);
   f32x16 acc[C::tiles] = {};
   int e = -126;
-  for (int t = p.beg; t < p.end; ++t) {
+  Load<T, TALL, NARROW> x, y;
+  auto start = [&](Load<T, TALL, NARROW>& l, int t) { l.start(M, b2, min(t, p.end - 1) * C::cols, s); };
+  auto work = [&](Load<T, TALL, NARROW>& l, int t) {
     const int k0 = t * C::cols;
-    float u[2][8];
-    load_u<T, TALL, true>(A, M, k0, s.ra, s.c, gs, u[0]);
-    load_u<T, TALL, true>(A, M, k0, s.rb, s.c, gs, u[1]);
+    const bool edge = at_edge<MT>(M, k0);
+    const Frame<TALL, NARROW> f(M, k0, s);
+    float u[2][8], nb[2][8];
+    form_u<T, true>(S, l.g[0], l.b[0], u[0], nb[0]);
+    form_u<T, true>(S, l.g[1], l.b[1], u[1], nb[1]);
+    if (NARROW || edge) {
+      fix(M, f, f.oka, u[0]);
+      fix(M, f, f.okb, u[1]);
+      if (S.use_mom) {
+        fix(M, f, f.oka, nb[0]);
+        fix(M, f, f.okb, nb[1]);
+      }
+    }
+    if (S.use_mom) {
+      put_row<T>(M.b, M.ld, M, f, f.ra, f.oka, edge, nb[0]);
+      put_row<T>(M.b, M.ld, M, f, f.rb, f.okb, edge, nb[1]);
+    }
+    start(l, t + 2);
     float big = 0.f;
 #pragma unroll
     for (int q = 0; q < 8; ++q) big = fmaxf(big, fmaxf(fabsf(u[0][q]), fabsf(u[1][q])));
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
-    if (lane == 0) top[wave] = exponent(big);
+    const int most = wave_max(__float_as_int(big));
+    if (lane == 0) top[wave] = exponent(most);
     __syncthreads();  // the tile of the pass before has been read, too
     int now = e;
 #pragma unroll
@@ -408,53 +500,106 @@ __device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Pa
     put_tile<!TALL>(hi, lo, C::ks, s, u);
     __syncthreads();
     gram_tile<MT>(hi, lo, acc, wave, lane);
+  };
+  start(x, p.beg);
+  start(y, p.beg + 1);
+  for (int t = p.beg; t < p.end; t += 2) {
+    work(x, t);
+    if (t + 1 >= p.end) break;
+    work(y, t + 1);
   }
   put_gram<MT>(A, M, p.index, acc, lds, wave, lane);
   if (tid == 0) reinterpret_cast<int32_t*>(A.ws + M.exp_off)[p.index] = e;
 }
 
+// The solve's matrices: mp x mp, hi then lo, in rows of 2 mp bytes without
+// padding (three of 64 x 64 let three workgroups share a CU). The 16-byte
+// chunks of a row are exchanged so that the same chunk of 16 rows in turn lies
+// in all banks.
 template <int MT>
-__device__ __forceinline__ void mul_lds(const _Float16* x, const _Float16* y, f32x16 (&acc)[Cfg<MT>::tiles], float scale, int wave, int lane) {
+__device__ __forceinline__ int chunk_at(int row, int c) {
+  constexpr int n = 4 * MT;  // chunks of a row
+  return row * (8 * n) + ((c ^ (MT == 1 ? row >> 2 : MT == 2 ? row >> 1 : row)) & (n - 1)) * 8;
+}
+template <int MT>
+__device__ __forceinline__ f16x8 frag_sq(const _Float16* x, int row, int k, int lane) {
+  return *reinterpret_cast<const f16x8*>(x + chunk_at<MT>(row + (lane & 31), (k >> 3) + (lane >> 5)));
+}
+
+// acc = scale * (X Y^T), and with TWO also bcc = scale2 * (Z Y^T), for the
+// matrices as they are stored. Cross terms have accumulators of their own: a
+// chain of dependent products half as long.
+template <int MT, bool TWO>
+__device__ __forceinline__ void mul_sq(const _Float16* x, const _Float16* z, const _Float16* y, f32x16 (&acc)[Cfg<MT>::tiles], f32x16 (&bcc)[Cfg<MT>::tiles],
+                                       float scale, float scale2, int wave, int lane) {
   typedef Cfg<MT> C;
+  constexpr int lo = C::mp * C::mp, kUnroll = MT == 4 ? 2 : 4;
   int ti, tj;
   tile_of<MT>(wave, ti, tj);
+  f32x16 a1[C::tiles] = {}, a2[C::tiles] = {}, b1[C::tiles] = {}, b2[C::tiles] = {};
+  if (MT > 1 || wave == 0) {
+#pragma unroll kUnroll
+    for (int k = 0; k < C::mp; k += 16) {
+      const f16x8 xh = frag_sq<MT>(x, 32 * ti, k, lane), xl = frag_sq<MT>(x + lo, 32 * ti, k, lane);
+      f16x8 zh, zl;
+      if (TWO) zh = frag_sq<MT>(z, 32 * ti, k, lane), zl = frag_sq<MT>(z + lo, 32 * ti, k, lane);
 #pragma unroll
-  for (int t = 0; t < C::tiles; ++t) acc[t] = f32x16{};
-  if (MT == 1 && wave > 0) return;
-#pragma unroll 2
-  for (int k = 0; k < C::mp; k += 16) {
-    const f16x8 xh = frag(x, 32 * ti, C::ms, k, lane), xl = frag(x + C::mp * C::ms, 32 * ti, C::ms, k, lane);
-#pragma unroll
-    for (int t = 0; t < C::tiles; ++t) {
-      const f16x8 yh = frag(y, 32 * (tj + t), C::ms, k, lane), yl = frag(y + C::mp * C::ms, 32 * (tj + t), C::ms, k, lane);
-      acc[t] = mul3(xh, xl, yh, yl, acc[t]);
+      for (int t = 0; t < C::tiles; ++t) {
+        const f16x8 yh = frag_sq<MT>(y, 32 * (tj + t), k, lane), yl = frag_sq<MT>(y + lo, 32 * (tj + t), k, lane);
+        a1[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh, yh, a1[t], 0, 0, 0);
+        a2[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh, yl, a2[t], 0, 0, 0);
+        a2[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xl, yh, a2[t], 0, 0, 0);
+        if (TWO) {
+          b1[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(zh, yh, b1[t], 0, 0, 0);
+          b2[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(zh, yl, b2[t], 0, 0, 0);
+          b2[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(zl, yh, b2[t], 0, 0, 0);
+        }
+      }
     }
   }
 #pragma unroll
   for (int t = 0; t < C::tiles; ++t)
 #pragma unroll
-    for (int q = 0; q < 16; ++q) acc[t][q] *= scale;
+    for (int q = 0; q < 16; ++q) {
+      acc[t][q] = (a1[t][q] + a2[t][q]) * scale;
+      if (TWO) bcc[t][q] = (b1[t][q] + b2[t][q]) * scale2;
+    }
 }
 
 template <int MT>
-__device__ __forceinline__ void put_lds(_Float16* x, const f32x16 (&v)[Cfg<MT>::tiles], float scale, int wave, int lane) {
+__device__ __forceinline__ void put_sq(_Float16* x, const f32x16 (&v)[Cfg<MT>::tiles], float scale, int wave, int lane) {
   typedef Cfg<MT> C;
   int ti, tj;
   tile_of<MT>(wave, ti, tj);
   if (MT == 1 && wave > 0) return;
 #pragma unroll
-  for (int t = 0; t < C::tiles; ++t) put_acc(x, x + C::mp * C::ms, C::ms, 32 * ti, 32 * (tj + t), v[t], scale, lane);
+  for (int t = 0; t < C::tiles; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint2 h, l;
+      split2(v[t][4 * g] * scale, v[t][4 * g + 1] * scale, h.x, l.x);
+      split2(v[t][4 * g + 2] * scale, v[t][4 * g + 3] * scale, h.y, l.y);
+      // row 32 (tj + t) + lane % 32, columns from 32 ti + 8 g + 4 (lane / 32)
+      const int at = chunk_at<MT>(32 * (tj + t) + (lane & 31), 4 * ti + g) + 4 * (lane >> 5);
+      *reinterpret_cast<uint2*>(x + at) = h;
+      *reinterpret_cast<uint2*>(x + C::mp * C::mp + at) = l;
+    }
 }
 
 // Phase solve: A from its parts, the norm (first run), the run's steps on A
-// and P. All matrices are symmetric, so a product X Y is X Y^T, and a tile
-// may be stored transposed.
+// and P. The matrices are symmetric but for rounding, and are stored
+// transposed (put_sq), so a product of two as stored is X^T Y. The order of
+// the factors matters for that rounding: T = A^T Q, A' = T^T Q = Q^T A Q and P' =
+// P^T Q keep the antisymmetric part of A's errors from growing faster than the
+// rest (with T = Q^T A it grew by 14 in every step of the quintic: X off by
+// 4e-4 after five steps on full-rank 64 x 768, 1e-5 in this order).
 template <int MT>
 __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run, char* lds) {
   typedef Cfg<MT> C;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  _Float16* const l1 = reinterpret_cast<_Float16*>(lds);
-  _Float16* const l2 = l1 + 2 * C::mp * C::ms;
+  _Float16* const la = reinterpret_cast<_Float16*>(lds);  // A, T
+  _Float16* const lq = la + C::square;                    // Q
+  _Float16* const lp = MT == 4 ? la : lq + C::square;     // P (mp = 128: where A was, for its product)
   __shared__ float red[C::waves];
   int ti, tj;
   tile_of<MT>(wave, ti, tj);
@@ -481,6 +626,8 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
           a[t][4 * g + 3] += ldexpf(x.w, shift);
         }
     }
+  // the identity's elements of this lane, for a I
+  auto diag = [&](int t, int i) { return ti == tj + t && acc_row(i >> 2, lane) + (i & 3) == (lane & 31); };
   float scale = 1.f / (kAScale * kAScale);  // X was scaled by 2^kXExp
   if (run == 0) {
     // the trace is the sum of squares
@@ -489,7 +636,7 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
     for (int t = 0; t < C::tiles; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (mine && ti == tj + t && acc_row(i >> 2, lane) + (i & 3) == (lane & 31)) d += a[t][i];
+        if (mine && diag(t, i)) d += a[t][i];
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) d += __shfl_xor(d, o, 64);
     if (lane == 0) red[wave] = d;
@@ -511,20 +658,21 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
   for (int t = 0; t < C::tiles; ++t)
 #pragma unroll
     for (int i = 0; i < 16; ++i) a[t][i] *= scale;
-  // the identity's elements of this lane, for a I
-  auto diag = [&](int t, int i) { return ti == tj + t && acc_row(i >> 2, lane) + (i & 3) == (lane & 31); };
   const int steps = A.each + (run < A.more ? 1 : 0);
   if (steps == 0) {
 #pragma unroll
     for (int t = 0; t < C::tiles; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) pr[t][i] = diag(t, i) ? 1.f : 0.f;
+  } else {
+    put_sq<MT>(la, a, kAScale, wave, lane);
+    __syncthreads();
   }
-  if (steps > 0) put_lds<MT>(l1, a, kAScale, wave, lane);
-  __syncthreads();
+  constexpr float kAQ = 1.f / (kAScale * kPScale), kPQ = 1.f / (kPScale * kPScale);
+#pragma unroll 1
   for (int i = 0; i < steps; ++i) {
     const bool more = i + 1 < steps;
-    mul_lds<MT>(l1, l1, acc, 1.f / (kAScale * kAScale), wave, lane);
+    mul_sq<MT, false>(la, la, la, acc, acc, 1.f / (kAScale * kAScale), 0.f, wave, lane);
 #pragma unroll
     for (int t = 0; t < C::tiles; ++t)
 #pragma unroll
@@ -534,24 +682,46 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
       for (int t = 0; t < C::tiles; ++t) pr[t] = q[t];
       if (!more) break;
     }
-    put_lds<MT>(l2, q, kPScale, wave, lane);
-    __syncthreads();
-    if (more) {
-      mul_lds<MT>(l2, l1, acc, 1.f / (kAScale * kPScale), wave, lane);
+    put_sq<MT>(lq, q, kPScale, wave, lane);
+    if constexpr (MT != 4) {
+      if (i == 0) {
+        put_sq<MT>(lp, pr, kPScale, wave, lane);
+        __syncthreads();
+        mul_sq<MT, false>(la, la, lq, acc, acc, kAQ, 0.f, wave, lane);
+      } else {
+        __syncthreads();
+        if (!more) {
+          mul_sq<MT, false>(lp, lp, lq, pr, pr, kPQ, 0.f, wave, lane);
+          break;
+        }
+        mul_sq<MT, true>(la, lp, lq, acc, pr, kAQ, kPQ, wave, lane);
+      }
       __syncthreads();
-      put_lds<MT>(l1, acc, kAScale, wave, lane);
+      put_sq<MT>(la, acc, kAScale, wave, lane);
+      if (i > 0) put_sq<MT>(lp, pr, kPScale, wave, lane);
       __syncthreads();
-      mul_lds<MT>(l1, l2, a, 1.f / (kAScale * kPScale), wave, lane);
-    }
-    if (i > 0) {
+      mul_sq<MT, false>(la, la, lq, a, a, kAQ, 0.f, wave, lane);
       __syncthreads();
-      put_lds<MT>(l1, pr, kPScale, wave, lane);
+      put_sq<MT>(la, a, kAScale, wave, lane);
       __syncthreads();
-      mul_lds<MT>(l2, l1, pr, 1.f / (kPScale * kPScale), wave, lane);
-    }
-    __syncthreads();
-    if (more) {
-      put_lds<MT>(l1, a, kAScale, wave, lane);
+    } else {
+      __syncthreads();
+      if (more) {
+        mul_sq<MT, false>(la, la, lq, acc, acc, kAQ, 0.f, wave, lane);
+        __syncthreads();
+        put_sq<MT>(la, acc, kAScale, wave, lane);
+        __syncthreads();
+        mul_sq<MT, false>(la, la, lq, a, a, kAQ, 0.f, wave, lane);
+      }
+      if (i > 0) {
+        __syncthreads();
+        put_sq<MT>(lp, pr, kPScale, wave, lane);
+        __syncthreads();
+        mul_sq<MT, false>(lp, lp, lq, pr, pr, kPQ, 0.f, wave, lane);
+      }
+      if (!more) break;
+      __syncthreads();
+      put_sq<MT>(la, a, kAScale, wave, lane);
       __syncthreads();
     }
   }
@@ -562,9 +732,18 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
   }
 }
 
+// What a tile of P X needs on its way: the gradient and momentum, or X, and
+// for the last run's weights those.
+template <typename T, bool TALL, bool NARROW, bool GRAD, bool WEIGHTS>
+struct ApplyLoad {
+  Load<T, TALL, NARROW> u;
+  Raw<float> x[2];
+  Raw<T> w[2];
+};
+
 // P X for the part's columns: GRAD: X is sigma u, from the gradients, else what
 // the run before left. LAST: out or the weights, else X and its X X^T.
-template <typename T, int MT, bool TALL, bool GRAD, bool LAST>
+template <typename T, int MT, bool TALL, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS>
 __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const Part& p, char* lds) {
   typedef Cfg<MT> C;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -574,13 +753,15 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
   _Float16* const kl = kh + C::mp * C::ks;
   float* const stage = reinterpret_cast<float*>(lds + C::lds_m);
   const int mi = wave % MT, ki = wave / MT;  // the wave's rows of X and columns of the tile, in 32s
-  const float gs = A.gscale ? *A.gscale : 1.f;
+  const Step S(A);
+  const void* const b2 = S.use_mom ? M.b : M.g;
   float f = 1.f / (kAScale * kPScale);
   int e = 0;
   if (GRAD) {
     f = reinterpret_cast<const float*>(A.ws + M.rec_off)[0] * (1.f / kPScale);
     e = reinterpret_cast<const int32_t*>(A.ws + M.rec_off)[1];
   }
+  const float keep = 1.f - (A.lr * M.lr_mul) * (A.wd * M.wd_mul), step = A.lr * M.lr_mul;
   f16x8 ph[C::mp / 16], pl[C::mp / 16];
   const _Float16* const pm = reinterpret_cast<const _Float16*>(A.ws + M.p_off);
 #pragma unroll
@@ -591,25 +772,49 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
   float* const xs = reinterpret_cast<float*>(A.ws + M.x_off);
   constexpr bool kRowsAreK = TALL || !GRAD;  // memory rows are columns of X
   const Spot s = spot<MT, !kRowsAreK, !kRowsAreK>(tid);
+  const Spot o = spot<MT, !TALL, false>(tid);
   f32x16 acc2[C::tiles] = {};
-  for (int t = p.beg; t < p.end; ++t) {
+  typedef ApplyLoad<T, TALL, NARROW, GRAD, WEIGHTS> L;
+  L x, y;
+  auto start = [&](L& l, int t) {
+    const int k0 = min(t, p.end - 1) * C::cols;
+    if constexpr (GRAD) {
+      l.u.start(M, b2, k0, s);
+    } else {
+      l.x[0].load(xs + int64_t(k0 + s.ra) * C::mp + s.c);
+      l.x[1].load(xs + int64_t(k0 + s.rb) * C::mp + s.c);
+    }
+  };
+  auto start_w = [&](L& l, int t) {
+    if constexpr (LAST && WEIGHTS) {
+      const Frame<TALL, NARROW> fr(M, min(t, p.end - 1) * C::cols, o);
+      fetch<T>(M.w, M.wld, M, fr, l.w);
+    }
+  };
+  auto work = [&](L& l, int t) {
     const int k0 = t * C::cols;
+    const bool edge = at_edge<MT>(M, k0);
     float u[2][8];
     if constexpr (GRAD) {
-      load_u<T, TALL, false>(A, M, k0, s.ra, s.c, gs, u[0]);
-      load_u<T, TALL, false>(A, M, k0, s.rb, s.c, gs, u[1]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) u[j][q] = ldexpf(u[j][q], kXExp - e);
+      float nb[2][8];
+      form_u<T, false>(S, l.u.g[0], l.u.b[0], u[0], nb[0]);
+      form_u<T, false>(S, l.u.g[1], l.u.b[1], u[1], nb[1]);
+      if (NARROW || edge) {
+        const Frame<TALL, NARROW> fr(M, k0, s);
+        fix(M, fr, fr.oka, u[0]);
+        fix(M, fr, fr.okb, u[1]);
+      }
     } else {
-      load8(xs + int64_t(k0 + s.ra) * C::mp + s.c, 8, u[0]);
-      load8(xs + int64_t(k0 + s.rb) * C::mp + s.c, 8, u[1]);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) u[j][q] *= kAScale;
+        for (int q = 0; q < 8; ++q) u[j][q] = l.x[j].get(q);
     }
+    start(l, t + 2);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) u[j][q] = GRAD ? ldexpf(u[j][q], kXExp - e) : u[j][q] * kAScale;
     put_tile<kRowsAreK>(mh, ml, C::ms, s, u);
     __syncthreads();
     f32x16 acc = {};
@@ -639,49 +844,61 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
         }
       }
       __syncthreads();
-      const Spot o = spot<MT, !TALL, false>(tid);
+      const Frame<TALL, NARROW> fr(M, k0, o);
+      float w[2][8];
+      if constexpr (WEIGHTS) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) w[j][q] = l.w[j].get(q);
+          if (NARROW || edge) fix(M, fr, j ? fr.okb : fr.oka, w[j]);
+        }
+        start_w(l, t + 2);
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int r = j ? o.rb : o.ra, n = extent<TALL>(M, k0, r, o.c);
-        if (n <= 0) continue;
-        const float* const in = stage + r * ((TALL ? C::mp : C::cols) + 4) + o.c;
-        float x[8];
-        load8(in, 8, x);
-        if (A.apply) {
-          const float keep = 1.f - (A.lr * M.lr_mul) * (A.wd * M.wd_mul), step = A.lr * M.lr_mul;
-          T* const w = static_cast<T*>(M.w) + place<TALL>(M.wld, k0, r, o.c);
-          float y[8];
-          load8(w, n, y);
+        const f32x4* const in = reinterpret_cast<const f32x4*>(stage + (j ? o.rb : o.ra) * ((TALL ? C::mp : C::cols) + 4) + o.c);
+        const f32x4 a = in[0], b = in[1];
+        float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        if constexpr (WEIGHTS) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) x[q] = __fmaf_rn(-step, x[q], y[q] * keep);
-          store8(w, n, x);
-        } else {
-          store8(static_cast<T*>(M.o) + place<TALL>(M.ld, k0, r, o.c), n, x);
+          for (int q = 0; q < 8; ++q) v[q] = __fmaf_rn(-step, v[q], w[j][q] * keep);
         }
+        put_row<T>(WEIGHTS ? M.w : M.o, WEIGHTS ? M.wld : M.ld, M, fr, j ? fr.rb : fr.ra, j ? fr.okb : fr.oka, edge, v);
       }
     }
+  };
+  start(x, p.beg);
+  start_w(x, p.beg);
+  start(y, p.beg + 1);
+  start_w(y, p.beg + 1);
+  for (int t = p.beg; t < p.end; t += 2) {
+    work(x, t);
+    if (t + 1 >= p.end) break;
+    work(y, t + 1);
   }
   if constexpr (!LAST) put_gram<MT>(A, M, p.index, acc2, lds, wave, lane);
 }
 
-template <typename T, int MT, bool GRAD, bool LAST>
+// The matrix's direction is the workgroup's own matter; the rest is the launch's.
+template <typename T, int MT, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS>
 __device__ __forceinline__ void apply_any(const Args& A, const Mat& M, const Part& p, char* lds) {
-  if (M.tall) phase_apply<T, MT, true, GRAD, LAST>(A, M, p, lds);
-  else phase_apply<T, MT, false, GRAD, LAST>(A, M, p, lds);
+  if (M.tall) phase_apply<T, MT, true, NARROW, GRAD, LAST, WEIGHTS>(A, M, p, lds);
+  else phase_apply<T, MT, false, NARROW, GRAD, LAST, WEIGHTS>(A, M, p, lds);
 }
-template <typename T, int MT>
+template <typename T, int MT, bool NARROW>
 __device__ __forceinline__ void gram_any(const Args& A, const Mat& M, const Part& p, char* lds) {
-  if (M.tall) phase_gram<T, MT, true>(A, M, p, lds);
-  else phase_gram<T, MT, false>(A, M, p, lds);
+  if (M.tall) phase_gram<T, MT, true, NARROW>(A, M, p, lds);
+  else phase_gram<T, MT, false, NARROW>(A, M, p, lds);
 }
 
 // ----------------------------------------------------------------- kernels
 
-template <typename T, int MT>
+template <typename T, int MT, bool NARROW>
 __global__ __launch_bounds__(Cfg<MT>::threads) void stack_gram_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
   const Part p = A.parts[blockIdx.x];
-  gram_any<T, MT>(A, A.mats[p.mat], p, lds);
+  gram_any<T, MT, NARROW>(A, A.mats[p.mat], p, lds);
 }
 
 template <int MT>
@@ -690,38 +907,22 @@ __global__ __launch_bounds__(Cfg<MT>::threads) void stack_solve_kernel(Args A, i
   phase_solve<MT>(A, A.mats[first + blockIdx.x], A.run, lds);
 }
 
-template <typename T, int MT, bool GRAD, bool LAST>
+template <typename T, int MT, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS>
 __global__ __launch_bounds__(Cfg<MT>::threads) void stack_apply_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
   const Part p = A.parts[blockIdx.x];
-  apply_any<T, MT, GRAD, LAST>(A, A.mats[p.mat], p, lds);
-}
-
-// A matrix a workgroup: all phases in one launch.
-template <typename T, int MT>
-__global__ __launch_bounds__(Cfg<MT>::threads) void stack_whole_kernel(Args A) {
-  extern __shared__ __align__(16) char lds[];
-  const Part p = A.parts[blockIdx.x];
-  const Mat& M = A.mats[p.mat];
-  gram_any<T, MT>(A, M, p, lds);
-  for (int run = 0; run < A.runs; ++run) {
-    __syncthreads();  // what the phase before wrote to the workspace is read by other waves
-    phase_solve<MT>(A, M, run, lds);
-    __syncthreads();
-    const bool last = run + 1 == A.runs;
-    if (run == 0 && last) apply_any<T, MT, true, true>(A, M, p, lds);
-    else if (run == 0) apply_any<T, MT, true, false>(A, M, p, lds);
-    else if (!last) phase_apply<T, MT, false, false, false>(A, M, p, lds);
-    else apply_any<T, MT, false, true>(A, M, p, lds);
-  }
+  apply_any<T, MT, NARROW, GRAD, LAST, WEIGHTS>(A, A.mats[p.mat], p, lds);
 }
 
 // -------------------------------------------------------------------- host
 
-constexpr int kClasses = 3;  // mp = 32, 64, 128
-int class_of(int64_t m) { return m <= 32 ? 0 : m <= 64 ? 1 : 2; }
-int mp_of(int cls) { return 32 << cls; }
-int cols_of(int cls) { return cls == 0 ? 128 : 64; }
+constexpr int kClasses = 4;  // mp = 32 with memory rows of under eight elements, 32, 64, 128
+int class_of(const muon_stack& s) {
+  const int64_t m = std::min(s.rows, s.cols);
+  return s.cols < 8 ? 0 : m <= 32 ? 1 : m <= 64 ? 2 : 3;
+}
+int mp_of(int cls) { return cls < 2 ? 32 : 16 << cls; }
+int cols_of(int cls) { return cls < 2 ? 128 : 64; }
 
 struct Host {
   muon_dtype dtype = MUON_BF16;
@@ -731,7 +932,6 @@ struct Host {
   std::vector<int64_t> index;          // its place in it
   std::vector<Part> parts;             // by class
   int32_t mat_beg[kClasses + 1] = {}, part_beg[kClasses + 1] = {};
-  bool whole[kClasses] = {};
   size_t ws_bytes = 0;
 };
 
@@ -788,9 +988,6 @@ muon_status validate(const muon_stack* st, int32_t n, muon_dtype dtype, const mu
   return muon::tensor_overlap::overlaps(iv) ? MUON_E_INVALID : MUON_OK;
 }
 
-// One launch with a matrix a workgroup where there are enough of them to fill
-// the CUs; otherwise the columns are split into parts.
-constexpr int64_t kWholeMats = 256;
 constexpr int64_t kMaxParts = 64;
 constexpr int64_t kTargetParts = 1024;
 
@@ -810,18 +1007,14 @@ muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
   for (int cls = 0; cls < kClasses; ++cls) {
     H->mat_beg[cls] = static_cast<int32_t>(H->mats.size());
     H->part_beg[cls] = static_cast<int32_t>(H->parts.size());
-    int64_t count = 0, tiles = 0;
+    int64_t tiles = 0;
     const int64_t cols = cols_of(cls), mp = mp_of(cls);
     for (int32_t i = 0; i < n; ++i)
-      if (!empty(st[i]) && class_of(std::min(st[i].rows, st[i].cols)) == cls) {
-        count += st[i].count;
-        tiles += st[i].count * ((std::max(st[i].rows, st[i].cols) + cols - 1) / cols);
-      }
-    H->whole[cls] = count >= kWholeMats;
+      if (!empty(st[i]) && class_of(st[i]) == cls) tiles += st[i].count * ((std::max(st[i].rows, st[i].cols) + cols - 1) / cols);
     const int64_t each = std::max<int64_t>(1, (tiles + kTargetParts - 1) / kTargetParts);
     for (int32_t i = 0; i < n; ++i) {
       const muon_stack& s = st[i];
-      if (empty(s) || class_of(std::min(s.rows, s.cols)) != cls) continue;
+      if (empty(s) || class_of(s) != cls) continue;
       for (int64_t t = 0; t < s.count; ++t) {
         Mat M{};
         M.g = static_cast<const char*>(s.grad) + t * s.stride * es;
@@ -832,7 +1025,7 @@ muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
         M.n = static_cast<int32_t>(std::max(s.rows, s.cols));
         M.tall = s.rows > s.cols;
         const int64_t nt = (M.n + cols - 1) / cols;
-        const int64_t per = H->whole[cls] ? nt : std::max(each, (nt + kMaxParts - 1) / kMaxParts);
+        const int64_t per = std::max(each, (nt + kMaxParts - 1) / kMaxParts);
         M.parts = static_cast<int32_t>((nt + per - 1) / per);
         M.gram_off = take(M.parts * mp * mp * 4);
         M.exp_off = take(M.parts * 4);
@@ -869,7 +1062,7 @@ int run_length(const muon_config& c, muon_dtype dtype) {
       x *= q;
     }
   }
-  const double limit = dtype == MUON_F32 ? 8.0 : 256.0;
+  const double limit = dtype == MUON_F32 ? 8.0 : 32768.0;
   int s = 1;
   double grown = slope, size = top * top;
   while (s < c.steps && grown <= limit && size <= 4096.0) {
@@ -902,7 +1095,7 @@ muon_status go(K kernel, unsigned grid, int threads, int lds, hipStream_t s, con
   return hipGetLastError() == hipSuccess ? MUON_OK : MUON_E_LAUNCH;
 }
 
-template <typename T, int MT>
+template <typename T, int MT, bool NARROW, bool WEIGHTS>
 muon_status run_class(const muon_stack_plan_s* p, int cls, Args a, hipStream_t s) {
   typedef Cfg<MT> C;
   const Host& H = p->host;
@@ -910,28 +1103,28 @@ muon_status run_class(const muon_stack_plan_s* p, int cls, Args a, hipStream_t s
   if (mats == 0) return MUON_OK;
   const unsigned parts = unsigned(H.part_beg[cls + 1] - H.part_beg[cls]);
   a.parts = p->d_parts + H.part_beg[cls];
-  if (H.whole[cls]) return go(stack_whole_kernel<T, MT>, parts, C::threads, C::lds_whole, s, a);
-  muon_status st = go(stack_gram_kernel<T, MT>, parts, C::threads, C::lds_tile, s, a);
+  muon_status st = go(stack_gram_kernel<T, MT, NARROW>, parts, C::threads, C::lds_gram, s, a);
   for (int run = 0; run < a.runs && st == MUON_OK; ++run) {
     a.run = run;
     hipLaunchKernelGGL(stack_solve_kernel<MT>, dim3(unsigned(mats)), dim3(C::threads), C::lds_solve, s, a, H.mat_beg[cls]);
     if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
     const bool last = run + 1 == a.runs;
     if (run == 0)
-      st = last ? go(stack_apply_kernel<T, MT, true, true>, parts, C::threads, C::lds_tile, s, a)
-                : go(stack_apply_kernel<T, MT, true, false>, parts, C::threads, C::lds_tile, s, a);
+      st = last ? go(stack_apply_kernel<T, MT, NARROW, true, true, WEIGHTS>, parts, C::threads, C::lds_tile, s, a)
+                : go(stack_apply_kernel<T, MT, NARROW, true, false, false>, parts, C::threads, C::lds_tile, s, a);
     else
-      st = last ? go(stack_apply_kernel<T, MT, false, true>, parts, C::threads, C::lds_tile, s, a)
-                : go(stack_apply_kernel<T, MT, false, false>, parts, C::threads, C::lds_tile, s, a);
+      st = last ? go(stack_apply_kernel<T, MT, NARROW, false, true, WEIGHTS>, parts, C::threads, C::lds_tile, s, a)
+                : go(stack_apply_kernel<T, MT, NARROW, false, false, false>, parts, C::threads, C::lds_tile, s, a);
   }
   return st;
 }
 
-template <typename T>
+template <typename T, bool WEIGHTS>
 muon_status run_all(const muon_stack_plan_s* p, const Args& a, hipStream_t s) {
-  muon_status st = run_class<T, 1>(p, 0, a, s);
-  if (st == MUON_OK) st = run_class<T, 2>(p, 1, a, s);
-  if (st == MUON_OK) st = run_class<T, 4>(p, 2, a, s);
+  muon_status st = run_class<T, 1, true, WEIGHTS>(p, 0, a, s);
+  if (st == MUON_OK) st = run_class<T, 1, false, WEIGHTS>(p, 1, a, s);
+  if (st == MUON_OK) st = run_class<T, 2, false, WEIGHTS>(p, 2, a, s);
+  if (st == MUON_OK) st = run_class<T, 4, false, WEIGHTS>(p, 3, a, s);
   return st;
 }
 
@@ -960,7 +1153,6 @@ muon_status step(muon_stack_plan_s* p, const muon_config* cfg, const muon_apply*
   a.eps = cfg->eps;
   a.nesterov = cfg->nesterov;
   a.use_mom = cfg->momentum != 0.f;
-  a.apply = ap != nullptr;
   if (ap != nullptr) {
     a.lr = ap->lr;
     a.wd = ap->wd;
@@ -970,7 +1162,8 @@ muon_status step(muon_stack_plan_s* p, const muon_config* cfg, const muon_apply*
   a.each = cfg->steps / a.runs;
   a.more = cfg->steps % a.runs;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return H.dtype == MUON_F32 ? run_all<float>(p, a, s) : run_all<uint16_t>(p, a, s);
+  if (H.dtype == MUON_F32) return ap ? run_all<float, true>(p, a, s) : run_all<float, false>(p, a, s);
+  return ap ? run_all<uint16_t, true>(p, a, s) : run_all<uint16_t, false>(p, a, s);
 }
 
 }  // namespace
