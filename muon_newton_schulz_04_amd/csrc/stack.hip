@@ -101,42 +101,53 @@ template <int MT> struct Cfg {
   static constexpr int lds_solve = (MT == 4 ? 2 : 3) * square * 2;
 };
 
+// A barrier that orders LDS alone: __syncthreads() would also wait for the
+// global loads on their way (no wave reads what another has stored to global
+// memory in the same launch).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // ------------------------------------------------------------- elementwise
 
-__device__ __forceinline__ float bf2f(uint32_t h) { return __uint_as_float(h << 16); }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // round to nearest even
   typedef float f2 __attribute__((ext_vector_type(2)));
   typedef __bf16 b2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
 }
-__device__ __forceinline__ float round_bf16(float a) { return __uint_as_float(pack_bf16(a, 0.f) << 16); }
+
+// The matrices' pointers come from a table in memory: unless told, the
+// compiler takes them for flat ones, whose accesses count as LDS accesses, too,
+// and are waited for with them.
+#define MUON_GLOBAL __attribute__((address_space(1)))
+template <typename T> using global = MUON_GLOBAL T;
 
 // Eight consecutive elements as they lie in memory.
 template <typename T> struct Raw;
 template <> struct Raw<uint16_t> {
   u32x4_u v;
-  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_u*>(p); }
+  __device__ __forceinline__ void load(const global<uint16_t>* p) { v = *reinterpret_cast<const global<u32x4_u>*>(p); }
   __device__ __forceinline__ float get(int q) const { return __uint_as_float(q & 1 ? v[q >> 1] & 0xffff0000u : v[q >> 1] << 16); }
 };
 template <> struct Raw<float> {
   f32x4_u v, w;
-  __device__ __forceinline__ void load(const float* p) {
-    v = *reinterpret_cast<const f32x4_u*>(p);
-    w = *reinterpret_cast<const f32x4_u*>(p + 4);
+  __device__ __forceinline__ void load(const global<float>* p) {
+    v = *reinterpret_cast<const global<f32x4_u>*>(p);
+    w = *reinterpret_cast<const global<f32x4_u>*>(p + 4);
   }
   __device__ __forceinline__ float get(int q) const { return q < 4 ? v[q] : w[q - 4]; }
 };
-__device__ __forceinline__ float load1(const uint16_t* p) { return bf2f(*p); }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ void store1(uint16_t* p, float x) { *p = static_cast<uint16_t>(pack_bf16(x, 0.f)); }
-__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+__device__ __forceinline__ void store1(global<uint16_t>* p, float x) { *p = static_cast<uint16_t>(pack_bf16(x, 0.f)); }
+__device__ __forceinline__ void store1(global<float>* p, float x) { *p = x; }
+__device__ __forceinline__ void store8(global<uint16_t>* p, const float (&x)[8]) {
   const u32x4_u w = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
-  *reinterpret_cast<u32x4_u*>(p) = w;
+  *reinterpret_cast<global<u32x4_u>*>(p) = w;
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  *reinterpret_cast<f32x4_u*>(p) = f32x4_u{x[0], x[1], x[2], x[3]};
-  *reinterpret_cast<f32x4_u*>(p + 4) = f32x4_u{x[4], x[5], x[6], x[7]};
+__device__ __forceinline__ void store8(global<float>* p, const float (&x)[8]) {
+  *reinterpret_cast<global<f32x4_u>*>(p) = f32x4_u{x[0], x[1], x[2], x[3]};
+  *reinterpret_cast<global<f32x4_u>*>(p + 4) = f32x4_u{x[4], x[5], x[6], x[7]};
 }
 
 // mu b + g rounded once to the buffer's type. fp32: the fused multiply-add.
@@ -144,18 +155,37 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 // it again is the nearest bf16 unless s lies half way between two of them and
 // the exact value does not. Then the sign of the exact remainder (float64:
 // the product is exact, the sum splits exactly into S + E, and so does S - s)
-// moves s off the halfway point.
-__device__ __forceinline__ float momentum(float mu, float b, float g, const float*) { return __fmaf_rn(mu, b, g); }
-__device__ __forceinline__ float momentum(float mu, float b, float g, const uint16_t*) {
-  const float s = __fmaf_rn(mu, b, g);
+// moves s off the halfway point. One element in 2^16 lies there: a vector is
+// rounded plainly, and again if one of its elements does.
+__device__ __forceinline__ float off_halfway(float mu, float b, float g, float s) {
   const uint32_t bits = __float_as_uint(s);
-  if ((bits & 0xffffu) == 0x8000u) {
-    const double p = __dmul_rn(double(mu), double(b)), big = __dadd_rn(p, double(g)), part = __dsub_rn(big, p);
-    const double rest = __dadd_rn(__dsub_rn(p, __dsub_rn(big, part)), __dsub_rn(double(g), part));
-    const double off = __dadd_rn(__dsub_rn(big, double(s)), rest);
-    if (off > 0.0 || off < 0.0) return round_bf16(__uint_as_float((off > 0.0) == (s > 0.0) ? bits + 1u : bits - 1u));
+  if ((bits & 0xffffu) != 0x8000u) return s;
+  const double p = __dmul_rn(double(mu), double(b)), big = __dadd_rn(p, double(g)), part = __dsub_rn(big, p);
+  const double rest = __dadd_rn(__dsub_rn(p, __dsub_rn(big, part)), __dsub_rn(double(g), part));
+  const double off = __dadd_rn(__dsub_rn(big, double(s)), rest);
+  return off > 0.0 || off < 0.0 ? __uint_as_float((off > 0.0) == (s > 0.0) ? bits + 1u : bits - 1u) : s;
+}
+__device__ __forceinline__ void momentum(float mu, const Raw<float>& b, const float (&g)[8], float (&nb)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) nb[q] = __fmaf_rn(mu, b.get(q), g[q]);
+}
+__device__ __forceinline__ void momentum(float mu, const Raw<uint16_t>& b, const float (&g)[8], float (&nb)[8]) {
+  bool tie = false;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    nb[q] = __fmaf_rn(mu, b.get(q), g[q]);
+    tie |= static_cast<uint16_t>(__float_as_uint(nb[q])) == uint16_t(0x8000);
   }
-  return round_bf16(s);
+  if (__builtin_expect(tie, 0)) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) nb[q] = off_halfway(mu, b.get(q), g[q], nb[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < 8; q += 2) {
+    const uint32_t r = pack_bf16(nb[q], nb[q + 1]);
+    nb[q] = __uint_as_float(r << 16);
+    nb[q + 1] = __uint_as_float(r & 0xffff0000u);
+  }
 }
 
 // The exponent e of x >= 0 (its bits) in [2^e, 2^(e+1)), in [-126, 127].
@@ -226,8 +256,8 @@ __device__ __forceinline__ bool at_edge(const Mat& M, int k0) {
 
 template <typename T, bool TALL, bool NARROW>
 __device__ __forceinline__ void fetch(const void* base, int64_t ld, const Mat& M, const Frame<TALL, NARROW>& f, Raw<T> (&x)[2]) {
-  const T* const a = static_cast<const T*>(base) + f.ra * ld + f.c;
-  const T* const b = static_cast<const T*>(base) + f.rb * ld + f.c;
+  const global<T>* const a = (const global<T>*)base + f.ra * ld + f.c;
+  const global<T>* const b = (const global<T>*)base + f.rb * ld + f.c;
   if constexpr (!NARROW) {
     x[0].load(a);
     x[1].load(b);
@@ -276,7 +306,7 @@ __device__ __forceinline__ void fix(const Mat& M, const Frame<TALL, NARROW>& f, 
 // Stores the thread's own elements of a row; the values are in their places.
 template <typename T, bool TALL, bool NARROW>
 __device__ __forceinline__ void put_row(void* base, int64_t ld, const Mat& M, const Frame<TALL, NARROW>& f, int64_t row, bool ok, bool edge, const float (&x)[8]) {
-  T* const p = static_cast<T*>(base) + row * ld + f.c + f.back;
+  global<T>* const p = (global<T>*)base + row * ld + f.c + f.back;
   if (!NARROW && !edge) {
     store8(p, x);
     return;
@@ -382,10 +412,10 @@ __device__ __forceinline__ void put_gram(const Args& A, const Mat& M, int part, 
   float4* const out = reinterpret_cast<float4*>(A.ws + M.gram_off) + int64_t(part) * (C::mp * C::mp / 4);
   if constexpr (MT == 1) {
     float4* const red = reinterpret_cast<float4*>(lds);
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int g = 0; g < 4; ++g) red[(wave * 4 + g) * 64 + lane] = make_float4(acc[0][4 * g], acc[0][4 * g + 1], acc[0][4 * g + 2], acc[0][4 * g + 3]);
-    __syncthreads();
+    lds_barrier();
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < C::waves; ++w) {
@@ -393,7 +423,7 @@ __device__ __forceinline__ void put_gram(const Args& A, const Mat& M, int part, 
       s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
     }
     out[wave * 64 + lane] = s;
-    __syncthreads();
+    lds_barrier();
   } else {
 #pragma unroll
     for (int t = 0; t < C::tiles; ++t)
@@ -419,11 +449,14 @@ __device__ __forceinline__ void form_u(const Step& S, const Raw<T>& g, const Raw
 #pragma unroll
   for (int q = 0; q < 8; ++q) u[q] = g.get(q) * S.gs;
   if (!S.use_mom) return;
+  if constexpr (FIRST) {
+    momentum(S.mu, b, u, nb);
+  } else {
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    nb[q] = FIRST ? momentum(S.mu, b.get(q), u[q], static_cast<const T*>(nullptr)) : b.get(q);
-    u[q] = S.nesterov ? __fmaf_rn(S.mu, nb[q], u[q]) : nb[q];
+    for (int q = 0; q < 8; ++q) nb[q] = b.get(q);
   }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) u[q] = S.nesterov ? __fmaf_rn(S.mu, nb[q], u[q]) : nb[q];
 }
 
 // A tile's gradient and momentum on their way.
@@ -481,7 +514,7 @@ __device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Pa
     for (int q = 0; q < 8; ++q) big = fmaxf(big, fmaxf(fabsf(u[0][q]), fabsf(u[1][q])));
     const int most = wave_max(__float_as_int(big));
     if (lane == 0) top[wave] = exponent(most);
-    __syncthreads();  // the tile of the pass before has been read, too
+    lds_barrier();  // the tile of the pass before has been read, too
     int now = e;
 #pragma unroll
     for (int w = 0; w < C::waves; ++w) now = max(now, top[w]);
@@ -498,10 +531,11 @@ __device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Pa
 #pragma unroll
       for (int q = 0; q < 8; ++q) u[j][q] = ldexpf(u[j][q], kXExp - e);
     put_tile<!TALL>(hi, lo, C::ks, s, u);
-    __syncthreads();
+    lds_barrier();
     gram_tile<MT>(hi, lo, acc, wave, lane);
   };
   start(x, p.beg);
+  __builtin_amdgcn_sched_barrier(0);  // loads are waited for in the order they went out
   start(y, p.beg + 1);
   for (int t = p.beg; t < p.end; t += 2) {
     work(x, t);
@@ -640,7 +674,7 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) d += __shfl_xor(d, o, 64);
     if (lane == 0) red[wave] = d;
-    __syncthreads();
+    lds_barrier();
     float sum = 0.f;
 #pragma unroll
     for (int w = 0; w < C::waves; ++w) sum += red[w];
@@ -666,7 +700,7 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
       for (int i = 0; i < 16; ++i) pr[t][i] = diag(t, i) ? 1.f : 0.f;
   } else {
     put_sq<MT>(la, a, kAScale, wave, lane);
-    __syncthreads();
+    lds_barrier();
   }
   constexpr float kAQ = 1.f / (kAScale * kPScale), kPQ = 1.f / (kPScale * kPScale);
 #pragma unroll 1
@@ -686,43 +720,43 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
     if constexpr (MT != 4) {
       if (i == 0) {
         put_sq<MT>(lp, pr, kPScale, wave, lane);
-        __syncthreads();
+        lds_barrier();
         mul_sq<MT, false>(la, la, lq, acc, acc, kAQ, 0.f, wave, lane);
       } else {
-        __syncthreads();
+        lds_barrier();
         if (!more) {
           mul_sq<MT, false>(lp, lp, lq, pr, pr, kPQ, 0.f, wave, lane);
           break;
         }
         mul_sq<MT, true>(la, lp, lq, acc, pr, kAQ, kPQ, wave, lane);
       }
-      __syncthreads();
+      lds_barrier();
       put_sq<MT>(la, acc, kAScale, wave, lane);
       if (i > 0) put_sq<MT>(lp, pr, kPScale, wave, lane);
-      __syncthreads();
+      lds_barrier();
       mul_sq<MT, false>(la, la, lq, a, a, kAQ, 0.f, wave, lane);
-      __syncthreads();
+      lds_barrier();
       put_sq<MT>(la, a, kAScale, wave, lane);
-      __syncthreads();
+      lds_barrier();
     } else {
-      __syncthreads();
+      lds_barrier();
       if (more) {
         mul_sq<MT, false>(la, la, lq, acc, acc, kAQ, 0.f, wave, lane);
-        __syncthreads();
+        lds_barrier();
         put_sq<MT>(la, acc, kAScale, wave, lane);
-        __syncthreads();
+        lds_barrier();
         mul_sq<MT, false>(la, la, lq, a, a, kAQ, 0.f, wave, lane);
       }
       if (i > 0) {
-        __syncthreads();
+        lds_barrier();
         put_sq<MT>(lp, pr, kPScale, wave, lane);
-        __syncthreads();
+        lds_barrier();
         mul_sq<MT, false>(lp, lp, lq, pr, pr, kPQ, 0.f, wave, lane);
       }
       if (!more) break;
-      __syncthreads();
+      lds_barrier();
       put_sq<MT>(la, a, kAScale, wave, lane);
-      __syncthreads();
+      lds_barrier();
     }
   }
   if (mine) {
@@ -769,7 +803,7 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
     ph[k] = frag(pm, 32 * mi, C::mp, 16 * k, lane);
     pl[k] = frag(pm + C::mp * C::mp, 32 * mi, C::mp, 16 * k, lane);
   }
-  float* const xs = reinterpret_cast<float*>(A.ws + M.x_off);
+  global<float>* const xs = (global<float>*)(A.ws + M.x_off);
   constexpr bool kRowsAreK = TALL || !GRAD;  // memory rows are columns of X
   const Spot s = spot<MT, !kRowsAreK, !kRowsAreK>(tid);
   const Spot o = spot<MT, !TALL, false>(tid);
@@ -816,7 +850,7 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
 #pragma unroll
       for (int q = 0; q < 8; ++q) u[j][q] = GRAD ? ldexpf(u[j][q], kXExp - e) : u[j][q] * kAScale;
     put_tile<kRowsAreK>(mh, ml, C::ms, s, u);
-    __syncthreads();
+    lds_barrier();
     f32x16 acc = {};
 #pragma unroll
     for (int k = 0; k < C::mp / 16; ++k)
@@ -829,7 +863,7 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
       for (int i = 0; i < 16; ++i)
         xs[int64_t(k0 + 32 * ki + acc_row(i >> 2, lane) + (i & 3)) * C::mp + col] = acc[i];
       put_acc(kh, kl, C::ks, 32 * ki, 32 * mi, acc, kAScale, lane);
-      __syncthreads();
+      lds_barrier();
       gram_tile<MT>(kh, kl, acc2, wave, lane);
     } else {
       // through LDS, so that memory rows are written whole
@@ -843,7 +877,7 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
           *reinterpret_cast<f32x4*>(stage + col * (C::cols + 4) + row) = f32x4{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
         }
       }
-      __syncthreads();
+      lds_barrier();
       const Frame<TALL, NARROW> fr(M, k0, o);
       float w[2][8];
       if constexpr (WEIGHTS) {
@@ -870,6 +904,7 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
   };
   start(x, p.beg);
   start_w(x, p.beg);
+  __builtin_amdgcn_sched_barrier(0);  // loads are waited for in the order they went out
   start(y, p.beg + 1);
   start_w(y, p.beg + 1);
   for (int t = p.beg; t < p.end; t += 2) {
@@ -898,20 +933,23 @@ template <typename T, int MT, bool NARROW>
 __global__ __launch_bounds__(Cfg<MT>::threads) void stack_gram_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
   const Part p = A.parts[blockIdx.x];
-  gram_any<T, MT, NARROW>(A, A.mats[p.mat], p, lds);
+  const Mat M = A.mats[p.mat];  // by value: a reference would be read again after every store
+  gram_any<T, MT, NARROW>(A, M, p, lds);
 }
 
 template <int MT>
 __global__ __launch_bounds__(Cfg<MT>::threads) void stack_solve_kernel(Args A, int first) {
   extern __shared__ __align__(16) char lds[];
-  phase_solve<MT>(A, A.mats[first + blockIdx.x], A.run, lds);
+  const Mat M = A.mats[first + blockIdx.x];
+  phase_solve<MT>(A, M, A.run, lds);
 }
 
 template <typename T, int MT, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS>
 __global__ __launch_bounds__(Cfg<MT>::threads) void stack_apply_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
   const Part p = A.parts[blockIdx.x];
-  apply_any<T, MT, NARROW, GRAD, LAST, WEIGHTS>(A, A.mats[p.mat], p, lds);
+  const Mat M = A.mats[p.mat];
+  apply_any<T, MT, NARROW, GRAD, LAST, WEIGHTS>(A, M, p, lds);
 }
 
 // -------------------------------------------------------------------- host
