@@ -38,6 +38,8 @@ DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-p
 SOURCES = [("kernels.hip", True), ("adam.hip", True), ("clip.hip", True), ("embed.hip", True), ("stack.hip", True),
            ("noalloc.hip", True), ("api.cpp", False),
            ("plan.cpp", False)]
+# stack.hip works on its accumulators between products: held in accumulation registers they are copied there and back
+EXTRA = {"stack.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def run(cmd):
@@ -59,7 +61,7 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(OBJDIR, src + ".o")
         cmd = [cc, *COMMON]
         if device:
-            cmd += DEVICE + ["-x", "hip"]
+            cmd += DEVICE + EXTRA.get(src, []) + ["-x", "hip"]
         else:
             cmd += ["-x", "c++", "-D__HIP_PLATFORM_AMD__", f"-I{rocm_include()}"]
         cmd += ["-c", os.path.join(CSRC, src), "-o", obj]

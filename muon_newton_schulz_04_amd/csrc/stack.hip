@@ -63,7 +63,8 @@ struct Mat {
   float lr_mul, wd_mul;
 };
 
-// Columns [beg, end) of a matrix, in tiles.
+// Columns [beg, end) of a matrix, in tiles. A workgroup has parts [first, first
+// of the next).
 struct Part {
   int32_t mat, beg, end, index;
 };
@@ -71,6 +72,7 @@ struct Part {
 struct Args {
   const Mat* mats;
   const Part* parts;
+  const int32_t* first;  // per workgroup
   char* ws;
   const float* gscale;
   float a, b, c, mu, eps, lr, wd;
@@ -130,6 +132,11 @@ template <> struct Raw<uint16_t> {
   u32x4_u v;
   __device__ __forceinline__ void load(const global<uint16_t>* p) { v = *reinterpret_cast<const global<u32x4_u>*>(p); }
   __device__ __forceinline__ float get(int q) const { return __uint_as_float(q & 1 ? v[q >> 1] & 0xffff0000u : v[q >> 1] << 16); }
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = pack_bf16(x[2 * q], x[2 * q + 1]);
+  }
+  __device__ __forceinline__ void store(global<uint16_t>* p) const { *reinterpret_cast<global<u32x4_u>*>(p) = v; }
 };
 template <> struct Raw<float> {
   f32x4_u v, w;
@@ -138,54 +145,69 @@ template <> struct Raw<float> {
     w = *reinterpret_cast<const global<f32x4_u>*>(p + 4);
   }
   __device__ __forceinline__ float get(int q) const { return q < 4 ? v[q] : w[q - 4]; }
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+    v = f32x4_u{x[0], x[1], x[2], x[3]};
+    w = f32x4_u{x[4], x[5], x[6], x[7]};
+  }
+  __device__ __forceinline__ void store(global<float>* p) const {
+    *reinterpret_cast<global<f32x4_u>*>(p) = v;
+    *reinterpret_cast<global<f32x4_u>*>(p + 4) = w;
+  }
 };
 __device__ __forceinline__ void store1(global<uint16_t>* p, float x) { *p = static_cast<uint16_t>(pack_bf16(x, 0.f)); }
 __device__ __forceinline__ void store1(global<float>* p, float x) { *p = x; }
-__device__ __forceinline__ void store8(global<uint16_t>* p, const float (&x)[8]) {
-  const u32x4_u w = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
-  *reinterpret_cast<global<u32x4_u>*>(p) = w;
-}
-__device__ __forceinline__ void store8(global<float>* p, const float (&x)[8]) {
-  *reinterpret_cast<global<f32x4_u>*>(p) = f32x4_u{x[0], x[1], x[2], x[3]};
-  *reinterpret_cast<global<f32x4_u>*>(p + 4) = f32x4_u{x[4], x[5], x[6], x[7]};
-}
 
 // mu b + g rounded once to the buffer's type. fp32: the fused multiply-add.
-// bf16: s = fma(mu, b, g) is the float32 nearest to the exact value; rounding
-// it again is the nearest bf16 unless s lies half way between two of them and
-// the exact value does not. Then the sign of the exact remainder (float64:
-// the product is exact, the sum splits exactly into S + E, and so does S - s)
-// moves s off the halfway point. One element in 2^16 lies there: a vector is
-// rounded plainly, and again if one of its elements does.
-__device__ __forceinline__ float off_halfway(float mu, float b, float g, float s) {
-  const uint32_t bits = __float_as_uint(s);
-  if ((bits & 0xffffu) != 0x8000u) return s;
-  const double p = __dmul_rn(double(mu), double(b)), big = __dadd_rn(p, double(g)), part = __dsub_rn(big, p);
-  const double rest = __dadd_rn(__dsub_rn(p, __dsub_rn(big, part)), __dsub_rn(double(g), part));
-  const double off = __dadd_rn(__dsub_rn(big, double(s)), rest);
-  return off > 0.0 || off < 0.0 ? __uint_as_float((off > 0.0) == (s > 0.0) ? bits + 1u : bits - 1u) : s;
+// bf16: rounding the nearest float32 once more is wrong where it lies half way
+// between two bf16 numbers and the exact value does not (one element in a
+// hundred with mu = 0.95, so a wave always has one). Rounded to odd it is
+// right: of the float32 numbers below and above an inexact value the odd one,
+// which is never half way, and on the exact value's side of it. The two come
+// from the rounding modes of the fused multiply-add; the mode is changed and
+// restored within the asm, so no other instruction sees it.
+__device__ __forceinline__ void fma_odd(float mu, const float (&b)[4], const float (&g)[4], float (&x)[4]) {
+  float d[4], u[4];
+  asm("s_setreg_imm32_b32 hwreg(HW_REG_MODE, 0, 2), 2\n\t"  // float32: toward -infinity
+      "s_nop 1\n\t"
+      "v_fma_f32 %0, %8, %9, %13\n\t"
+      "v_fma_f32 %1, %8, %10, %14\n\t"
+      "v_fma_f32 %2, %8, %11, %15\n\t"
+      "v_fma_f32 %3, %8, %12, %16\n\t"
+      "s_setreg_imm32_b32 hwreg(HW_REG_MODE, 0, 2), 1\n\t"  // toward +infinity
+      "s_nop 1\n\t"
+      "v_fma_f32 %4, %8, %9, %13\n\t"
+      "v_fma_f32 %5, %8, %10, %14\n\t"
+      "v_fma_f32 %6, %8, %11, %15\n\t"
+      "v_fma_f32 %7, %8, %12, %16\n\t"
+      "s_setreg_imm32_b32 hwreg(HW_REG_MODE, 0, 2), 0\n\t"  // to nearest
+      "s_nop 1"
+      : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(u[0]), "=&v"(u[1]), "=&v"(u[2]), "=&v"(u[3])
+      : "v"(mu), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(g[0]), "v"(g[1]), "v"(g[2]), "v"(g[3]));
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t lo = __float_as_uint(d[q]), hi = __float_as_uint(u[q]);
+    const uint32_t odd = 0u - (lo & 1u);
+    x[q] = __uint_as_float((lo & odd) | (hi & ~odd));  // (equal where the value is exact; +0 for a sum of zero)
+  }
 }
-__device__ __forceinline__ void momentum(float mu, const Raw<float>& b, const float (&g)[8], float (&nb)[8]) {
+// nb: as stored.
+__device__ __forceinline__ void momentum(float mu, const Raw<float>& b, const float (&g)[8], Raw<float>& nb) {
+  float s[8];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) nb[q] = __fmaf_rn(mu, b.get(q), g[q]);
+  for (int q = 0; q < 8; ++q) s[q] = __fmaf_rn(mu, b.get(q), g[q]);
+  nb.set(s);
 }
-__device__ __forceinline__ void momentum(float mu, const Raw<uint16_t>& b, const float (&g)[8], float (&nb)[8]) {
-  bool tie = false;
+__device__ __forceinline__ void momentum(float mu, const Raw<uint16_t>& b, const float (&g)[8], Raw<uint16_t>& nb) {
+  float s[8];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    nb[q] = __fmaf_rn(mu, b.get(q), g[q]);
-    tie |= static_cast<uint16_t>(__float_as_uint(nb[q])) == uint16_t(0x8000);
-  }
-  if (__builtin_expect(tie, 0)) {
+  for (int h = 0; h < 8; h += 4) {
+    const float x[4] = {b.get(h), b.get(h + 1), b.get(h + 2), b.get(h + 3)}, y[4] = {g[h], g[h + 1], g[h + 2], g[h + 3]};
+    float z[4];
+    fma_odd(mu, x, y, z);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) nb[q] = off_halfway(mu, b.get(q), g[q], nb[q]);
+    for (int q = 0; q < 4; ++q) s[h + q] = z[q];
   }
-#pragma unroll
-  for (int q = 0; q < 8; q += 2) {
-    const uint32_t r = pack_bf16(nb[q], nb[q + 1]);
-    nb[q] = __uint_as_float(r << 16);
-    nb[q + 1] = __uint_as_float(r & 0xffff0000u);
-  }
+  nb.set(s);
 }
 
 // The exponent e of x >= 0 (its bits) in [2^e, 2^(e+1)), in [-126, 127].
@@ -206,7 +228,8 @@ __device__ __forceinline__ int wave_max(int v) {
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   typedef float f2 __attribute__((ext_vector_type(2)));
   const f16x2 h = __builtin_convertvector((f2{x, y}), f16x2);
-  const f16x2 l = __builtin_convertvector((f2{x - static_cast<float>(h[0]), y - static_cast<float>(h[1])}), f16x2);
+  // (x - h in one mixed-precision instruction; exact)
+  const f16x2 l = __builtin_convertvector((f2{__builtin_fmaf(static_cast<float>(h[0]), -1.f, x), __builtin_fmaf(static_cast<float>(h[1]), -1.f, y)}), f16x2);
   hi = __builtin_bit_cast(uint32_t, h);
   lo = __builtin_bit_cast(uint32_t, l);
 }
@@ -228,24 +251,34 @@ __device__ __forceinline__ Spot spot(int tid) {
   return {r, r + C::threads / vpr, c};
 }
 
-// Where a thread's two vectors are in memory. A vector that would reach over a
-// row's end is moved back to end with it (`back` elements, eight or more: it
-// has none of its own), a row that does not exist is the last one: the loads
-// need no branch, and fix() puts the values in their places. NARROW: memory
-// rows of under eight elements, which are loaded one by one.
+// Where a thread's two vectors are in memory, in elements from the matrix's
+// first. In a tile at the matrix's edge a vector that would reach over a row's
+// end is moved back to end with it (`back` elements, eight or more: it has none
+// of its own), and a row that does not exist is the last one: the loads need
+// no branch, and fix() puts the values in their places. NARROW: memory rows of
+// under eight elements, which are loaded one by one.
 template <bool TALL, bool NARROW>
 struct Frame {
-  int64_t ra, rb;  // elements from the matrix's first, without the row's part
-  int c, back;
+  int64_t a, b;
+  int c, back;  // first element in the row as loaded
   bool oka, okb;
-  __device__ __forceinline__ Frame(const Mat& M, int k0, const Spot& s) {
-    const int rows = TALL ? M.n : M.m, len = TALL ? M.m : M.n, r0 = TALL ? k0 : 0, at = TALL ? s.c : k0 + s.c;
-    c = NARROW ? min(at, len - 1) : min(at, len - 8);
-    back = at - c;
-    oka = r0 + s.ra < rows;
-    okb = r0 + s.rb < rows;
-    ra = min(r0 + s.ra, rows - 1);
-    rb = min(r0 + s.rb, rows - 1);
+  __device__ __forceinline__ Frame(const Mat& M, int64_t ld, int k0, const Spot& s, bool edge) {
+    const int r0 = TALL ? k0 : 0, at = TALL ? s.c : k0 + s.c;
+    c = at;
+    back = 0;
+    oka = okb = true;
+    if (NARROW || edge) {
+      const int rows = TALL ? M.n : M.m, len = TALL ? M.m : M.n;
+      c = NARROW ? min(at, len - 1) : min(at, len - 8);
+      back = at - c;
+      oka = r0 + s.ra < rows;
+      okb = r0 + s.rb < rows;
+      a = int64_t(min(r0 + s.ra, rows - 1)) * ld + c;
+      b = int64_t(min(r0 + s.rb, rows - 1)) * ld + c;
+    } else {
+      a = (r0 * ld + (TALL ? 0 : k0)) + (s.ra * ld + s.c);
+      b = (r0 * ld + (TALL ? 0 : k0)) + (s.rb * ld + s.c);
+    }
   }
 };
 // Whether a tile reaches over the matrix's sides.
@@ -255,9 +288,9 @@ __device__ __forceinline__ bool at_edge(const Mat& M, int k0) {
 }
 
 template <typename T, bool TALL, bool NARROW>
-__device__ __forceinline__ void fetch(const void* base, int64_t ld, const Mat& M, const Frame<TALL, NARROW>& f, Raw<T> (&x)[2]) {
-  const global<T>* const a = (const global<T>*)base + f.ra * ld + f.c;
-  const global<T>* const b = (const global<T>*)base + f.rb * ld + f.c;
+__device__ __forceinline__ void fetch(const void* base, const Mat& M, const Frame<TALL, NARROW>& f, Raw<T> (&x)[2]) {
+  const global<T>* const a = (const global<T>*)base + f.a;
+  const global<T>* const b = (const global<T>*)base + f.b;
   if constexpr (!NARROW) {
     x[0].load(a);
     x[1].load(b);
@@ -303,19 +336,38 @@ __device__ __forceinline__ void fix(const Mat& M, const Frame<TALL, NARROW>& f, 
 #pragma unroll
   for (int q = 0; q < 8; ++q) x[q] = q < n ? x[q] : 0.f;
 }
-// Stores the thread's own elements of a row; the values are in their places.
+// The other way: values in their places go to where the vector was loaded.
+template <bool TALL, bool NARROW>
+__device__ __forceinline__ void spread(const Frame<TALL, NARROW>& f, float (&x)[8]) {
+  if constexpr (!NARROW) {
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+      for (int q = 7; q >= 0; --q) x[q] = f.back & s ? (q >= s ? x[q - s] : 0.f) : x[q];
+  }
+}
+// Stores the thread's own elements of one of its rows (at: f.a or f.b). At an
+// edge the values have not been put in their places yet.
 template <typename T, bool TALL, bool NARROW>
-__device__ __forceinline__ void put_row(void* base, int64_t ld, const Mat& M, const Frame<TALL, NARROW>& f, int64_t row, bool ok, bool edge, const float (&x)[8]) {
-  global<T>* const p = (global<T>*)base + row * ld + f.c + f.back;
+__device__ __forceinline__ void put_row(void* base, const Mat& M, const Frame<TALL, NARROW>& f, int64_t at, bool ok, bool edge, Raw<T>& x) {
   if (!NARROW && !edge) {
-    store8(p, x);
+    x.store((global<T>*)base + at);
     return;
   }
+  float v[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = x.get(q);
+  fix(M, f, ok, v);
+  global<T>* const p = (global<T>*)base + at + f.back;
   const int n = own(M, f, ok);
-  if (n == 8) store8(p, x);
-  else
+  if (n == 8) {
+    x.set(v);
+    x.store(p);
+  } else {
+#pragma unroll
     for (int q = 0; q < 7; ++q)
-      if (q < n) store1(p + q, x[q]);
+      if (q < n) store1(p + q, v[q]);
+  }
 }
 
 // Writes a thread's 2 x 8 values (scaled to fp16's range) as hi and lo.
@@ -441,32 +493,30 @@ struct Step {
   bool use_mom, nesterov;
   __device__ __forceinline__ Step(const Args& A) : gs(A.gscale ? *A.gscale : 1.f), mu(A.mu), use_mom(A.use_mom), nesterov(A.nesterov) {}
 };
-// u of a vector from the gradient and the momentum as loaded; FIRST: the
-// momentum's new value is left in nb. (Without momentum the second operand is
-// the gradient again: it is loaded, and not used.)
+// u of a vector from the gradient and the momentum as loaded; FIRST: b becomes
+// the momentum's new value. (Without momentum the second operand is the
+// gradient again: it is loaded, and not used.)
 template <typename T, bool FIRST>
-__device__ __forceinline__ void form_u(const Step& S, const Raw<T>& g, const Raw<T>& b, float (&u)[8], float (&nb)[8]) {
+__device__ __forceinline__ void form_u(const Step& S, const Raw<T>& g, Raw<T>& b, float (&u)[8]) {
 #pragma unroll
   for (int q = 0; q < 8; ++q) u[q] = g.get(q) * S.gs;
   if (!S.use_mom) return;
   if constexpr (FIRST) {
-    momentum(S.mu, b, u, nb);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) nb[q] = b.get(q);
+    const Raw<T> old = b;
+    momentum(S.mu, old, u, b);
   }
 #pragma unroll
-  for (int q = 0; q < 8; ++q) u[q] = S.nesterov ? __fmaf_rn(S.mu, nb[q], u[q]) : nb[q];
+  for (int q = 0; q < 8; ++q) u[q] = S.nesterov ? __fmaf_rn(S.mu, b.get(q), u[q]) : b.get(q);
 }
 
 // A tile's gradient and momentum on their way.
-template <typename T, bool TALL, bool NARROW>
+template <typename T, int MT, bool TALL, bool NARROW>
 struct Load {
   Raw<T> g[2], b[2];
   __device__ __forceinline__ void start(const Mat& M, const void* b2, int k0, const Spot& s) {
-    const Frame<TALL, NARROW> f(M, k0, s);
-    fetch<T>(M.g, M.ld, M, f, g);
-    fetch<T>(b2, M.ld, M, f, b);
+    const Frame<TALL, NARROW> f(M, M.ld, k0, s, at_edge<MT>(M, k0));
+    fetch<T>(M.g, M, f, g);
+    fetch<T>(b2, M, f, b);
   }
 };
 
@@ -487,26 +537,22 @@ __device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Pa
   const Spot s = spot<MT, !TALL, TALL>(tid);
   f32x16 acc[C::tiles] = {};
   int e = -126;
-  Load<T, TALL, NARROW> x, y;
-  auto start = [&](Load<T, TALL, NARROW>& l, int t) { l.start(M, b2, min(t, p.end - 1) * C::cols, s); };
-  auto work = [&](Load<T, TALL, NARROW>& l, int t) {
+  Load<T, MT, TALL, NARROW> x, y;
+  auto start = [&](Load<T, MT, TALL, NARROW>& l, int t) { l.start(M, b2, min(t, p.end - 1) * C::cols, s); };
+  auto work = [&](Load<T, MT, TALL, NARROW>& l, int t) {
     const int k0 = t * C::cols;
     const bool edge = at_edge<MT>(M, k0);
-    const Frame<TALL, NARROW> f(M, k0, s);
-    float u[2][8], nb[2][8];
-    form_u<T, true>(S, l.g[0], l.b[0], u[0], nb[0]);
-    form_u<T, true>(S, l.g[1], l.b[1], u[1], nb[1]);
+    const Frame<TALL, NARROW> f(M, M.ld, k0, s, edge);
+    float u[2][8];
+    form_u<T, true>(S, l.g[0], l.b[0], u[0]);
+    form_u<T, true>(S, l.g[1], l.b[1], u[1]);
+    if (S.use_mom) {
+      put_row<T>(M.b, M, f, f.a, f.oka, edge, l.b[0]);
+      put_row<T>(M.b, M, f, f.b, f.okb, edge, l.b[1]);
+    }
     if (NARROW || edge) {
       fix(M, f, f.oka, u[0]);
       fix(M, f, f.okb, u[1]);
-      if (S.use_mom) {
-        fix(M, f, f.oka, nb[0]);
-        fix(M, f, f.okb, nb[1]);
-      }
-    }
-    if (S.use_mom) {
-      put_row<T>(M.b, M.ld, M, f, f.ra, f.oka, edge, nb[0]);
-      put_row<T>(M.b, M.ld, M, f, f.rb, f.okb, edge, nb[1]);
     }
     start(l, t + 2);
     float big = 0.f;
@@ -768,9 +814,9 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
 
 // What a tile of P X needs on its way: the gradient and momentum, or X, and
 // for the last run's weights those.
-template <typename T, bool TALL, bool NARROW, bool GRAD, bool WEIGHTS>
+template <typename T, int MT, bool TALL, bool NARROW, bool GRAD, bool WEIGHTS>
 struct ApplyLoad {
-  Load<T, TALL, NARROW> u;
+  Load<T, MT, TALL, NARROW> u;
   Raw<float> x[2];
   Raw<T> w[2];
 };
@@ -808,7 +854,9 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
   const Spot s = spot<MT, !kRowsAreK, !kRowsAreK>(tid);
   const Spot o = spot<MT, !TALL, false>(tid);
   f32x16 acc2[C::tiles] = {};
-  typedef ApplyLoad<T, TALL, NARROW, GRAD, WEIGHTS> L;
+  // tiles on their way while one is worked on (registers: P's share and two tiles of fp32 gradients do not fit with mp = 128)
+  constexpr int kAhead = MT == 4 && GRAD && sizeof(T) == 4 ? 1 : 2;
+  typedef ApplyLoad<T, MT, TALL, NARROW, GRAD, WEIGHTS> L;
   L x, y;
   auto start = [&](L& l, int t) {
     const int k0 = min(t, p.end - 1) * C::cols;
@@ -821,8 +869,9 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
   };
   auto start_w = [&](L& l, int t) {
     if constexpr (LAST && WEIGHTS) {
-      const Frame<TALL, NARROW> fr(M, min(t, p.end - 1) * C::cols, o);
-      fetch<T>(M.w, M.wld, M, fr, l.w);
+      const int k0 = min(t, p.end - 1) * C::cols;
+      const Frame<TALL, NARROW> fr(M, M.wld, k0, o, at_edge<MT>(M, k0));
+      fetch<T>(M.w, M, fr, l.w);
     }
   };
   auto work = [&](L& l, int t) {
@@ -830,11 +879,10 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
     const bool edge = at_edge<MT>(M, k0);
     float u[2][8];
     if constexpr (GRAD) {
-      float nb[2][8];
-      form_u<T, false>(S, l.u.g[0], l.u.b[0], u[0], nb[0]);
-      form_u<T, false>(S, l.u.g[1], l.u.b[1], u[1], nb[1]);
+      form_u<T, false>(S, l.u.g[0], l.u.b[0], u[0]);
+      form_u<T, false>(S, l.u.g[1], l.u.b[1], u[1]);
       if (NARROW || edge) {
-        const Frame<TALL, NARROW> fr(M, k0, s);
+        const Frame<TALL, NARROW> fr(M, M.ld, k0, s, edge);
         fix(M, fr, fr.oka, u[0]);
         fix(M, fr, fr.okb, u[1]);
       }
@@ -844,7 +892,7 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
 #pragma unroll
         for (int q = 0; q < 8; ++q) u[j][q] = l.x[j].get(q);
     }
-    start(l, t + 2);
+    start(l, t + kAhead);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -878,39 +926,39 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
         }
       }
       lds_barrier();
-      const Frame<TALL, NARROW> fr(M, k0, o);
-      float w[2][8];
-      if constexpr (WEIGHTS) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) w[j][q] = l.w[j].get(q);
-          if (NARROW || edge) fix(M, fr, j ? fr.okb : fr.oka, w[j]);
-        }
-        start_w(l, t + 2);
-      }
+      const Frame<TALL, NARROW> fr(M, WEIGHTS ? M.wld : M.ld, k0, o, edge);
+      // values of weights at an edge are where they were loaded: those of X go there
+      Raw<T> r[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const f32x4* const in = reinterpret_cast<const f32x4*>(stage + (j ? o.rb : o.ra) * ((TALL ? C::mp : C::cols) + 4) + o.c);
         const f32x4 a = in[0], b = in[1];
         float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        if (NARROW || edge) spread<TALL, NARROW>(fr, v);
         if constexpr (WEIGHTS) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = __fmaf_rn(-step, v[q], w[j][q] * keep);
+          for (int q = 0; q < 8; ++q) v[q] = __fmaf_rn(-step, v[q], l.w[j].get(q) * keep);
         }
-        put_row<T>(WEIGHTS ? M.w : M.o, WEIGHTS ? M.wld : M.ld, M, fr, j ? fr.rb : fr.ra, j ? fr.okb : fr.oka, edge, v);
+        r[j].set(v);
       }
+      start_w(l, t + kAhead);
+      put_row<T>(WEIGHTS ? M.w : M.o, M, fr, fr.a, fr.oka, edge, r[0]);
+      put_row<T>(WEIGHTS ? M.w : M.o, M, fr, fr.b, fr.okb, edge, r[1]);
     }
   };
   start(x, p.beg);
   start_w(x, p.beg);
-  __builtin_amdgcn_sched_barrier(0);  // loads are waited for in the order they went out
-  start(y, p.beg + 1);
-  start_w(y, p.beg + 1);
-  for (int t = p.beg; t < p.end; t += 2) {
-    work(x, t);
-    if (t + 1 >= p.end) break;
-    work(y, t + 1);
+  if constexpr (kAhead == 1) {
+    for (int t = p.beg; t < p.end; ++t) work(x, t);
+  } else {
+    __builtin_amdgcn_sched_barrier(0);  // loads are waited for in the order they went out
+    start(y, p.beg + 1);
+    start_w(y, p.beg + 1);
+    for (int t = p.beg; t < p.end; t += 2) {
+      work(x, t);
+      if (t + 1 >= p.end) break;
+      work(y, t + 1);
+    }
   }
   if constexpr (!LAST) put_gram<MT>(A, M, p.index, acc2, lds, wave, lane);
 }
@@ -932,9 +980,14 @@ __device__ __forceinline__ void gram_any(const Args& A, const Mat& M, const Part
 template <typename T, int MT, bool NARROW>
 __global__ __launch_bounds__(Cfg<MT>::threads) void stack_gram_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
-  const Part p = A.parts[blockIdx.x];
-  const Mat M = A.mats[p.mat];  // by value: a reference would be read again after every store
-  gram_any<T, MT, NARROW>(A, M, p, lds);
+  const int last = A.first[blockIdx.x + 1];
+#pragma unroll 1
+  for (int i = A.first[blockIdx.x]; i < last; ++i) {
+    const Part p = A.parts[i];
+    const Mat M = A.mats[p.mat];  // by value: a reference would be read again after every store
+    gram_any<T, MT, NARROW>(A, M, p, lds);
+    lds_barrier();
+  }
 }
 
 template <int MT>
@@ -947,9 +1000,14 @@ __global__ __launch_bounds__(Cfg<MT>::threads) void stack_solve_kernel(Args A, i
 template <typename T, int MT, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS>
 __global__ __launch_bounds__(Cfg<MT>::threads) void stack_apply_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
-  const Part p = A.parts[blockIdx.x];
-  const Mat M = A.mats[p.mat];
-  apply_any<T, MT, NARROW, GRAD, LAST, WEIGHTS>(A, M, p, lds);
+  const int last = A.first[blockIdx.x + 1];
+#pragma unroll 1
+  for (int i = A.first[blockIdx.x]; i < last; ++i) {
+    const Part p = A.parts[i];
+    const Mat M = A.mats[p.mat];
+    apply_any<T, MT, NARROW, GRAD, LAST, WEIGHTS>(A, M, p, lds);
+    lds_barrier();
+  }
 }
 
 // -------------------------------------------------------------------- host
@@ -969,7 +1027,8 @@ struct Host {
   std::vector<int32_t> owner;          // the stack of each
   std::vector<int64_t> index;          // its place in it
   std::vector<Part> parts;             // by class
-  int32_t mat_beg[kClasses + 1] = {}, part_beg[kClasses + 1] = {};
+  std::vector<int32_t> first;          // by class: the workgroups' first parts, and the end of the last one's
+  int32_t mat_beg[kClasses + 1] = {}, first_beg[kClasses + 1] = {};
   size_t ws_bytes = 0;
 };
 
@@ -1026,8 +1085,12 @@ muon_status validate(const muon_stack* st, int32_t n, muon_dtype dtype, const mu
   return muon::tensor_overlap::overlaps(iv) ? MUON_E_INVALID : MUON_OK;
 }
 
-constexpr int64_t kMaxParts = 64;
-constexpr int64_t kTargetParts = 1024;
+// The tiles of a class, one matrix after the other, are dealt out in equal runs
+// to as many workgroups as run at once (three of 256 threads or one of 512 on
+// each of 256 CUs), but none is given fewer than kLeast tiles, or so few that a
+// matrix falls into more than kMaxParts parts.
+constexpr int64_t kMaxParts = 64, kLeast = 2;
+int64_t groups_of(int cls) { return cls == 3 ? 256 : 768; }
 
 muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
   int64_t total = 0;
@@ -1044,12 +1107,21 @@ muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
   };
   for (int cls = 0; cls < kClasses; ++cls) {
     H->mat_beg[cls] = static_cast<int32_t>(H->mats.size());
-    H->part_beg[cls] = static_cast<int32_t>(H->parts.size());
-    int64_t tiles = 0;
+    H->first_beg[cls] = static_cast<int32_t>(H->first.size());
+    int64_t tiles = 0, longest = 0;
     const int64_t cols = cols_of(cls), mp = mp_of(cls);
+    auto tiles_of = [&](const muon_stack& s) { return (std::max(s.rows, s.cols) + cols - 1) / cols; };
     for (int32_t i = 0; i < n; ++i)
-      if (!empty(st[i]) && class_of(st[i]) == cls) tiles += st[i].count * ((std::max(st[i].rows, st[i].cols) + cols - 1) / cols);
-    const int64_t each = std::max<int64_t>(1, (tiles + kTargetParts - 1) / kTargetParts);
+      if (!empty(st[i]) && class_of(st[i]) == cls) {
+        tiles += st[i].count * tiles_of(st[i]);
+        longest = std::max(longest, tiles_of(st[i]));
+      }
+    if (tiles == 0) continue;
+    const int64_t least = std::max(kLeast, (longest + kMaxParts - 1) / kMaxParts);
+    const int64_t groups = std::max<int64_t>(1, std::min(groups_of(cls), tiles / least));
+    int64_t at = 0, group = 0;  // tiles dealt out, and the workgroup the next one goes to
+    auto end_of = [&](int64_t g) { return (g + 1) * tiles / groups; };
+    H->first.push_back(static_cast<int32_t>(H->parts.size()));
     for (int32_t i = 0; i < n; ++i) {
       const muon_stack& s = st[i];
       if (empty(s) || class_of(s) != cls) continue;
@@ -1062,17 +1134,22 @@ muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
         M.m = static_cast<int32_t>(std::min(s.rows, s.cols));
         M.n = static_cast<int32_t>(std::max(s.rows, s.cols));
         M.tall = s.rows > s.cols;
-        const int64_t nt = (M.n + cols - 1) / cols;
-        const int64_t per = std::max(each, (nt + kMaxParts - 1) / kMaxParts);
-        M.parts = static_cast<int32_t>((nt + per - 1) / per);
+        const int64_t nt = tiles_of(s);
+        for (int64_t beg = 0; beg < nt;) {
+          const int64_t end = std::min(nt, beg + end_of(group) - at);
+          H->parts.push_back({static_cast<int32_t>(H->mats.size()), static_cast<int32_t>(beg), static_cast<int32_t>(end), M.parts++});
+          at += end - beg;
+          beg = end;
+          if (at == end_of(group)) {
+            H->first.push_back(static_cast<int32_t>(H->parts.size()));
+            ++group;
+          }
+        }
         M.gram_off = take(M.parts * mp * mp * 4);
         M.exp_off = take(M.parts * 4);
         M.rec_off = take(8);
         M.p_off = take(mp * mp * 4);
         M.x_off = take(nt * cols * mp * 4);
-        for (int32_t p = 0; p < M.parts; ++p)
-          H->parts.push_back({static_cast<int32_t>(H->mats.size()), static_cast<int32_t>(p * per),
-                              static_cast<int32_t>(std::min(nt, (p + 1) * per)), p});
         H->mats.push_back(M);
         H->owner.push_back(i);
         H->index.push_back(t);
@@ -1080,7 +1157,7 @@ muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
     }
   }
   H->mat_beg[kClasses] = static_cast<int32_t>(H->mats.size());
-  H->part_beg[kClasses] = static_cast<int32_t>(H->parts.size());
+  H->first_beg[kClasses] = static_cast<int32_t>(H->first.size());
   H->ws_bytes = off;
   return MUON_OK;
 }
@@ -1119,6 +1196,7 @@ struct muon_stack_plan_s {
   void* dmem = nullptr;
   const muon_stack_ns::Mat* d_mats = nullptr;
   const muon_stack_ns::Part* d_parts = nullptr;
+  const int32_t* d_first = nullptr;
   bool has_weights = false;
   const float* gscale = nullptr;
 };
@@ -1139,20 +1217,21 @@ muon_status run_class(const muon_stack_plan_s* p, int cls, Args a, hipStream_t s
   const Host& H = p->host;
   const int mats = H.mat_beg[cls + 1] - H.mat_beg[cls];
   if (mats == 0) return MUON_OK;
-  const unsigned parts = unsigned(H.part_beg[cls + 1] - H.part_beg[cls]);
-  a.parts = p->d_parts + H.part_beg[cls];
-  muon_status st = go(stack_gram_kernel<T, MT, NARROW>, parts, C::threads, C::lds_gram, s, a);
+  const unsigned groups = unsigned(H.first_beg[cls + 1] - H.first_beg[cls] - 1);  // workgroups
+  a.parts = p->d_parts;
+  a.first = p->d_first + H.first_beg[cls];
+  muon_status st = go(stack_gram_kernel<T, MT, NARROW>, groups, C::threads, C::lds_gram, s, a);
   for (int run = 0; run < a.runs && st == MUON_OK; ++run) {
     a.run = run;
     hipLaunchKernelGGL(stack_solve_kernel<MT>, dim3(unsigned(mats)), dim3(C::threads), C::lds_solve, s, a, H.mat_beg[cls]);
     if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
     const bool last = run + 1 == a.runs;
     if (run == 0)
-      st = last ? go(stack_apply_kernel<T, MT, NARROW, true, true, WEIGHTS>, parts, C::threads, C::lds_tile, s, a)
-                : go(stack_apply_kernel<T, MT, NARROW, true, false, false>, parts, C::threads, C::lds_tile, s, a);
+      st = last ? go(stack_apply_kernel<T, MT, NARROW, true, true, WEIGHTS>, groups, C::threads, C::lds_tile, s, a)
+                : go(stack_apply_kernel<T, MT, NARROW, true, false, false>, groups, C::threads, C::lds_tile, s, a);
     else
-      st = last ? go(stack_apply_kernel<T, MT, NARROW, false, true, WEIGHTS>, parts, C::threads, C::lds_tile, s, a)
-                : go(stack_apply_kernel<T, MT, NARROW, false, false, false>, parts, C::threads, C::lds_tile, s, a);
+      st = last ? go(stack_apply_kernel<T, MT, NARROW, false, true, WEIGHTS>, groups, C::threads, C::lds_tile, s, a)
+                : go(stack_apply_kernel<T, MT, NARROW, false, false, false>, groups, C::threads, C::lds_tile, s, a);
   }
   return st;
 }
@@ -1239,9 +1318,11 @@ muon_status muon_stack_plan_create(const muon_stack* stacks, int32_t n, muon_dty
     }
     const Host& H = p->host;
     const size_t mb = (sizeof(Mat) * H.mats.size() + 255) / 256 * 256;
-    std::vector<char> h(std::max<size_t>(256, mb + sizeof(Part) * H.parts.size()), 0);
+    const size_t pb = mb + (sizeof(Part) * H.parts.size() + 255) / 256 * 256;
+    std::vector<char> h(std::max<size_t>(256, pb + sizeof(int32_t) * H.first.size()), 0);
     if (!H.mats.empty()) std::memcpy(h.data(), H.mats.data(), sizeof(Mat) * H.mats.size());
     if (!H.parts.empty()) std::memcpy(h.data() + mb, H.parts.data(), sizeof(Part) * H.parts.size());
+    if (!H.first.empty()) std::memcpy(h.data() + pb, H.first.data(), sizeof(int32_t) * H.first.size());
     if (hipMalloc(&p->dmem, h.size()) != hipSuccess) {
       (void)hipGetLastError();
       delete p;
@@ -1255,6 +1336,7 @@ muon_status muon_stack_plan_create(const muon_stack* stacks, int32_t n, muon_dty
     }
     p->d_mats = static_cast<const Mat*>(p->dmem);
     p->d_parts = reinterpret_cast<const Part*>(static_cast<char*>(p->dmem) + mb);
+    p->d_first = reinterpret_cast<const int32_t*>(static_cast<char*>(p->dmem) + pb);
     *plan = p;
     return MUON_OK;
   } catch (...) {
