@@ -63,16 +63,19 @@ struct Mat {
   float lr_mul, wd_mul;
 };
 
-// Columns [beg, end) of a matrix, in tiles. A workgroup has parts [first, first
-// of the next).
+// Part `index` of a matrix: columns [beg, end), in tiles. The workgroups' first
+// parts come first, in their order; `next` leads to a workgroup's others (-1:
+// none). The matrix stands in the record, so that a workgroup's first gradients
+// are one read away from its launch arguments (with a table of its own for
+// each, three reads: 1 us more of a workgroup's 6 on a small set).
 struct Part {
-  int32_t mat, beg, end, index;
+  Mat M;
+  int32_t beg, end, index, next;
 };
 
 struct Args {
-  const Mat* mats;
-  const Part* parts;
-  const int32_t* first;  // per workgroup
+  const Mat* mats;    // by class
+  const Part* parts;  // of the class
   char* ws;
   const float* gscale;
   float a, b, c, mu, eps, lr, wd;
@@ -102,6 +105,9 @@ template <int MT> struct Cfg {
   static constexpr int square = 2 * mp * mp;           // halves of an mp x mp matrix in the solve, hi and lo
   static constexpr int lds_solve = (MT == 4 ? 2 : 3) * square * 2;
 };
+
+// Waves on a SIMD that the registers have to allow for the workgroups of a launch to run at once (groups_of).
+constexpr int per_simd(int mt, bool narrow) { return mt == 4 || narrow ? 2 : 3; }
 
 // A barrier that orders LDS alone: __syncthreads() would also wait for the
 // global loads on their way (no wave reads what another has stored to global
@@ -522,8 +528,7 @@ struct Load {
 
 // Phase gram over the part's columns. The operands are scaled by a power of
 // two that puts the largest |u| so far into [2^12, 2^13): when a tile raises
-// it, the sums so far are rescaled, which is exact. Two tiles are on their way
-// while one is worked on.
+// it, the sums so far are rescaled, which is exact.
 template <typename T, int MT, bool TALL, bool NARROW>
 __device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Part& p, char* lds) {
   typedef Cfg<MT> C;
@@ -537,6 +542,7 @@ __device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Pa
   const Spot s = spot<MT, !TALL, TALL>(tid);
   f32x16 acc[C::tiles] = {};
   int e = -126;
+  constexpr int kAhead = NARROW ? 1 : 2;  // tiles on their way while one is worked on
   Load<T, MT, TALL, NARROW> x, y;
   auto start = [&](Load<T, MT, TALL, NARROW>& l, int t) { l.start(M, b2, min(t, p.end - 1) * C::cols, s); };
   auto work = [&](Load<T, MT, TALL, NARROW>& l, int t) {
@@ -554,7 +560,7 @@ __device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Pa
       fix(M, f, f.oka, u[0]);
       fix(M, f, f.okb, u[1]);
     }
-    start(l, t + 2);
+    start(l, t + kAhead);
     float big = 0.f;
 #pragma unroll
     for (int q = 0; q < 8; ++q) big = fmaxf(big, fmaxf(fabsf(u[0][q]), fabsf(u[1][q])));
@@ -581,12 +587,16 @@ __device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Pa
     gram_tile<MT>(hi, lo, acc, wave, lane);
   };
   start(x, p.beg);
-  __builtin_amdgcn_sched_barrier(0);  // loads are waited for in the order they went out
-  start(y, p.beg + 1);
-  for (int t = p.beg; t < p.end; t += 2) {
-    work(x, t);
-    if (t + 1 >= p.end) break;
-    work(y, t + 1);
+  if constexpr (kAhead == 1) {
+    for (int t = p.beg; t < p.end; ++t) work(x, t);
+  } else {
+    __builtin_amdgcn_sched_barrier(0);  // loads are waited for in the order they went out
+    start(y, p.beg + 1);
+    for (int t = p.beg; t < p.end; t += 2) {
+      work(x, t);
+      if (t + 1 >= p.end) break;
+      work(y, t + 1);
+    }
   }
   put_gram<MT>(A, M, p.index, acc, lds, wave, lane);
   if (tid == 0) reinterpret_cast<int32_t*>(A.ws + M.exp_off)[p.index] = e;
@@ -687,24 +697,38 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
   const int32_t* const exps = reinterpret_cast<const int32_t*>(A.ws + M.exp_off);
   int e = kXExp;
   if (run == 0) {
-    e = -126;
-    for (int p = 0; p < M.parts; ++p) e = max(e, exps[p]);
+    int top = 0;
+    for (int p = lane; p < M.parts; p += 64) top = max(top, exps[p] + 126);
+    e = wave_max(top) - 126;
   }
   f32x16 a[C::tiles] = {}, pr[C::tiles] = {}, q[C::tiles], acc[C::tiles];
-  const float4* in = reinterpret_cast<const float4*>(A.ws + M.gram_off);
+  const float4* const in = reinterpret_cast<const float4*>(A.ws + M.gram_off);
+  constexpr int kJoin = MT == 4 ? 2 : 4;  // parts on their way at once
   if (mine)
-    for (int p = 0; p < M.parts; ++p, in += C::mp * C::mp / 4) {
-      const int shift = run == 0 ? 2 * (exps[p] - e) : 0;
+    for (int p = 0; p < M.parts; p += kJoin) {
+      float4 x[kJoin][C::tiles][4];
+      int shift[kJoin];
 #pragma unroll
-      for (int t = 0; t < C::tiles; ++t)
+      for (int j = 0; j < kJoin; ++j) {
+        const int q = min(p + j, M.parts - 1);
+        shift[j] = run == 0 ? 2 * (exps[q] - e) : 0;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float4 x = in[((wave * C::tiles + t) * 4 + g) * 64 + lane];
-          a[t][4 * g] += ldexpf(x.x, shift);
-          a[t][4 * g + 1] += ldexpf(x.y, shift);
-          a[t][4 * g + 2] += ldexpf(x.z, shift);
-          a[t][4 * g + 3] += ldexpf(x.w, shift);
-        }
+        for (int t = 0; t < C::tiles; ++t)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) x[j][t][g] = in[int64_t(q) * (C::mp * C::mp / 4) + ((wave * C::tiles + t) * 4 + g) * 64 + lane];
+      }
+#pragma unroll
+      for (int j = 0; j < kJoin; ++j)
+        if (p + j < M.parts)
+#pragma unroll
+          for (int t = 0; t < C::tiles; ++t)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              a[t][4 * g] += ldexpf(x[j][t][g].x, shift[j]);
+              a[t][4 * g + 1] += ldexpf(x[j][t][g].y, shift[j]);
+              a[t][4 * g + 2] += ldexpf(x[j][t][g].z, shift[j]);
+              a[t][4 * g + 3] += ldexpf(x[j][t][g].w, shift[j]);
+            }
     }
   // the identity's elements of this lane, for a I
   auto diag = [&](int t, int i) { return ti == tj + t && acc_row(i >> 2, lane) + (i & 3) == (lane & 31); };
@@ -812,13 +836,11 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
   }
 }
 
-// What a tile of P X needs on its way: the gradient and momentum, or X, and
-// for the last run's weights those.
-template <typename T, int MT, bool TALL, bool NARROW, bool GRAD, bool WEIGHTS>
+// What a tile of P X needs on its way: the gradient and momentum, or X.
+template <typename T, int MT, bool TALL, bool NARROW>
 struct ApplyLoad {
   Load<T, MT, TALL, NARROW> u;
   Raw<float> x[2];
-  Raw<T> w[2];
 };
 
 // P X for the part's columns: GRAD: X is sigma u, from the gradients, else what
@@ -854,10 +876,11 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
   const Spot s = spot<MT, !kRowsAreK, !kRowsAreK>(tid);
   const Spot o = spot<MT, !TALL, false>(tid);
   f32x16 acc2[C::tiles] = {};
-  // tiles on their way while one is worked on (registers: P's share and two tiles of fp32 gradients do not fit with mp = 128)
-  constexpr int kAhead = MT == 4 && GRAD && sizeof(T) == 4 ? 1 : 2;
-  typedef ApplyLoad<T, MT, TALL, NARROW, GRAD, WEIGHTS> L;
+  // tiles on their way while one is worked on (fp32's second one does not fit in the registers beside P's share)
+  constexpr int kAhead = sizeof(T) == 4 || NARROW ? 1 : 2;
+  typedef ApplyLoad<T, MT, TALL, NARROW> L;
   L x, y;
+  Raw<T> wt[2];  // the weights, one tile ahead
   auto start = [&](L& l, int t) {
     const int k0 = min(t, p.end - 1) * C::cols;
     if constexpr (GRAD) {
@@ -867,11 +890,11 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
       l.x[1].load(xs + int64_t(k0 + s.rb) * C::mp + s.c);
     }
   };
-  auto start_w = [&](L& l, int t) {
+  auto start_w = [&](int t) {
     if constexpr (LAST && WEIGHTS) {
       const int k0 = min(t, p.end - 1) * C::cols;
       const Frame<TALL, NARROW> fr(M, M.wld, k0, o, at_edge<MT>(M, k0));
-      fetch<T>(M.w, M, fr, l.w);
+      fetch<T>(M.w, M, fr, wt);
     }
   };
   auto work = [&](L& l, int t) {
@@ -937,23 +960,22 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
         if (NARROW || edge) spread<TALL, NARROW>(fr, v);
         if constexpr (WEIGHTS) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = __fmaf_rn(-step, v[q], l.w[j].get(q) * keep);
+          for (int q = 0; q < 8; ++q) v[q] = __fmaf_rn(-step, v[q], wt[j].get(q) * keep);
         }
         r[j].set(v);
       }
-      start_w(l, t + kAhead);
+      start_w(t + 1);
       put_row<T>(WEIGHTS ? M.w : M.o, M, fr, fr.a, fr.oka, edge, r[0]);
       put_row<T>(WEIGHTS ? M.w : M.o, M, fr, fr.b, fr.okb, edge, r[1]);
     }
   };
   start(x, p.beg);
-  start_w(x, p.beg);
+  start_w(p.beg);
   if constexpr (kAhead == 1) {
     for (int t = p.beg; t < p.end; ++t) work(x, t);
   } else {
     __builtin_amdgcn_sched_barrier(0);  // loads are waited for in the order they went out
     start(y, p.beg + 1);
-    start_w(y, p.beg + 1);
     for (int t = p.beg; t < p.end; t += 2) {
       work(x, t);
       if (t + 1 >= p.end) break;
@@ -978,15 +1000,14 @@ __device__ __forceinline__ void gram_any(const Args& A, const Mat& M, const Part
 // ----------------------------------------------------------------- kernels
 
 template <typename T, int MT, bool NARROW>
-__global__ __launch_bounds__(Cfg<MT>::threads) void stack_gram_kernel(Args A) {
+__global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW)) void stack_gram_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
-  const int last = A.first[blockIdx.x + 1];
 #pragma unroll 1
-  for (int i = A.first[blockIdx.x]; i < last; ++i) {
-    const Part p = A.parts[i];
-    const Mat M = A.mats[p.mat];  // by value: a reference would be read again after every store
-    gram_any<T, MT, NARROW>(A, M, p, lds);
+  for (int i = int(blockIdx.x); i >= 0;) {
+    const Part p = A.parts[i];  // by value: a reference would be read again after every store
+    gram_any<T, MT, NARROW>(A, p.M, p, lds);
     lds_barrier();
+    i = p.next;
   }
 }
 
@@ -998,15 +1019,14 @@ __global__ __launch_bounds__(Cfg<MT>::threads) void stack_solve_kernel(Args A, i
 }
 
 template <typename T, int MT, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS>
-__global__ __launch_bounds__(Cfg<MT>::threads) void stack_apply_kernel(Args A) {
+__global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW)) void stack_apply_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
-  const int last = A.first[blockIdx.x + 1];
 #pragma unroll 1
-  for (int i = A.first[blockIdx.x]; i < last; ++i) {
+  for (int i = int(blockIdx.x); i >= 0;) {
     const Part p = A.parts[i];
-    const Mat M = A.mats[p.mat];
-    apply_any<T, MT, NARROW, GRAD, LAST, WEIGHTS>(A, M, p, lds);
+    apply_any<T, MT, NARROW, GRAD, LAST, WEIGHTS>(A, p.M, p, lds);
     lds_barrier();
+    i = p.next;
   }
 }
 
@@ -1026,9 +1046,9 @@ struct Host {
   std::vector<Mat> mats;               // by class, then in the caller's order
   std::vector<int32_t> owner;          // the stack of each
   std::vector<int64_t> index;          // its place in it
-  std::vector<Part> parts;             // by class
-  std::vector<int32_t> first;          // by class: the workgroups' first parts, and the end of the last one's
-  int32_t mat_beg[kClasses + 1] = {}, first_beg[kClasses + 1] = {};
+  std::vector<Part> parts;             // by class, the matrices' records not filled in
+  std::vector<int32_t> part_mat;       // the matrix of each
+  int32_t mat_beg[kClasses + 1] = {}, part_beg[kClasses + 1] = {}, groups[kClasses] = {};
   size_t ws_bytes = 0;
 };
 
@@ -1086,11 +1106,11 @@ muon_status validate(const muon_stack* st, int32_t n, muon_dtype dtype, const mu
 }
 
 // The tiles of a class, one matrix after the other, are dealt out in equal runs
-// to as many workgroups as run at once (three of 256 threads or one of 512 on
-// each of 256 CUs), but none is given fewer than kLeast tiles, or so few that a
+// to as many workgroups as run at once (three of 256 threads, two for narrow
+// matrices, or one of 512 on each of 256 CUs), but none is given fewer than kLeast tiles, or so few that a
 // matrix falls into more than kMaxParts parts.
 constexpr int64_t kMaxParts = 64, kLeast = 2;
-int64_t groups_of(int cls) { return cls == 3 ? 256 : 768; }
+int64_t groups_of(int cls) { return cls == 3 ? 256 : cls == 0 ? 512 : 768; }
 
 muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
   int64_t total = 0;
@@ -1107,7 +1127,8 @@ muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
   };
   for (int cls = 0; cls < kClasses; ++cls) {
     H->mat_beg[cls] = static_cast<int32_t>(H->mats.size());
-    H->first_beg[cls] = static_cast<int32_t>(H->first.size());
+    const size_t part0 = H->parts.size();
+    H->part_beg[cls] = static_cast<int32_t>(part0);
     int64_t tiles = 0, longest = 0;
     const int64_t cols = cols_of(cls), mp = mp_of(cls);
     auto tiles_of = [&](const muon_stack& s) { return (std::max(s.rows, s.cols) + cols - 1) / cols; };
@@ -1121,7 +1142,10 @@ muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
     const int64_t groups = std::max<int64_t>(1, std::min(groups_of(cls), tiles / least));
     int64_t at = 0, group = 0;  // tiles dealt out, and the workgroup the next one goes to
     auto end_of = [&](int64_t g) { return (g + 1) * tiles / groups; };
-    H->first.push_back(static_cast<int32_t>(H->parts.size()));
+    H->groups[cls] = static_cast<int32_t>(groups);
+    H->parts.resize(part0 + groups);
+    H->part_mat.resize(part0 + groups);
+    int64_t of_group = -1;  // the part that the group's next one follows (-1: it has none)
     for (int32_t i = 0; i < n; ++i) {
       const muon_stack& s = st[i];
       if (empty(s) || class_of(s) != cls) continue;
@@ -1137,11 +1161,24 @@ muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
         const int64_t nt = tiles_of(s);
         for (int64_t beg = 0; beg < nt;) {
           const int64_t end = std::min(nt, beg + end_of(group) - at);
-          H->parts.push_back({static_cast<int32_t>(H->mats.size()), static_cast<int32_t>(beg), static_cast<int32_t>(end), M.parts++});
+          int64_t place = static_cast<int64_t>(part0) + group;
+          if (of_group >= 0) {
+            place = static_cast<int64_t>(H->parts.size());
+            H->parts[of_group].next = static_cast<int32_t>(place - static_cast<int64_t>(part0));
+            H->parts.emplace_back();
+            H->part_mat.emplace_back();
+          }
+          Part& p = H->parts[place];
+          p.beg = static_cast<int32_t>(beg);
+          p.end = static_cast<int32_t>(end);
+          p.index = M.parts++;
+          p.next = -1;
+          H->part_mat[place] = static_cast<int32_t>(H->mats.size());
+          of_group = place;
           at += end - beg;
           beg = end;
           if (at == end_of(group)) {
-            H->first.push_back(static_cast<int32_t>(H->parts.size()));
+            of_group = -1;
             ++group;
           }
         }
@@ -1157,9 +1194,23 @@ muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
     }
   }
   H->mat_beg[kClasses] = static_cast<int32_t>(H->mats.size());
-  H->first_beg[kClasses] = static_cast<int32_t>(H->first.size());
+  H->part_beg[kClasses] = static_cast<int32_t>(H->parts.size());
   H->ws_bytes = off;
   return MUON_OK;
+}
+
+// The plan's tables in device memory: the matrices, then the parts.
+size_t parts_at(const Host& H) { return (sizeof(Mat) * H.mats.size() + 255) / 256 * 256; }
+std::vector<char> tables(const Host& H, const std::vector<Mat>& mats) {
+  const size_t at = parts_at(H);
+  std::vector<char> h(std::max<size_t>(256, at + sizeof(Part) * H.parts.size()), 0);
+  if (!mats.empty()) std::memcpy(h.data(), mats.data(), sizeof(Mat) * mats.size());
+  for (size_t i = 0; i < H.parts.size(); ++i) {
+    Part p = H.parts[i];
+    p.M = mats[H.part_mat[i]];
+    std::memcpy(h.data() + at + i * sizeof(Part), &p, sizeof(Part));
+  }
+  return h;
 }
 
 // The largest number of steps from one Gram matrix. Errors of A grow by at
@@ -1196,7 +1247,6 @@ struct muon_stack_plan_s {
   void* dmem = nullptr;
   const muon_stack_ns::Mat* d_mats = nullptr;
   const muon_stack_ns::Part* d_parts = nullptr;
-  const int32_t* d_first = nullptr;
   bool has_weights = false;
   const float* gscale = nullptr;
 };
@@ -1217,9 +1267,8 @@ muon_status run_class(const muon_stack_plan_s* p, int cls, Args a, hipStream_t s
   const Host& H = p->host;
   const int mats = H.mat_beg[cls + 1] - H.mat_beg[cls];
   if (mats == 0) return MUON_OK;
-  const unsigned groups = unsigned(H.first_beg[cls + 1] - H.first_beg[cls] - 1);  // workgroups
-  a.parts = p->d_parts;
-  a.first = p->d_first + H.first_beg[cls];
+  const unsigned groups = unsigned(H.groups[cls]);
+  a.parts = p->d_parts + H.part_beg[cls];
   muon_status st = go(stack_gram_kernel<T, MT, NARROW>, groups, C::threads, C::lds_gram, s, a);
   for (int run = 0; run < a.runs && st == MUON_OK; ++run) {
     a.run = run;
@@ -1316,13 +1365,7 @@ muon_status muon_stack_plan_create(const muon_stack* stacks, int32_t n, muon_dty
       delete p;
       return st;
     }
-    const Host& H = p->host;
-    const size_t mb = (sizeof(Mat) * H.mats.size() + 255) / 256 * 256;
-    const size_t pb = mb + (sizeof(Part) * H.parts.size() + 255) / 256 * 256;
-    std::vector<char> h(std::max<size_t>(256, pb + sizeof(int32_t) * H.first.size()), 0);
-    if (!H.mats.empty()) std::memcpy(h.data(), H.mats.data(), sizeof(Mat) * H.mats.size());
-    if (!H.parts.empty()) std::memcpy(h.data() + mb, H.parts.data(), sizeof(Part) * H.parts.size());
-    if (!H.first.empty()) std::memcpy(h.data() + pb, H.first.data(), sizeof(int32_t) * H.first.size());
+    const std::vector<char> h = tables(p->host, p->host.mats);
     if (hipMalloc(&p->dmem, h.size()) != hipSuccess) {
       (void)hipGetLastError();
       delete p;
@@ -1335,8 +1378,7 @@ muon_status muon_stack_plan_create(const muon_stack* stacks, int32_t n, muon_dty
       return MUON_E_DEVICE;
     }
     p->d_mats = static_cast<const Mat*>(p->dmem);
-    p->d_parts = reinterpret_cast<const Part*>(static_cast<char*>(p->dmem) + mb);
-    p->d_first = reinterpret_cast<const int32_t*>(static_cast<char*>(p->dmem) + pb);
+    p->d_parts = reinterpret_cast<const Part*>(static_cast<char*>(p->dmem) + parts_at(p->host));
     *plan = p;
     return MUON_OK;
   } catch (...) {
@@ -1371,9 +1413,9 @@ muon_status muon_stack_plan_set_weights(muon_stack_plan* plan, const muon_stack_
     }
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess || dev != plan->device) return MUON_E_DEVICE;
+    const std::vector<char> h = tables(H, mats);
     if (hipDeviceSynchronize() != hipSuccess) return MUON_E_DEVICE;
-    if (!mats.empty() && hipMemcpy(plan->dmem, mats.data(), sizeof(Mat) * mats.size(), hipMemcpyHostToDevice) != hipSuccess)
-      return MUON_E_DEVICE;
+    if (hipMemcpy(plan->dmem, h.data(), h.size(), hipMemcpyHostToDevice) != hipSuccess) return MUON_E_DEVICE;
     H.mats = std::move(mats);
     plan->has_weights = true;
     return MUON_OK;
