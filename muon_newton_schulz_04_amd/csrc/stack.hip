@@ -14,7 +14,8 @@
 //
 // Phases of a matrix, each over runs of columns ("parts") or as a whole:
 //   gram    buf' and u from the gradient, A = sum of u u^T over the part
-//   solve   one workgroup: the norm (the trace of A), s steps, P
+//   solve   one workgroup: the norm (the trace of A), s steps, P; in small sets
+//           with mp = 32 every workgroup of the next phase for itself
 //   update  X <- P X for the part's columns, and its sum of X X^T
 //   last    X <- P X for the part's columns, out or the weights
 // A tile of X is mp x kCols (mp = m padded to 32, 64 or 128), in LDS as two
@@ -101,9 +102,10 @@ template <int MT> struct Cfg {
   static constexpr int lds_stage = 4 * (mp * (cols + 4) > cols * (mp + 4) ? mp * (cols + 4) : cols * (mp + 4));
   static constexpr int lds_second = lds_k > lds_stage ? lds_k : lds_stage;
   static constexpr int lds_gram = MT == 1 && lds_k < waves * 4096 ? waves * 4096 : lds_k;
-  static constexpr int lds_tile = lds_m + lds_second;
   static constexpr int square = 2 * mp * mp;           // halves of an mp x mp matrix in the solve, hi and lo
   static constexpr int lds_solve = (MT == 4 ? 2 : 3) * square * 2;
+  static constexpr int lds_tile = lds_m + lds_second;  // (with mp = 32 the solve and P fit in, too)
+  static_assert(MT > 1 || lds_tile >= lds_solve + mp * ms * 4);
 };
 
 // Waves on a SIMD that the registers have to allow for the workgroups of a launch to run at once (groups_of).
@@ -463,11 +465,19 @@ __device__ __forceinline__ void gram_tile(const _Float16* hi, const _Float16* lo
   }
 }
 
-// The part's sum of X X^T goes to the workspace, in accumulator order.
+// Where the partial Gram matrices of a run of steps are. With mp = 32 the
+// workgroups of `update` may read them all before they write the next run's,
+// each at its own time, so the runs take turns with two arrays.
 template <int MT>
-__device__ __forceinline__ void put_gram(const Args& A, const Mat& M, int part, f32x16 (&acc)[Cfg<MT>::tiles], char* lds, int wave, int lane) {
+__device__ __forceinline__ int64_t gram_at(const Mat& M, int run) {
+  return M.gram_off + (MT == 1 && run % 2 ? int64_t(M.parts) * (Cfg<MT>::mp * Cfg<MT>::mp * 4) : 0);
+}
+
+// The part's sum of X X^T, for a run, goes to the workspace, in accumulator order.
+template <int MT>
+__device__ __forceinline__ void put_gram(const Args& A, const Mat& M, int run, int part, f32x16 (&acc)[Cfg<MT>::tiles], char* lds, int wave, int lane) {
   typedef Cfg<MT> C;
-  float4* const out = reinterpret_cast<float4*>(A.ws + M.gram_off) + int64_t(part) * (C::mp * C::mp / 4);
+  float4* const out = reinterpret_cast<float4*>(A.ws + gram_at<MT>(M, run)) + int64_t(part) * (C::mp * C::mp / 4);
   if constexpr (MT == 1) {
     float4* const red = reinterpret_cast<float4*>(lds);
     lds_barrier();
@@ -598,7 +608,7 @@ __device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Pa
       work(y, t + 1);
     }
   }
-  put_gram<MT>(A, M, p.index, acc, lds, wave, lane);
+  put_gram<MT>(A, M, 0, p.index, acc, lds, wave, lane);
   if (tid == 0) reinterpret_cast<int32_t*>(A.ws + M.exp_off)[p.index] = e;
 }
 
@@ -616,17 +626,16 @@ __device__ __forceinline__ f16x8 frag_sq(const _Float16* x, int row, int k, int 
   return *reinterpret_cast<const f16x8*>(x + chunk_at<MT>(row + (lane & 31), (k >> 3) + (lane >> 5)));
 }
 
-// acc = scale * (X Y^T), and with TWO also bcc = scale2 * (Z Y^T), for the
-// matrices as they are stored. Cross terms have accumulators of their own: a
-// chain of dependent products half as long.
+// acc = X Y^T, and with TWO also bcc = Z Y^T, for the matrices as they are
+// stored.
 template <int MT, bool TWO>
 __device__ __forceinline__ void mul_sq(const _Float16* x, const _Float16* z, const _Float16* y, f32x16 (&acc)[Cfg<MT>::tiles], f32x16 (&bcc)[Cfg<MT>::tiles],
-                                       float scale, float scale2, int wave, int lane) {
+                                       int wave, int lane) {
   typedef Cfg<MT> C;
   constexpr int lo = C::mp * C::mp, kUnroll = MT == 4 ? 2 : 4;
   int ti, tj;
   tile_of<MT>(wave, ti, tj);
-  f32x16 a1[C::tiles] = {}, a2[C::tiles] = {}, b1[C::tiles] = {}, b2[C::tiles] = {};
+  f32x16 a[C::tiles] = {}, b[C::tiles] = {};  // (acc may be x's or z's own value)
   if (MT > 1 || wave == 0) {
 #pragma unroll kUnroll
     for (int k = 0; k < C::mp; k += 16) {
@@ -636,24 +645,16 @@ __device__ __forceinline__ void mul_sq(const _Float16* x, const _Float16* z, con
 #pragma unroll
       for (int t = 0; t < C::tiles; ++t) {
         const f16x8 yh = frag_sq<MT>(y, 32 * (tj + t), k, lane), yl = frag_sq<MT>(y + lo, 32 * (tj + t), k, lane);
-        a1[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh, yh, a1[t], 0, 0, 0);
-        a2[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh, yl, a2[t], 0, 0, 0);
-        a2[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xl, yh, a2[t], 0, 0, 0);
-        if (TWO) {
-          b1[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(zh, yh, b1[t], 0, 0, 0);
-          b2[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(zh, yl, b2[t], 0, 0, 0);
-          b2[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(zl, yh, b2[t], 0, 0, 0);
-        }
+        a[t] = mul3(xh, xl, yh, yl, a[t]);
+        if (TWO) b[t] = mul3(zh, zl, yh, yl, b[t]);
       }
     }
   }
 #pragma unroll
-  for (int t = 0; t < C::tiles; ++t)
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      acc[t][q] = (a1[t][q] + a2[t][q]) * scale;
-      if (TWO) bcc[t][q] = (b1[t][q] + b2[t][q]) * scale2;
-    }
+  for (int t = 0; t < C::tiles; ++t) {
+    acc[t] = a[t];
+    if (TWO) bcc[t] = b[t];
+  }
 }
 
 template <int MT>
@@ -676,17 +677,24 @@ __device__ __forceinline__ void put_sq(_Float16* x, const f32x16 (&v)[Cfg<MT>::t
     }
 }
 
+// What makes X of u: sigma, and the exponent it is scaled for.
+struct Norm {
+  float sigma;
+  int e;
+};
+
 // Phase solve: A from its parts, the norm (first run), the run's steps on A
 // and P. The matrices are symmetric but for rounding, and are stored
 // transposed (put_sq), so a product of two as stored is X^T Y. The order of
 // the factors matters for that rounding: T = A^T Q, A' = T^T Q = Q^T A Q and P' =
 // P^T Q keep the antisymmetric part of A's errors from growing faster than the
 // rest (with T = Q^T A it grew by 14 in every step of the quintic: X off by
-// 4e-4 after five steps on full-rank 64 x 768, 1e-5 in this order).
+// 4e-4 after five steps on full-rank 64 x 768, 1e-5 in this order). P goes to
+// out: mp x mp hi, then lo, in rows of `stride` halves.
 template <int MT>
-__device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run, char* lds) {
+__device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, char* lds, _Float16* out, int stride, Norm& norm) {
   typedef Cfg<MT> C;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int run = A.run, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   _Float16* const la = reinterpret_cast<_Float16*>(lds);  // A, T
   _Float16* const lq = la + C::square;                    // Q
   _Float16* const lp = MT == 4 ? la : lq + C::square;     // P (mp = 128: where A was, for its product)
@@ -702,7 +710,7 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
     e = wave_max(top) - 126;
   }
   f32x16 a[C::tiles] = {}, pr[C::tiles] = {}, q[C::tiles], acc[C::tiles];
-  const float4* const in = reinterpret_cast<const float4*>(A.ws + M.gram_off);
+  const float4* const in = reinterpret_cast<const float4*>(A.ws + gram_at<MT>(M, run));
   constexpr int kJoin = MT == 4 ? 2 : 4;  // parts on their way at once
   if (mine)
     for (int p = 0; p < M.parts; p += kJoin) {
@@ -749,14 +757,10 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
 #pragma unroll
     for (int w = 0; w < C::waves; ++w) sum += red[w];
     // sigma = 1 / ((norm + eps) 2^(kXExp - e)), whatever float32 makes of the norm; zeros give zeros
-    const double norm = ldexp(sqrt(double(sum)), e - kXExp);
-    float sigma = static_cast<float>(1.0 / ldexp(norm + double(A.eps), kXExp - e));
-    if (sum == 0.f) sigma = 0.f;
-    scale = sigma * sigma;
-    if (tid == 0) {
-      reinterpret_cast<float*>(A.ws + M.rec_off)[0] = sigma;
-      reinterpret_cast<int32_t*>(A.ws + M.rec_off)[1] = e;
-    }
+    const double size = ldexp(sqrt(double(sum)), e - kXExp);
+    norm.sigma = sum == 0.f ? 0.f : static_cast<float>(1.0 / ldexp(size + double(A.eps), kXExp - e));
+    norm.e = e;
+    scale = norm.sigma * norm.sigma;
   }
 #pragma unroll
   for (int t = 0; t < C::tiles; ++t)
@@ -772,15 +776,18 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
     put_sq<MT>(la, a, kAScale, wave, lane);
     lds_barrier();
   }
-  constexpr float kAQ = 1.f / (kAScale * kPScale), kPQ = 1.f / (kPScale * kPScale);
+  // products are of the matrices as stored: A = sa a, P = sp pr
+  constexpr float kAA = 1.f / (kAScale * kAScale), kAQ = 1.f / (kAScale * kPScale), kPQ = 1.f / (kPScale * kPScale);
+  float sa = 1.f, sp = 1.f;
 #pragma unroll 1
   for (int i = 0; i < steps; ++i) {
     const bool more = i + 1 < steps;
-    mul_sq<MT, false>(la, la, la, acc, acc, 1.f / (kAScale * kAScale), 0.f, wave, lane);
+    mul_sq<MT, false>(la, la, la, acc, acc, wave, lane);
+    const float c = A.c * kAA, b = A.b * sa;
 #pragma unroll
     for (int t = 0; t < C::tiles; ++t)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) q[t][j] = __fmaf_rn(A.c, acc[t][j], __fmaf_rn(A.b, a[t][j], diag(t, j) ? A.a : 0.f));
+      for (int j = 0; j < 16; ++j) q[t][j] = __fmaf_rn(c, acc[t][j], __fmaf_rn(b, a[t][j], diag(t, j) ? A.a : 0.f));
     if (i == 0) {
 #pragma unroll
       for (int t = 0; t < C::tiles; ++t) pr[t] = q[t];
@@ -791,48 +798,47 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, int run
       if (i == 0) {
         put_sq<MT>(lp, pr, kPScale, wave, lane);
         lds_barrier();
-        mul_sq<MT, false>(la, la, lq, acc, acc, kAQ, 0.f, wave, lane);
+        mul_sq<MT, false>(la, la, lq, acc, acc, wave, lane);
       } else {
         lds_barrier();
+        sp = kPQ;
         if (!more) {
-          mul_sq<MT, false>(lp, lp, lq, pr, pr, kPQ, 0.f, wave, lane);
+          mul_sq<MT, false>(lp, lp, lq, pr, pr, wave, lane);
           break;
         }
-        mul_sq<MT, true>(la, lp, lq, acc, pr, kAQ, kPQ, wave, lane);
+        mul_sq<MT, true>(la, lp, lq, acc, pr, wave, lane);
       }
       lds_barrier();
-      put_sq<MT>(la, acc, kAScale, wave, lane);
-      if (i > 0) put_sq<MT>(lp, pr, kPScale, wave, lane);
+      put_sq<MT>(la, acc, kAQ * kAScale, wave, lane);
+      if (i > 0) put_sq<MT>(lp, pr, kPQ * kPScale, wave, lane);
       lds_barrier();
-      mul_sq<MT, false>(la, la, lq, a, a, kAQ, 0.f, wave, lane);
-      lds_barrier();
-      put_sq<MT>(la, a, kAScale, wave, lane);
-      lds_barrier();
+      mul_sq<MT, false>(la, la, lq, a, a, wave, lane);
     } else {
       lds_barrier();
       if (more) {
-        mul_sq<MT, false>(la, la, lq, acc, acc, kAQ, 0.f, wave, lane);
+        mul_sq<MT, false>(la, la, lq, acc, acc, wave, lane);
         lds_barrier();
-        put_sq<MT>(la, acc, kAScale, wave, lane);
+        put_sq<MT>(la, acc, kAQ * kAScale, wave, lane);
         lds_barrier();
-        mul_sq<MT, false>(la, la, lq, a, a, kAQ, 0.f, wave, lane);
+        mul_sq<MT, false>(la, la, lq, a, a, wave, lane);
       }
       if (i > 0) {
         lds_barrier();
-        put_sq<MT>(lp, pr, kPScale, wave, lane);
+        put_sq<MT>(lp, pr, sp * kPScale, wave, lane);
         lds_barrier();
-        mul_sq<MT, false>(lp, lp, lq, pr, pr, kPQ, 0.f, wave, lane);
+        mul_sq<MT, false>(lp, lp, lq, pr, pr, wave, lane);
+        sp = kPQ;
       }
       if (!more) break;
-      lds_barrier();
-      put_sq<MT>(la, a, kAScale, wave, lane);
-      lds_barrier();
     }
+    sa = kAQ;
+    lds_barrier();
+    put_sq<MT>(la, a, kAQ * kAScale, wave, lane);
+    lds_barrier();
   }
   if (mine) {
-    _Float16* const out = reinterpret_cast<_Float16*>(A.ws + M.p_off);
 #pragma unroll
-    for (int t = 0; t < C::tiles; ++t) put_acc(out, out + C::mp * C::mp, C::mp, 32 * ti, 32 * (tj + t), pr[t], kPScale, lane);
+    for (int t = 0; t < C::tiles; ++t) put_acc(out, out + C::mp * stride, stride, 32 * ti, 32 * (tj + t), pr[t], sp * kPScale, lane);
   }
 }
 
@@ -845,8 +851,8 @@ struct ApplyLoad {
 
 // P X for the part's columns: GRAD: X is sigma u, from the gradients, else what
 // the run before left. LAST: out or the weights, else X and its X X^T.
-template <typename T, int MT, bool TALL, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS>
-__device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const Part& p, char* lds) {
+template <typename T, int MT, bool TALL, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS, bool SOLVE>
+__device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const Part& p, Norm norm, char* lds) {
   typedef Cfg<MT> C;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   _Float16* const mh = reinterpret_cast<_Float16*>(lds);        // [k][m]
@@ -857,27 +863,14 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
   const int mi = wave % MT, ki = wave / MT;  // the wave's rows of X and columns of the tile, in 32s
   const Step S(A);
   const void* const b2 = S.use_mom ? M.b : M.g;
-  float f = 1.f / (kAScale * kPScale);
-  int e = 0;
-  if (GRAD) {
-    f = reinterpret_cast<const float*>(A.ws + M.rec_off)[0] * (1.f / kPScale);
-    e = reinterpret_cast<const int32_t*>(A.ws + M.rec_off)[1];
-  }
   const float keep = 1.f - (A.lr * M.lr_mul) * (A.wd * M.wd_mul), step = A.lr * M.lr_mul;
-  f16x8 ph[C::mp / 16], pl[C::mp / 16];
-  const _Float16* const pm = reinterpret_cast<const _Float16*>(A.ws + M.p_off);
-#pragma unroll
-  for (int k = 0; k < C::mp / 16; ++k) {
-    ph[k] = frag(pm, 32 * mi, C::mp, 16 * k, lane);
-    pl[k] = frag(pm + C::mp * C::mp, 32 * mi, C::mp, 16 * k, lane);
-  }
   global<float>* const xs = (global<float>*)(A.ws + M.x_off);
   constexpr bool kRowsAreK = TALL || !GRAD;  // memory rows are columns of X
   const Spot s = spot<MT, !kRowsAreK, !kRowsAreK>(tid);
   const Spot o = spot<MT, !TALL, false>(tid);
   f32x16 acc2[C::tiles] = {};
-  // tiles on their way while one is worked on (fp32's second one does not fit in the registers beside P's share)
-  constexpr int kAhead = sizeof(T) == 4 || NARROW ? 1 : 2;
+  // tiles on their way while one is worked on (a second one of fp32 numbers does not fit in the registers beside P's share)
+  constexpr int kAhead = !GRAD || sizeof(T) == 4 || NARROW ? 1 : 2;
   typedef ApplyLoad<T, MT, TALL, NARROW> L;
   L x, y;
   Raw<T> wt[2];  // the weights, one tile ahead
@@ -897,6 +890,28 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
       fetch<T>(M.w, M, fr, wt);
     }
   };
+  start(x, p.beg);
+  start_w(p.beg);
+  f16x8 ph[C::mp / 16], pl[C::mp / 16];
+  if constexpr (SOLVE) {
+    const _Float16* const pm = reinterpret_cast<const _Float16*>(lds + C::lds_solve);
+#pragma unroll
+    for (int k = 0; k < C::mp / 16; ++k) {
+      ph[k] = frag(pm, 0, C::ms, 16 * k, lane);
+      pl[k] = frag(pm + C::mp * C::ms, 0, C::ms, 16 * k, lane);
+    }
+    lds_barrier();
+  } else {
+    const _Float16* const pm = reinterpret_cast<const _Float16*>(A.ws + M.p_off);
+#pragma unroll
+    for (int k = 0; k < C::mp / 16; ++k) {
+      ph[k] = frag(pm, 32 * mi, C::mp, 16 * k, lane);
+      pl[k] = frag(pm + C::mp * C::mp, 32 * mi, C::mp, 16 * k, lane);
+    }
+    if (GRAD) norm = *reinterpret_cast<const Norm*>(A.ws + M.rec_off);
+  }
+  const float f = GRAD ? norm.sigma * (1.f / kPScale) : 1.f / (kAScale * kPScale);
+  const int e = norm.e;
   auto work = [&](L& l, int t) {
     const int k0 = t * C::cols;
     const bool edge = at_edge<MT>(M, k0);
@@ -969,8 +984,6 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
       put_row<T>(WEIGHTS ? M.w : M.o, M, fr, fr.b, fr.okb, edge, r[1]);
     }
   };
-  start(x, p.beg);
-  start_w(p.beg);
   if constexpr (kAhead == 1) {
     for (int t = p.beg; t < p.end; ++t) work(x, t);
   } else {
@@ -982,14 +995,14 @@ __device__ __forceinline__ void phase_apply(const Args& A, const Mat& M, const P
       work(y, t + 1);
     }
   }
-  if constexpr (!LAST) put_gram<MT>(A, M, p.index, acc2, lds, wave, lane);
+  if constexpr (!LAST) put_gram<MT>(A, M, A.run + 1, p.index, acc2, lds, wave, lane);
 }
 
 // The matrix's direction is the workgroup's own matter; the rest is the launch's.
-template <typename T, int MT, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS>
-__device__ __forceinline__ void apply_any(const Args& A, const Mat& M, const Part& p, char* lds) {
-  if (M.tall) phase_apply<T, MT, true, NARROW, GRAD, LAST, WEIGHTS>(A, M, p, lds);
-  else phase_apply<T, MT, false, NARROW, GRAD, LAST, WEIGHTS>(A, M, p, lds);
+template <typename T, int MT, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS, bool SOLVE>
+__device__ __forceinline__ void apply_any(const Args& A, const Mat& M, const Part& p, Norm norm, char* lds) {
+  if (M.tall) phase_apply<T, MT, true, NARROW, GRAD, LAST, WEIGHTS, SOLVE>(A, M, p, norm, lds);
+  else phase_apply<T, MT, false, NARROW, GRAD, LAST, WEIGHTS, SOLVE>(A, M, p, norm, lds);
 }
 template <typename T, int MT, bool NARROW>
 __device__ __forceinline__ void gram_any(const Args& A, const Mat& M, const Part& p, char* lds) {
@@ -1015,16 +1028,24 @@ template <int MT>
 __global__ __launch_bounds__(Cfg<MT>::threads) void stack_solve_kernel(Args A, int first) {
   extern __shared__ __align__(16) char lds[];
   const Mat M = A.mats[first + blockIdx.x];
-  phase_solve<MT>(A, M, A.run, lds);
+  Norm norm = {};
+  phase_solve<MT>(A, M, lds, reinterpret_cast<_Float16*>(A.ws + M.p_off), Cfg<MT>::mp, norm);
+  if (A.run == 0 && threadIdx.x == 0) *reinterpret_cast<Norm*>(A.ws + M.rec_off) = norm;
 }
 
-template <typename T, int MT, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS>
-__global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW)) void stack_apply_kernel(Args A) {
+// SOLVE: each part's workgroup solves for P itself.
+template <typename T, int MT, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS, bool SOLVE>
+__global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW || SOLVE)) void stack_apply_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
 #pragma unroll 1
   for (int i = int(blockIdx.x); i >= 0;) {
     const Part p = A.parts[i];
-    apply_any<T, MT, NARROW, GRAD, LAST, WEIGHTS>(A, p.M, p, lds);
+    Norm norm = {};
+    if constexpr (SOLVE) {  // P into the tile's LDS, behind what the solve uses itself
+      phase_solve<MT>(A, p.M, lds, reinterpret_cast<_Float16*>(lds + Cfg<MT>::lds_solve), Cfg<MT>::ms, norm);
+      lds_barrier();
+    }
+    apply_any<T, MT, NARROW, GRAD, LAST, WEIGHTS, SOLVE>(A, p.M, p, norm, lds);
     lds_barrier();
     i = p.next;
   }
@@ -1049,6 +1070,7 @@ struct Host {
   std::vector<Part> parts;             // by class, the matrices' records not filled in
   std::vector<int32_t> part_mat;       // the matrix of each
   int32_t mat_beg[kClasses + 1] = {}, part_beg[kClasses + 1] = {}, groups[kClasses] = {};
+  bool solve_there[kClasses] = {};     // the parts' workgroups solve for P themselves
   size_t ws_bytes = 0;
 };
 
@@ -1111,6 +1133,12 @@ muon_status validate(const muon_stack* st, int32_t n, muon_dtype dtype, const mu
 // matrix falls into more than kMaxParts parts.
 constexpr int64_t kMaxParts = 64, kLeast = 2;
 int64_t groups_of(int cls) { return cls == 3 ? 256 : cls == 0 ? 512 : 768; }
+// Matrices of mp = 32 that all run at once in two workgroups on each CU have
+// their P solved for by the workgroups that use it: the launch that this saves
+// costs more than one wave's solve does in each of them (96 fp32 matrices of 16
+// x 765, four runs of steps: 69 us with, 58 us without it; 288 bf16 matrices of
+// 32 x 768, which take turns: 41 us with, 47 us without).
+constexpr int64_t kSolveThere = 512;
 
 muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
   int64_t total = 0;
@@ -1140,6 +1168,7 @@ muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
     if (tiles == 0) continue;
     const int64_t least = std::max(kLeast, (longest + kMaxParts - 1) / kMaxParts);
     const int64_t groups = std::max<int64_t>(1, std::min(groups_of(cls), tiles / least));
+    H->solve_there[cls] = mp == 32 && tiles / least <= kSolveThere;
     int64_t at = 0, group = 0;  // tiles dealt out, and the workgroup the next one goes to
     auto end_of = [&](int64_t g) { return (g + 1) * tiles / groups; };
     H->groups[cls] = static_cast<int32_t>(groups);
@@ -1182,7 +1211,7 @@ muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
             ++group;
           }
         }
-        M.gram_off = take(M.parts * mp * mp * 4);
+        M.gram_off = take((mp == 32 ? 2 : 1) * M.parts * mp * mp * 4);  // (gram_at)
         M.exp_off = take(M.parts * 4);
         M.rec_off = take(8);
         M.p_off = take(mp * mp * 4);
@@ -1262,28 +1291,38 @@ muon_status go(K kernel, unsigned grid, int threads, int lds, hipStream_t s, con
   return hipGetLastError() == hipSuccess ? MUON_OK : MUON_E_LAUNCH;
 }
 
-template <typename T, int MT, bool NARROW, bool WEIGHTS>
-muon_status run_class(const muon_stack_plan_s* p, int cls, Args a, hipStream_t s) {
+// The steps' phases, launch by launch. SOLVE: without a launch for the solve.
+template <typename T, int MT, bool NARROW, bool WEIGHTS, bool SOLVE>
+muon_status run_phases(unsigned groups, int mats, int first, Args a, hipStream_t s) {
   typedef Cfg<MT> C;
-  const Host& H = p->host;
-  const int mats = H.mat_beg[cls + 1] - H.mat_beg[cls];
-  if (mats == 0) return MUON_OK;
-  const unsigned groups = unsigned(H.groups[cls]);
-  a.parts = p->d_parts + H.part_beg[cls];
   muon_status st = go(stack_gram_kernel<T, MT, NARROW>, groups, C::threads, C::lds_gram, s, a);
   for (int run = 0; run < a.runs && st == MUON_OK; ++run) {
     a.run = run;
-    hipLaunchKernelGGL(stack_solve_kernel<MT>, dim3(unsigned(mats)), dim3(C::threads), C::lds_solve, s, a, H.mat_beg[cls]);
-    if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
+    if constexpr (!SOLVE) {
+      hipLaunchKernelGGL(stack_solve_kernel<MT>, dim3(unsigned(mats)), dim3(C::threads), C::lds_solve, s, a, first);
+      if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
+    }
     const bool last = run + 1 == a.runs;
     if (run == 0)
-      st = last ? go(stack_apply_kernel<T, MT, NARROW, true, true, WEIGHTS>, groups, C::threads, C::lds_tile, s, a)
-                : go(stack_apply_kernel<T, MT, NARROW, true, false, false>, groups, C::threads, C::lds_tile, s, a);
+      st = last ? go(stack_apply_kernel<T, MT, NARROW, true, true, WEIGHTS, SOLVE>, groups, C::threads, C::lds_tile, s, a)
+                : go(stack_apply_kernel<T, MT, NARROW, true, false, false, SOLVE>, groups, C::threads, C::lds_tile, s, a);
     else
-      st = last ? go(stack_apply_kernel<T, MT, NARROW, false, true, WEIGHTS>, groups, C::threads, C::lds_tile, s, a)
-                : go(stack_apply_kernel<T, MT, NARROW, false, false, false>, groups, C::threads, C::lds_tile, s, a);
+      st = last ? go(stack_apply_kernel<T, MT, NARROW, false, true, WEIGHTS, SOLVE>, groups, C::threads, C::lds_tile, s, a)
+                : go(stack_apply_kernel<T, MT, NARROW, false, false, false, SOLVE>, groups, C::threads, C::lds_tile, s, a);
   }
   return st;
+}
+
+template <typename T, int MT, bool NARROW, bool WEIGHTS>
+muon_status run_class(const muon_stack_plan_s* p, int cls, Args a, hipStream_t s) {
+  const Host& H = p->host;
+  const int first = H.mat_beg[cls], mats = H.mat_beg[cls + 1] - first;
+  if (mats == 0) return MUON_OK;
+  const unsigned groups = unsigned(H.groups[cls]);
+  a.parts = p->d_parts + H.part_beg[cls];
+  if constexpr (MT == 1)
+    if (H.solve_there[cls]) return run_phases<T, MT, NARROW, WEIGHTS, true>(groups, mats, first, a, s);
+  return run_phases<T, MT, NARROW, WEIGHTS, false>(groups, mats, first, a, s);
 }
 
 template <typename T, bool WEIGHTS>

@@ -253,6 +253,17 @@ def test_weights(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", [(170, 16, 765), (171, 16, 765), (171, 765, 16), (3, 515, 4), (260, 515, 4)], ids=str)
+def test_short_sides_in_small_and_large_sets(shape, dtype):
+    """170 matrices of 6 tiles are a set whose workgroups solve for P themselves, 171 are not; one run of steps and several."""
+    sample = (0, 1, shape[0] - 1)
+    check(shape, dtype, sample=sample)
+    check(shape, dtype, CUBIC, 10, sample=sample, seed=1)
+    check(shape, dtype, CUBIC, 23, side=True, pad=1, offset=1, sample=sample, seed=2)
+    test_weights(shape, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_aliases_steps_in_a_row_and_equal_bits(dtype):
     """out may be the gradient; two plans on equal inputs give equal bits, over three steps; a factor of one changes nothing."""
     gen = torch.Generator().manual_seed(8)
