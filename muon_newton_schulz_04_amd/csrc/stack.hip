@@ -612,7 +612,45 @@ __device__ __forceinline__ void phase_gram(const Args& A, const Mat& M, const Pa
   if (tid == 0) reinterpret_cast<int32_t*>(A.ws + M.exp_off)[p.index] = e;
 }
 
-// The solve's matrices: mp x mp, hi then lo, in rows of 2 mp bytes without
+// The solve's matrices. A wave has 16 whole columns of each (its own ones), one
+// per lane % 16, as accumulators of v_mfma_f32_16x16x32_f16: element e of step
+// s of a lane is row row_of(s, e). As an operand of a product over the rows the
+// same registers hold that lane's part of the inner dimension, in an order that
+// the LDS copy of a matrix (column by column, chunks of eight rows) follows: a
+// wave's own operand never goes through LDS, and a step has two barriers (mp =
+// 128: four). Against 32 x 32 tiles with both operands in LDS and six to eight
+// barriers a step: 96 matrices of 16 x 765, four runs of steps, 58 -> 52 us; 48
+// matrices of 64 x 768 16 -> 15 us; 256 of 128 x 2048 the same 61 us, for which
+// four waves of 32 columns take 74.
+template <int MT> struct Sq {
+  static constexpr int mp = 32 * MT;
+  static constexpr int waves = mp / 16, threads = 64 * waves;
+  static constexpr int steps = mp / 32, tiles = mp / 16;
+};
+template <int MT> struct Acc {  // own columns in float32
+  f32x4 t[Sq<MT>::tiles];
+  __device__ __forceinline__ float get(int s, int e) const { return t[2 * s + (e >> 2)][e & 3]; }
+  __device__ __forceinline__ void set(int s, int e, float x) { t[2 * s + (e >> 2)][e & 3] = x; }
+};
+template <int MT> struct Own {  // own columns as hi + lo
+  f16x8 h[Sq<MT>::steps], l[Sq<MT>::steps];
+  __device__ __forceinline__ float get(int s, int e) const { return static_cast<float>(h[s][e]) + static_cast<float>(l[s][e]); }
+  __device__ __forceinline__ void set(const Acc<MT>& x, float scale) {
+#pragma unroll
+    for (int s = 0; s < Sq<MT>::steps; ++s) {
+      uint4 a, b;
+      split2(x.get(s, 0) * scale, x.get(s, 1) * scale, a.x, b.x);
+      split2(x.get(s, 2) * scale, x.get(s, 3) * scale, a.y, b.y);
+      split2(x.get(s, 4) * scale, x.get(s, 5) * scale, a.z, b.z);
+      split2(x.get(s, 6) * scale, x.get(s, 7) * scale, a.w, b.w);
+      h[s] = __builtin_bit_cast(f16x8, a);
+      l[s] = __builtin_bit_cast(f16x8, b);
+    }
+  }
+};
+__device__ __forceinline__ int row_of(int s, int e, int lane) { return 32 * s + 16 * (e >> 2) + 4 * (lane >> 4) + (e & 3); }
+
+// The LDS copy: hi, then lo, in rows of 2 mp bytes (a column each) without
 // padding (three of 64 x 64 let three workgroups share a CU). The 16-byte
 // chunks of a row are exchanged so that the same chunk of 16 rows in turn lies
 // in all banks.
@@ -622,59 +660,34 @@ __device__ __forceinline__ int chunk_at(int row, int c) {
   return row * (8 * n) + ((c ^ (MT == 1 ? row >> 2 : MT == 2 ? row >> 1 : row)) & (n - 1)) * 8;
 }
 template <int MT>
-__device__ __forceinline__ f16x8 frag_sq(const _Float16* x, int row, int k, int lane) {
-  return *reinterpret_cast<const f16x8*>(x + chunk_at<MT>(row + (lane & 31), (k >> 3) + (lane >> 5)));
-}
-
-// acc = X Y^T, and with TWO also bcc = Z Y^T, for the matrices as they are
-// stored.
-template <int MT, bool TWO>
-__device__ __forceinline__ void mul_sq(const _Float16* x, const _Float16* z, const _Float16* y, f32x16 (&acc)[Cfg<MT>::tiles], f32x16 (&bcc)[Cfg<MT>::tiles],
-                                       int wave, int lane) {
-  typedef Cfg<MT> C;
-  constexpr int lo = C::mp * C::mp, kUnroll = MT == 4 ? 2 : 4;
-  int ti, tj;
-  tile_of<MT>(wave, ti, tj);
-  f32x16 a[C::tiles] = {}, b[C::tiles] = {};  // (acc may be x's or z's own value)
-  if (MT > 1 || wave == 0) {
-#pragma unroll kUnroll
-    for (int k = 0; k < C::mp; k += 16) {
-      const f16x8 xh = frag_sq<MT>(x, 32 * ti, k, lane), xl = frag_sq<MT>(x + lo, 32 * ti, k, lane);
-      f16x8 zh, zl;
-      if (TWO) zh = frag_sq<MT>(z, 32 * ti, k, lane), zl = frag_sq<MT>(z + lo, 32 * ti, k, lane);
+__device__ __forceinline__ void put_own(_Float16* x, const Own<MT>& v, int wave, int lane) {
+  typedef Sq<MT> Q;
 #pragma unroll
-      for (int t = 0; t < C::tiles; ++t) {
-        const f16x8 yh = frag_sq<MT>(y, 32 * (tj + t), k, lane), yl = frag_sq<MT>(y + lo, 32 * (tj + t), k, lane);
-        a[t] = mul3(xh, xl, yh, yl, a[t]);
-        if (TWO) b[t] = mul3(zh, zl, yh, yl, b[t]);
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < C::tiles; ++t) {
-    acc[t] = a[t];
-    if (TWO) bcc[t] = b[t];
+  for (int s = 0; s < Q::steps; ++s) {
+    const int at = chunk_at<MT>(16 * wave + (lane & 15), 4 * s + (lane >> 4));
+    *reinterpret_cast<f16x8*>(x + at) = v.h[s];
+    *reinterpret_cast<f16x8*>(x + Q::mp * Q::mp + at) = v.l[s];
   }
 }
-
+// The own columns of Y^T X: Y from LDS, the own columns of X.
 template <int MT>
-__device__ __forceinline__ void put_sq(_Float16* x, const f32x16 (&v)[Cfg<MT>::tiles], float scale, int wave, int lane) {
-  typedef Cfg<MT> C;
-  int ti, tj;
-  tile_of<MT>(wave, ti, tj);
-  if (MT == 1 && wave > 0) return;
+__device__ __forceinline__ void mul_own(const _Float16* y, const Own<MT>& x, Acc<MT>& acc, int lane) {
+  typedef Sq<MT> Q;
 #pragma unroll
-  for (int t = 0; t < C::tiles; ++t)
+  for (int t = 0; t < Q::tiles; ++t) acc.t[t] = f32x4{};
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      uint2 h, l;
-      split2(v[t][4 * g] * scale, v[t][4 * g + 1] * scale, h.x, l.x);
-      split2(v[t][4 * g + 2] * scale, v[t][4 * g + 3] * scale, h.y, l.y);
-      // row 32 (tj + t) + lane % 32, columns from 32 ti + 8 g + 4 (lane / 32)
-      const int at = chunk_at<MT>(32 * (tj + t) + (lane & 31), 4 * ti + g) + 4 * (lane >> 5);
-      *reinterpret_cast<uint2*>(x + at) = h;
-      *reinterpret_cast<uint2*>(x + C::mp * C::mp + at) = l;
+  for (int s = 0; s < Q::steps; ++s) {
+    // (128 rows: else the loads of all steps are hoisted, and registers spilled)
+    if (MT == 4 && s % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < Q::tiles; ++t) {
+      const int at = chunk_at<MT>(16 * t + (lane & 15), 4 * s + (lane >> 4));
+      const f16x8 yh = *reinterpret_cast<const f16x8*>(y + at), yl = *reinterpret_cast<const f16x8*>(y + Q::mp * Q::mp + at);
+      acc.t[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(yh, x.h[s], acc.t[t], 0, 0, 0);
+      acc.t[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(yh, x.l[s], acc.t[t], 0, 0, 0);
+      acc.t[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(yl, x.h[s], acc.t[t], 0, 0, 0);
     }
+  }
 }
 
 // What makes X of u: sigma, and the exponent it is scaled for.
@@ -684,24 +697,22 @@ struct Norm {
 };
 
 // Phase solve: A from its parts, the norm (first run), the run's steps on A
-// and P. The matrices are symmetric but for rounding, and are stored
-// transposed (put_sq), so a product of two as stored is X^T Y. The order of
-// the factors matters for that rounding: T = A^T Q, A' = T^T Q = Q^T A Q and P' =
-// P^T Q keep the antisymmetric part of A's errors from growing faster than the
-// rest (with T = Q^T A it grew by 14 in every step of the quintic: X off by
-// 4e-4 after five steps on full-rank 64 x 768, 1e-5 in this order). P goes to
-// out: mp x mp hi, then lo, in rows of `stride` halves.
+// and P. The matrices are symmetric but for rounding. The order of the factors
+// matters for that rounding: T = A^T Q, A' = T^T Q = Q^T A Q and P' = P^T Q keep
+// the antisymmetric part of A's errors from growing faster than the rest (with
+// T = Q^T A it grew by 14 in every step of the quintic: X off by 4e-4 after five
+// steps on full-rank 64 x 768, 1e-5 in this order). P goes to out: mp x mp hi,
+// then lo, in rows of `stride` halves.
 template <int MT>
 __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, char* lds, _Float16* out, int stride, Norm& norm) {
-  typedef Cfg<MT> C;
+  typedef Sq<MT> Q;
   const int run = A.run, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  _Float16* const la = reinterpret_cast<_Float16*>(lds);  // A, T
-  _Float16* const lq = la + C::square;                    // Q
-  _Float16* const lp = MT == 4 ? la : lq + C::square;     // P (mp = 128: where A was, for its product)
-  __shared__ float red[C::waves];
-  int ti, tj;
-  tile_of<MT>(wave, ti, tj);
-  const bool mine = MT != 1 || wave == 0;
+  constexpr int kSquare = Cfg<MT>::square;
+  _Float16* const la = reinterpret_cast<_Float16*>(lds);  // A
+  _Float16* const lt = la + kSquare;                      // T
+  _Float16* const lp = MT == 4 ? la : lt + kSquare;       // P (mp = 128: where A was, for its product)
+  __shared__ float red[Q::waves];
+  const bool mine = wave < Q::waves;  // (with mp = 32 a workgroup may have more)
   const int32_t* const exps = reinterpret_cast<const int32_t*>(A.ws + M.exp_off);
   int e = kXExp;
   if (run == 0) {
@@ -709,53 +720,59 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, char* l
     for (int p = lane; p < M.parts; p += 64) top = max(top, exps[p] + 126);
     e = wave_max(top) - 126;
   }
-  f32x16 a[C::tiles] = {}, pr[C::tiles] = {}, q[C::tiles], acc[C::tiles];
+  Acc<MT> acc;
+#pragma unroll
+  for (int t = 0; t < Q::tiles; ++t) acc.t[t] = f32x4{};
   const float4* const in = reinterpret_cast<const float4*>(A.ws + gram_at<MT>(M, run));
   constexpr int kJoin = MT == 4 ? 2 : 4;  // parts on their way at once
+  // the four rows from row_of(s, 4 u): put_gram's tile (r / 32, column / 32), its g and lane
+  auto place = [&](int s, int u) {
+    const int r = row_of(s, 4 * u, lane), c = 16 * wave + (lane & 15);
+    return ((MT * (r >> 5) + (c >> 5)) * 4 + (r >> 3 & 3)) * 64 + (r >> 2 & 1) * 32 + (c & 31);
+  };
   if (mine)
     for (int p = 0; p < M.parts; p += kJoin) {
-      float4 x[kJoin][C::tiles][4];
+      float4 x[kJoin][Q::steps][2];
       int shift[kJoin];
 #pragma unroll
       for (int j = 0; j < kJoin; ++j) {
         const int q = min(p + j, M.parts - 1);
         shift[j] = run == 0 ? 2 * (exps[q] - e) : 0;
 #pragma unroll
-        for (int t = 0; t < C::tiles; ++t)
+        for (int s = 0; s < Q::steps; ++s)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) x[j][t][g] = in[int64_t(q) * (C::mp * C::mp / 4) + ((wave * C::tiles + t) * 4 + g) * 64 + lane];
+          for (int u = 0; u < 2; ++u) x[j][s][u] = in[int64_t(q) * (Q::mp * Q::mp / 4) + place(s, u)];
       }
 #pragma unroll
       for (int j = 0; j < kJoin; ++j)
         if (p + j < M.parts)
 #pragma unroll
-          for (int t = 0; t < C::tiles; ++t)
+          for (int s = 0; s < Q::steps; ++s)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              a[t][4 * g] += ldexpf(x[j][t][g].x, shift[j]);
-              a[t][4 * g + 1] += ldexpf(x[j][t][g].y, shift[j]);
-              a[t][4 * g + 2] += ldexpf(x[j][t][g].z, shift[j]);
-              a[t][4 * g + 3] += ldexpf(x[j][t][g].w, shift[j]);
+            for (int u = 0; u < 2; ++u) {
+              acc.set(s, 4 * u, acc.get(s, 4 * u) + ldexpf(x[j][s][u].x, shift[j]));
+              acc.set(s, 4 * u + 1, acc.get(s, 4 * u + 1) + ldexpf(x[j][s][u].y, shift[j]));
+              acc.set(s, 4 * u + 2, acc.get(s, 4 * u + 2) + ldexpf(x[j][s][u].z, shift[j]));
+              acc.set(s, 4 * u + 3, acc.get(s, 4 * u + 3) + ldexpf(x[j][s][u].w, shift[j]));
             }
     }
-  // the identity's elements of this lane, for a I
-  auto diag = [&](int t, int i) { return ti == tj + t && acc_row(i >> 2, lane) + (i & 3) == (lane & 31); };
+  auto diag = [&](int s, int k) { return row_of(s, k, lane) == 16 * wave + (lane & 15); };
   float scale = 1.f / (kAScale * kAScale);  // X was scaled by 2^kXExp
   if (run == 0) {
     // the trace is the sum of squares
     float d = 0.f;
 #pragma unroll
-    for (int t = 0; t < C::tiles; ++t)
+    for (int s = 0; s < Q::steps; ++s)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (mine && diag(t, i)) d += a[t][i];
+      for (int k = 0; k < 8; ++k)
+        if (diag(s, k)) d += acc.get(s, k);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) d += __shfl_xor(d, o, 64);
-    if (lane == 0) red[wave] = d;
+    if (mine && lane == 0) red[wave] = d;
     lds_barrier();
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < C::waves; ++w) sum += red[w];
+    for (int w = 0; w < Q::waves; ++w) sum += red[w];
     // sigma = 1 / ((norm + eps) 2^(kXExp - e)), whatever float32 makes of the norm; zeros give zeros
     const double size = ldexp(sqrt(double(sum)), e - kXExp);
     norm.sigma = sum == 0.f ? 0.f : static_cast<float>(1.0 / ldexp(size + double(A.eps), kXExp - e));
@@ -763,82 +780,69 @@ __device__ __forceinline__ void phase_solve(const Args& A, const Mat& M, char* l
     scale = norm.sigma * norm.sigma;
   }
 #pragma unroll
-  for (int t = 0; t < C::tiles; ++t)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) a[t][i] *= scale;
+  for (int t = 0; t < Q::tiles; ++t) acc.t[t] *= scale;
+  Own<MT> x, q, pr;  // A, Q and P
   const int steps = A.each + (run < A.more ? 1 : 0);
   if (steps == 0) {
 #pragma unroll
-    for (int t = 0; t < C::tiles; ++t)
+    for (int s = 0; s < Q::steps; ++s)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) pr[t][i] = diag(t, i) ? 1.f : 0.f;
+      for (int k = 0; k < 8; ++k) acc.set(s, k, diag(s, k) ? 1.f : 0.f);
+    pr.set(acc, kPScale);
   } else {
-    put_sq<MT>(la, a, kAScale, wave, lane);
+    x.set(acc, kAScale);
+    if (mine) put_own<MT>(la, x, wave, lane);
     lds_barrier();
   }
-  // products are of the matrices as stored: A = sa a, P = sp pr
   constexpr float kAA = 1.f / (kAScale * kAScale), kAQ = 1.f / (kAScale * kPScale), kPQ = 1.f / (kPScale * kPScale);
-  float sa = 1.f, sp = 1.f;
 #pragma unroll 1
   for (int i = 0; i < steps; ++i) {
     const bool more = i + 1 < steps;
-    mul_sq<MT, false>(la, la, la, acc, acc, wave, lane);
-    const float c = A.c * kAA, b = A.b * sa;
+    if (mine) {
+      mul_own<MT>(la, x, acc, lane);
+      const float b = A.b / kAScale, c = A.c * kAA;
 #pragma unroll
-    for (int t = 0; t < C::tiles; ++t)
+      for (int s = 0; s < Q::steps; ++s)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) q[t][j] = __fmaf_rn(c, acc[t][j], __fmaf_rn(b, a[t][j], diag(t, j) ? A.a : 0.f));
-    if (i == 0) {
-#pragma unroll
-      for (int t = 0; t < C::tiles; ++t) pr[t] = q[t];
-      if (!more) break;
-    }
-    put_sq<MT>(lq, q, kPScale, wave, lane);
-    if constexpr (MT != 4) {
-      if (i == 0) {
-        put_sq<MT>(lp, pr, kPScale, wave, lane);
-        lds_barrier();
-        mul_sq<MT, false>(la, la, lq, acc, acc, wave, lane);
-      } else {
-        lds_barrier();
-        sp = kPQ;
-        if (!more) {
-          mul_sq<MT, false>(lp, lp, lq, pr, pr, wave, lane);
-          break;
-        }
-        mul_sq<MT, true>(la, lp, lq, acc, pr, wave, lane);
-      }
-      lds_barrier();
-      put_sq<MT>(la, acc, kAQ * kAScale, wave, lane);
-      if (i > 0) put_sq<MT>(lp, pr, kPQ * kPScale, wave, lane);
-      lds_barrier();
-      mul_sq<MT, false>(la, la, lq, a, a, wave, lane);
-    } else {
-      lds_barrier();
+        for (int k = 0; k < 8; ++k) acc.set(s, k, __fmaf_rn(c, acc.get(s, k), __fmaf_rn(b, x.get(s, k), diag(s, k) ? A.a : 0.f)));
+      q.set(acc, kPScale);
+      if (i == 0) pr = q;
       if (more) {
-        mul_sq<MT, false>(la, la, lq, acc, acc, wave, lane);
-        lds_barrier();
-        put_sq<MT>(la, acc, kAQ * kAScale, wave, lane);
-        lds_barrier();
-        mul_sq<MT, false>(la, la, lq, a, a, wave, lane);
+        mul_own<MT>(la, q, acc, lane);
+        x.set(acc, kAQ * kAScale);
+        put_own<MT>(lt, x, wave, lane);
       }
-      if (i > 0) {
-        lds_barrier();
-        put_sq<MT>(lp, pr, sp * kPScale, wave, lane);
-        lds_barrier();
-        mul_sq<MT, false>(lp, lp, lq, pr, pr, wave, lane);
-        sp = kPQ;
-      }
-      if (!more) break;
     }
-    sa = kAQ;
-    lds_barrier();
-    put_sq<MT>(la, a, kAQ * kAScale, wave, lane);
+    if (i > 0) {
+      if (MT == 4) lds_barrier();  // A has been read
+      if (mine) put_own<MT>(lp, pr, wave, lane);
+    }
+    if (i > 0 || more) lds_barrier();
+    if (mine) {
+      if (i > 0) {
+        mul_own<MT>(lp, q, acc, lane);
+        pr.set(acc, kPQ * kPScale);
+      }
+      if (more) {
+        mul_own<MT>(lt, q, acc, lane);
+        x.set(acc, kAQ * kAScale);
+      }
+    }
+    if (!more) break;
+    if (MT == 4 && i > 0) lds_barrier();  // P has been read
+    if (mine) put_own<MT>(la, x, wave, lane);
     lds_barrier();
   }
   if (mine) {
+    const int c = 16 * wave + (lane & 15);
 #pragma unroll
-    for (int t = 0; t < C::tiles; ++t) put_acc(out, out + C::mp * stride, stride, 32 * ti, 32 * (tj + t), pr[t], sp * kPScale, lane);
+    for (int s = 0; s < Q::steps; ++s)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int at = c * stride + row_of(s, 4 * u, lane);
+        *reinterpret_cast<f16x4*>(out + at) = f16x4{pr.h[s][4 * u], pr.h[s][4 * u + 1], pr.h[s][4 * u + 2], pr.h[s][4 * u + 3]};
+        *reinterpret_cast<f16x4*>(out + Q::mp * stride + at) = f16x4{pr.l[s][4 * u], pr.l[s][4 * u + 1], pr.l[s][4 * u + 2], pr.l[s][4 * u + 3]};
+      }
   }
 }
 
@@ -1025,7 +1029,7 @@ __global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW)) void stack_
 }
 
 template <int MT>
-__global__ __launch_bounds__(Cfg<MT>::threads) void stack_solve_kernel(Args A, int first) {
+__global__ __launch_bounds__(Sq<MT>::threads) void stack_solve_kernel(Args A, int first) {
   extern __shared__ __align__(16) char lds[];
   const Mat M = A.mats[first + blockIdx.x];
   Norm norm = {};
@@ -1299,7 +1303,7 @@ muon_status run_phases(unsigned groups, int mats, int first, Args a, hipStream_t
   for (int run = 0; run < a.runs && st == MUON_OK; ++run) {
     a.run = run;
     if constexpr (!SOLVE) {
-      hipLaunchKernelGGL(stack_solve_kernel<MT>, dim3(unsigned(mats)), dim3(C::threads), C::lds_solve, s, a, first);
+      hipLaunchKernelGGL(stack_solve_kernel<MT>, dim3(unsigned(mats)), dim3(Sq<MT>::threads), C::lds_solve, s, a, first);
       if (hipGetLastError() != hipSuccess) return MUON_E_LAUNCH;
     }
     const bool last = run + 1 == a.runs;
