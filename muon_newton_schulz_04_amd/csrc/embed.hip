@@ -156,8 +156,21 @@ __device__ __forceinline__ void load_tokens(const I* tokens, int64_t i0, int64_t
     for (int u = 0; u < U; ++u) t[u] = tokens[min(i0 + 64 * u + lane, fin - 1)];
   }
 }
-__device__ __forceinline__ uint32_t unsigned_of(int32_t t) { return static_cast<uint32_t>(t); }
-__device__ __forceinline__ uint64_t unsigned_of(int64_t t) { return static_cast<uint64_t>(t); }
+// A token as 32 bits, all of them set for one that no vocabulary (at most 2^24
+// entries) has. Both passes of the sort test each token's range in as few
+// instructions as they can: every block reads the whole batch.
+__device__ __forceinline__ uint32_t narrow(int32_t t) { return static_cast<uint32_t>(t); }
+__device__ __forceinline__ uint32_t narrow(int64_t t) { return static_cast<uint64_t>(t) >> 32 ? ~0u : static_cast<uint32_t>(t); }
+// The first `left` of a wave's batch; none of the others is in a range.
+template <int U, typename I>
+__device__ __forceinline__ void narrow_all(const I (&t)[U], int left, int lane, uint32_t (&v)[U]) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) v[u] = narrow(t[u]);
+  if (left < 64 * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = 64 * u + lane < left ? v[u] : ~0u;
+  }
+}
 
 // k / d for magic = (2^32 - 1) / d: 2^32 - magic d lies in [1, d], so the
 // product's high word is the quotient or one less.
@@ -285,26 +298,26 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(SortArgs A) {
       to = stage == 0 ? before : behind;
     }
     const int pitch = stage == 1 ? W : 1;
-    I t[U], next[U];
+    I next[U];
     if (beg < fin) load_tokens(tokens, beg, fin, lane, next);
 #pragma unroll 1
     for (int64_t i0 = beg; i0 < fin; i0 += 64 * U) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) t[u] = next[u];
+      uint32_t v[U];
+      narrow_all(next, static_cast<int>(min(fin - i0, int64_t(64 * U))), lane, v);
       load_tokens(tokens, min(i0 + 64 * U, fin - 1), fin, lane, next);  // in flight meanwhile
-      const int left = static_cast<int>(min(fin - i0, int64_t(64 * U)));
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        // (a negative token is above all others as an unsigned number)
-        const bool there = 64 * u + lane < left;
-        under += __popcll(__ballot(there && unsigned_of(t[u]) < unsigned_of(I(lo))));
-        const auto k = unsigned_of(t[u]) - unsigned_of(I(lo));
-        if (there && k < unsigned_of(I(nk))) atomicAdd(to + static_cast<uint32_t>(k) * pitch, 1);
+        under += __popcll(__ballot(v[u] < static_cast<uint32_t>(lo)));
+        const uint32_t k = v[u] - lo;
+        if (k < static_cast<uint32_t>(nk)) atomicAdd(to + k * pitch, 1);
       }
     }
   }
   if (lane == 0) below[wave] = under;
   __syncthreads();
+
+  I ahead[U];  // the wave's first tokens to place, on their way during the scan
+  if (run0 < run1) load_tokens(tokens, run0, run1, lane, ahead);
 
   // Starts of the tokens: a scan over the keys of (count, is there any) in one 64-bit sum.
   int64_t carry = 0;
@@ -367,17 +380,17 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(SortArgs A) {
     int have = 0;
 #pragma unroll 1
     for (int64_t i0 = run0; i0 < run1; i0 += 64 * U) {
-      I t[U];
-      load_tokens(tokens, i0, run1, lane, t);
-      const int left = static_cast<int>(min(run1 - i0, int64_t(64 * U)));
+      uint32_t v[U];
+      narrow_all(ahead, static_cast<int>(min(run1 - i0, int64_t(64 * U))), lane, v);
+      load_tokens(tokens, min(i0 + 64 * U, run1 - 1), run1, lane, ahead);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const auto k = unsigned_of(t[u]) - unsigned_of(I(lo));
-        const bool in = 64 * u + lane < left && k < unsigned_of(I(nk));
+        const uint32_t k = v[u] - lo;
+        const bool in = k < static_cast<uint32_t>(nk);
         const uint64_t found = __ballot(in);
         if (in) {
           const int at = have + lanes_below(found, lane);
-          queue[at].x = static_cast<uint32_t>(k);
+          queue[at].x = k;
           queue[at].y = static_cast<uint32_t>(i0) + 64 * u + lane;
         }
         have += __popcll(found);
