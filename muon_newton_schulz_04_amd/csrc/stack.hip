@@ -21,7 +21,13 @@
 // A tile of X is mp x kCols (mp = m padded to 32, 64 or 128), in LDS as two
 // fp16 numbers hi + lo per element, rows along the product's inner dimension:
 // [m][k] for X X^T, [k][m] for P X. Products are hi hi + hi lo + lo hi with
-// v_mfma_f32_32x32x16_f16.
+// v_mfma_f32_32x32x16_f16 (16x16x32 in the solve).
+//
+// What bounds it: gram and last move every element's 6 and 8 bytes (bf16) and
+// are within 1.4 to 1.8 of a copy's time; without their products they take 38
+// for 41 and 46 for 47 us on 576 matrices of 64 x 768, without any LDS 37 and 46. The solve is matrix instructions, LDS reads and barriers in turn,
+// one workgroup for a matrix. In small sets the phases' chains of dependent
+// steps count: launch, record, first tile, and the solve's steps one by one.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -1016,6 +1022,9 @@ __device__ __forceinline__ void gram_any(const Args& A, const Mat& M, const Part
 
 // ----------------------------------------------------------------- kernels
 
+// Gradient and momentum read, the momentum written, parts' Gram matrices: 576
+// bf16 matrices of 64 x 768 (170 MB and 19 MB of parts) 40 us, 4.7 TB/s; 192 of
+// 128 x 2048 (302 MB and 25 MB) 83 us, 3.9 TB/s; 48 of 64 x 768 9 us.
 template <typename T, int MT, bool NARROW>
 __global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW)) void stack_gram_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
@@ -1028,6 +1037,9 @@ __global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW)) void stack_
   }
 }
 
+// Five quintic steps: 48 matrices of 64 rows 14.5 us (parts 4, a step 2), 576 in
+// two or three on each CU 28 us; 192 of 128 rows 60 us, a step 11, for which the
+// products alone (12 288 cycles a step) take 5 and their LDS reads 7.
 template <int MT>
 __global__ __launch_bounds__(Sq<MT>::threads) void stack_solve_kernel(Args A, int first) {
   extern __shared__ __align__(16) char lds[];
@@ -1037,7 +1049,10 @@ __global__ __launch_bounds__(Sq<MT>::threads) void stack_solve_kernel(Args A, in
   if (A.run == 0 && threadIdx.x == 0) *reinterpret_cast<Norm*>(A.ws + M.rec_off) = norm;
 }
 
-// SOLVE: each part's workgroup solves for P itself.
+// LAST with weights: 576 bf16 matrices of 64 x 768 (226 MB) 47 us, 4.9 TB/s; 192
+// of 128 x 2048 (403 MB) 95 us, 4.2 TB/s; 48 of 64 x 768, no weights, 8 us. With
+// 172 registers, so that two workgroups shared a CU and a third of them waited,
+// the first took 53. SOLVE: each part's workgroup solves for P itself.
 template <typename T, int MT, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS, bool SOLVE>
 __global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW || SOLVE)) void stack_apply_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
@@ -1134,8 +1149,15 @@ muon_status validate(const muon_stack* st, int32_t n, muon_dtype dtype, const mu
 // The tiles of a class, one matrix after the other, are dealt out in equal runs
 // to as many workgroups as run at once (three of 256 threads, two for narrow
 // matrices, or one of 512 on each of 256 CUs), but none is given fewer than kLeast tiles, or so few that a
-// matrix falls into more than kMaxParts parts.
-constexpr int64_t kMaxParts = 64, kLeast = 2;
+// matrix falls into more than kMaxParts parts. More workgroups than run at once
+// mean more parts, whose Gram matrices are written and added up again: gram and
+// update of 576 matrices of 64 x 768 take 41 + 47 us in 768 workgroups, 45 + 53
+// in 1152, 47 + 57 in 2304; of 192 of 128 x 2048 83 + 95 in 256, 102 + 118 in
+// 384, 92 + 108 in 768. kLeast 1, 2 and 4: 48 matrices of 64 x 768 31, 31 and 34
+// us, 96 of 16 x 765 56, 52 and 76. kMaxParts 16, 64 and 128: two of 65536 x 64
+// 208, 77 and 67 us, two of 128 x 65536 365, 171 and 174, eight of 32 x 32768 68,
+// 58 and 47.
+constexpr int64_t kMaxParts = 128, kLeast = 2;
 int64_t groups_of(int cls) { return cls == 3 ? 256 : cls == 0 ? 512 : 768; }
 // Matrices of mp = 32 that all run at once in two workgroups on each CU have
 // their P solved for by the workgroups that use it: the launch that this saves

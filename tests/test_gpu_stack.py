@@ -117,7 +117,7 @@ def test_step_in_parts(shape, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("shape", [(300, 8, 40), (260, 64, 200), (257, 200, 64), (257, 128, 130), (256, 130, 128), (256, 20, 515)], ids=str)
 def test_step_a_matrix_a_workgroup(shape, dtype):
-    """Enough matrices for the one-launch form."""
+    """Enough matrices for whole ones, and runs of several, to fall to a workgroup."""
     sample = (0, 1, 7, 100, shape[0] - 1)
     check(shape, dtype, sample=sample)
     check(shape, dtype, side=True, pad=1, offset=1, seed=3, sample=sample)
