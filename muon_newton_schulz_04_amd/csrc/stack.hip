@@ -1038,8 +1038,8 @@ __global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW)) void stack_
 }
 
 // Five quintic steps: 48 matrices of 64 rows 14.5 us (parts 4, a step 2), 576 in
-// two or three on each CU 28 us; 192 of 128 rows 60 us, a step 11, for which the
-// products alone (12 288 cycles a step) take 5 and their LDS reads 7.
+// two or three on each CU 28 us; 192 of 128 rows 60 us, a step 11, of which
+// the matrix cores are busy for 5 and the LDS for 3.5, in turns.
 template <int MT>
 __global__ __launch_bounds__(Sq<MT>::threads) void stack_solve_kernel(Args A, int first) {
   extern __shared__ __align__(16) char lds[];
