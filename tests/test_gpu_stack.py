@@ -349,6 +349,35 @@ def test_two_streams_with_a_workspace_each():
     assert all(torch.equal(a, o) for a, (_, o) in zip(want, sets))
 
 
+@pytest.mark.parametrize("shape", [(40, 16, 765), (180, 16, 765), (30, 64, 500), (5, 128, 900)], ids=str)
+def test_two_graphs_of_one_plan_at_once(shape):
+    """One plan, captured twice with a workspace each, replayed at once on two streams: several runs of steps (fp32), no
+    state in the plan."""
+    gen = torch.Generator().manual_seed(12)
+    g, o = (view(*shape, "fp32", gen)[1] for _ in range(2))
+    plan = mu.StackPlan([g], None, [o])
+    cfg = config(CUBIC, 7, momentum=0.0)
+    plan.step(cfg)
+    torch.cuda.synchronize()
+    want = o.clone()
+    graphs, spaces = [], [torch.full((plan.workspace_bytes,), 255, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    for ws in spaces:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            plan.step(cfg, ws)
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for k in range(4):
+        o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want), k  # both write the same bits
+
+
 def test_call_refusals():
     g = torch.randn(2, 8, 40, device=DEV)
     b, o, w = torch.zeros_like(g), torch.full_like(g, 3.0), torch.zeros_like(g)
