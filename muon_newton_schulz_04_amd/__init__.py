@@ -237,6 +237,14 @@ def _ld(t) -> int:
     return t.stride(0) if rows > 1 else cols
 
 
+def _row_stride(t) -> int:
+    """_ld of a matrix whose rows must not share elements (as those of an expanded view do)."""
+    ld = _ld(t)
+    if ld < t.shape[1]:
+        raise ValueError("rows must not share elements: give a contiguous copy of a broadcast or overlapping view")
+    return ld
+
+
 def _matrices(grads, momenta, outs):
     """muon_matrix array (and dtype code) from lists of torch tensors."""
     n = len(grads)
@@ -863,18 +871,19 @@ class EmbeddingPlan:
     Tokens are int32 or int64 tensors of any contiguous shape; one outside [0, vocab) looks
     up zeros and carries no gradient. Activations (``out``, ``dout``) have the tokens' shape
     and ``cols`` behind it, in bf16 or float32 whatever the table's type, and rows at one
-    stride. A gradient needs a ``workspace``, allocated per call unless one is given; calls
-    that overlap in time need one each. Nothing waits for the device."""
+    stride that share no elements (a broadcast ``dout`` is refused: pass a contiguous copy).
+    A gradient needs a ``workspace``, allocated per call unless one is given; calls that
+    overlap in time need one each. Nothing waits for the device."""
 
     def __init__(self, table, max_tokens: int, exp_avg=None, exp_avg_sq=None, lr_mul: float = 1.0,
                  wd_mul: float = 1.0):
         import torch
         lib = load_library()
         self.handle = ctypes.c_void_p(None)
+        ld = _row_stride(table)
         if not table.is_cuda:
             raise ValueError("the table must be in device memory")
         self.dtype, self.device = _dtype_code(table), table.device
-        ld = _ld(table)
         for t in (exp_avg, exp_avg_sq):
             if t is None:
                 continue
@@ -886,7 +895,7 @@ class EmbeddingPlan:
         self.max_tokens = int(max_tokens)
         self._keep = (table, exp_avg, exp_avg_sq)
         self.workspace_bytes = muon_embed_workspace_bytes(self.vocab, self.cols, self.max_tokens)
-        t = MuonEmbedTable(self.vocab, self.cols, max(ld, self.cols), _ptr(table), _ptr(exp_avg), _ptr(exp_avg_sq),
+        t = MuonEmbedTable(self.vocab, self.cols, ld, _ptr(table), _ptr(exp_avg), _ptr(exp_avg_sq),
                            float(lr_mul), float(wd_mul))
         h = ctypes.c_void_p(None)
         with torch.cuda.device(self.device):
@@ -912,7 +921,7 @@ class EmbeddingPlan:
             y = x.flatten(0, -2) if x.dim() > 2 else x
             if y.dim() != 2 or y.data_ptr() != x.data_ptr():
                 raise ValueError("activations must be rows of consecutive elements at one row stride")
-            ld = max(_ld(y), self.cols)
+            ld = _row_stride(y)
         return MuonEmbedActs(x.data_ptr(), ld, dt, 0)
 
     def _rows(self, rows, values, count, need):
@@ -963,10 +972,10 @@ class EmbeddingPlan:
         t, d = self._tokens(tokens), self._acts(dout, tokens)
         if _dtype_code(grad) != self.dtype or grad.shape != self._keep[0].shape or grad.device != self.device:
             raise ValueError("grad must match the table's shape, type and device")
+        ld = _row_stride(grad)
         ws = self._ws(workspace, stream)
         self._call("muon_embed_plan_gradient", ctypes.byref(t), ctypes.byref(d), float(scale), grad.data_ptr(),
-                   max(_ld(grad), self.cols), 1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(),
-                   stream=stream)
+                   ld, 1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(), stream=stream)
         return grad
 
     def gradient_rows(self, tokens, dout, rows, values, count, scale: float = 1.0, workspace=None, stream=None):

@@ -86,3 +86,51 @@ def test_workspace_grows_with_the_batch(lib):
 def test_binding_refuses_host_tensors_and_wrong_types():
     with pytest.raises(ValueError):
         mu.EmbeddingPlan(torch.zeros(4, 4), 8)  # host memory
+
+
+def host_plan(vocab, cols):
+    """A plan of the binding without the library's: what the binding checks comes before any call."""
+    plan = object.__new__(mu.EmbeddingPlan)
+    plan.handle, plan.device, plan.dtype = ctypes.c_void_p(None), torch.device("cpu"), mu.MUON_F32
+    plan.vocab, plan.cols, plan.max_tokens, plan.workspace_bytes = vocab, cols, 64, 64
+    plan._keep = (torch.zeros(vocab, cols), None, None)
+    return plan
+
+
+def shared_rows(n, cols):
+    """Views of n rows of cols elements whose rows share elements: broadcast ones, overlapping ones, and the gradient that
+    autograd hands to what a sum over the rows was taken of."""
+    leaf = torch.zeros(n, cols, requires_grad=True)
+    views = [torch.ones(cols).expand(n, cols), torch.ones(1, cols).expand(n, cols),
+             torch.autograd.grad((leaf + 0).sum(0), leaf, torch.ones(cols))[0]]
+    if cols > 1:
+        views.append(torch.ones(n + cols).as_strided((n, cols), (1, 1)))
+        views.append(torch.ones(n * cols).as_strided((n, cols), (cols - 1, 1)))
+    assert all(v.stride(0) < cols and v.shape == (n, cols) for v in views)
+    return views
+
+
+@pytest.mark.parametrize("cols", [1, 2, 8])
+def test_rows_that_share_elements_are_refused(cols):
+    plan, tok = host_plan(6, cols), torch.zeros(5, dtype=torch.int64)
+    good = torch.zeros(5, cols)
+    for x in shared_rows(5, cols):
+        for call in (lambda: plan.lookup(tok, x), lambda: plan.gradient(tok, x, torch.zeros(6, cols)),
+                     lambda: plan.gradient_rows(tok, x, torch.zeros(5, dtype=torch.int32), good.clone(), torch.zeros(1, dtype=torch.int32))):
+            with pytest.raises(ValueError, match="share"):
+                call()
+    for x in shared_rows(6, cols):
+        with pytest.raises(ValueError, match="share"):
+            mu.EmbeddingPlan(x, 4)
+        with pytest.raises(ValueError, match="share"):
+            plan.gradient(tok, good, x)
+    # tokens of two dimensions: a broadcast of all rows
+    tok2, x = torch.zeros(2, 5, dtype=torch.int64), torch.ones(cols).expand(2, 5, cols)
+    with pytest.raises(ValueError, match="share"):
+        plan.lookup(tok2, x)
+    with pytest.raises(ValueError):
+        plan.lookup(tok2, torch.ones(5, cols).expand(2, 5, cols))
+    # one row, or none, shares nothing
+    for n in (0, 1):
+        assert plan._acts(torch.ones(cols).expand(n, cols), torch.zeros(n, dtype=torch.int64)).ld == cols
+    assert plan._acts(torch.zeros(5, cols + 3)[:, :cols], tok).ld == cols + 3

@@ -459,3 +459,26 @@ def test_many_tokens():
     # a run of 64 terms is summed in turn, then up to 2^11 runs' sums, four lists of them: 64 + 2^9 + 4 additions deep at most
     depth = 64 + 512 + 4
     assert bool(((g.double() - want).abs() <= depth * 2.0 ** -24 * 1.001 * mag + 2.0 ** -24 * want.abs()).all())
+
+
+def test_gradient_of_a_broadcast_dout():
+    """Rows that share elements are refused; a copy of them gives the gradient (that of a sum over the lookup's rows)."""
+    vocab, cols = 6, 40
+    e = torch.zeros(vocab, cols, device=DEV)
+    tok = torch.tensor([0, 3, 3, -1, 5, 3], device=DEV)
+    plan = mu.EmbeddingPlan(e, 6)
+    row = torch.arange(cols, dtype=torch.float32, device=DEV)
+    leaf = torch.zeros(6, cols, device=DEV, requires_grad=True)
+    d = torch.autograd.grad((leaf + 0).sum(0), leaf, row)[0]
+    assert d.stride() == (0, 1)
+    g = torch.full_like(e, 7.0)
+    rows, vals = torch.zeros(6, dtype=torch.int32, device=DEV), torch.zeros(6, cols, device=DEV)
+    count = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for call in (lambda: plan.gradient(tok, d, g), lambda: plan.gradient_rows(tok, d, rows, vals, count), lambda: plan.lookup(tok, d),
+                 lambda: plan.gradient(tok, d.contiguous(), row.expand(vocab, cols)), lambda: mu.EmbeddingPlan(row.expand(vocab, cols), 6)):
+        with pytest.raises(ValueError):
+            call()
+    assert bool((g == 7.0).all()) and not rows.any() and not count.any()
+    plan.gradient(tok, d.contiguous(), g)
+    assert torch.equal(g, torch.tensor([1.0, 0, 0, 3, 0, 1], device=DEV)[:, None] * row)
+    plan.destroy()
