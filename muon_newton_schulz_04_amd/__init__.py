@@ -809,11 +809,14 @@ class ClipPlan:
     def set_live_rows(self, index: int, count, cols: Optional[int] = None):
         """Tensor ``index`` holds rows of ``cols`` elements (its last dimension unless given), of
         which later calls take the first ``count``, a one-element int32 tensor on the plan's device
-        that is read when they run; the rows behind it are neither read nor written. None: all rows."""
+        that is read when they run; the rows behind it are neither read nor written. The tensor must
+        be contiguous. None: all rows."""
         import torch
         g = self._keep[0][index]
         if count is not None and (count.dtype != torch.int32 or count.numel() != 1 or count.device != self.device):
             raise ValueError("the number of live rows is one int32 element on the plan's device")
+        if count is not None and not g.is_contiguous():
+            raise MuonError(3, "muon_clip_plan_set_live_rows")  # (a permuted dense tensor is one row to the library)
         cols = (g.shape[-1] if g.dim() else 1) if cols is None else int(cols)
         index = index % self.n
         with torch.cuda.device(self.device):

@@ -287,3 +287,15 @@ def test_overlaps_against_every_byte():
             ts += [rect(B, ld, r0, n, a, b - a, rng.random() < 0.7) for r0, n in ((at, mid - at), (mid, rows - mid)) if n]
         order = rng.permutation(len(ts))
         assert not meets(ts) and status([ts[i] for i in order])[0] == 0
+
+
+def test_live_rows_need_rows_one_behind_another():
+    """A permuted dense tensor is one run of memory to the norm, but its first rows are not the run's beginning."""
+    plan = object.__new__(mu.ClipPlan)  # what the binding checks comes before any call
+    plan.handle, plan.device, plan.n = ctypes.c_void_p(None), torch.device("cpu"), 3
+    plan._keep = ([torch.zeros(8, 4).t(), torch.zeros(2, 3, 4).transpose(0, 1), torch.zeros(4, 9)[:, :8]], None)
+    count = torch.zeros(1, dtype=torch.int32)
+    for i in range(3):
+        with pytest.raises(mu.MuonError) as exc:
+            plan.set_live_rows(i, count)
+        assert exc.value.code == 3

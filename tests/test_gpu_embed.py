@@ -482,3 +482,15 @@ def test_gradient_of_a_broadcast_dout():
     plan.gradient(tok, d.contiguous(), g)
     assert torch.equal(g, torch.tensor([1.0, 0, 0, 3, 0, 1], device=DEV)[:, None] * row)
     plan.destroy()
+
+
+def test_live_rows_of_a_permuted_tensor_are_refused():
+    x = torch.randn(6, 4, device=DEV)
+    count = torch.ones(1, dtype=torch.int32, device=DEV)
+    plan = mu.ClipPlan([x.t()], [None])
+    with pytest.raises(mu.MuonError) as exc:
+        plan.set_live_rows(0, count)
+    assert exc.value.code == 3
+    want = torch.linalg.vector_norm(x.double()).item()
+    assert abs(plan.norm()[0].item() - want) <= 2.0 ** -23 * want  # all of it, as before
+    plan.destroy()
