@@ -27,14 +27,12 @@
 
 #include "../../include/muon_embed.h"
 #include "adam_elem.hpp"
+#include "embed_grid.hpp"
 
 namespace muon_embed {
 
 using muon_adam::kVec;
 
-constexpr int kThreads = 256;
-constexpr int kLookVec = 8;        // consecutive elements per thread of the lookup
-constexpr int kLookRuns = 4;       // such vectors per thread, kThreads apart
 constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortLoads = 8;      // tokens a lane has in flight
@@ -1054,12 +1052,13 @@ muon_status muon_embed_plan_lookup(muon_embed_plan* plan, const muon_embed_token
   a.n = n;
   a.vocab = static_cast<int32_t>(plan->t.vocab);
   a.cols = static_cast<int32_t>(plan->t.cols);
-  a.vpr = static_cast<int32_t>((plan->t.cols + kLookVec - 1) / kLookVec);
+  const LookGrid look = lookup_grid(plan->t.cols, n);
+  a.vpr = static_cast<int32_t>(look.vpr);
   a.magic = magic_of(a.vpr);
-  a.per = std::max(1, kThreads * kLookRuns / a.vpr);
+  a.per = static_cast<int32_t>(look.per);
   a.scale = scale;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const unsigned grid = unsigned((n + a.per - 1) / a.per);
+  const unsigned grid = unsigned(look.blocks);
   const bool w = tokens->wide != 0, f = plan->dtype == MUON_F32, of = out->dtype == MUON_F32;
   if (f && of) launch_lookup<float, float>(a, w, grid, s);
   else if (f) launch_lookup<float, uint16_t>(a, w, grid, s);

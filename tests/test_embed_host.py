@@ -2,6 +2,9 @@
 sizes and arguments that are refused before any device call, workspace sizes,
 and how the binding checks and lays out tensors."""
 import ctypes
+import itertools
+import os
+import subprocess
 
 import pytest
 import torch
@@ -134,3 +137,35 @@ def test_rows_that_share_elements_are_refused(cols):
     for n in (0, 1):
         assert plan._acts(torch.ones(cols).expand(n, cols), torch.zeros(n, dtype=torch.int64)).ld == cols
     assert plan._acts(torch.zeros(5, cols + 3)[:, :cols], tok).ld == cols + 3
+
+
+def test_lookup_grid_fits_a_launch(tmp_path):
+    """A launch holds under 2^32 threads, 2^24 - 1 blocks of 256. Every size that a plan accepts: all tokens have a block,
+    none is empty, and a block's vectors count within 32 bits."""
+    csrc = os.path.join(os.path.dirname(mu.__file__), "csrc")
+    src = tmp_path / "grid.cpp"
+    src.write_text("""#include <cstdio>
+#include "embed_grid.hpp"
+int main() {
+  long long cols, n;
+  while (std::scanf("%lld %lld", &cols, &n) == 2) {
+    const muon_embed::LookGrid g = muon_embed::lookup_grid(cols, n);
+    std::printf("%lld %lld %lld\\n", (long long)g.vpr, (long long)g.per, (long long)g.blocks);
+  }
+}
+""")
+    exe = str(tmp_path / "grid")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", f"-I{csrc}", str(src), "-o", exe], check=True)
+    slabs = lambda cols: (cols + 255) // 256  # noqa: E731
+    sizes = [(c, n) for c, n in itertools.product(
+        (1, 7, 8, 9, 768, 4095, 4096, 4097, 4104, 8191, 8192, 8193, 65535, 65536),
+        (1, 2, 255, 256, 1 << 20, (1 << 21) - 1, 1 << 21, (1 << 23) + 1, (1 << 24) - 2, (1 << 24) - 1, 1 << 24))
+        if (n + 63) // 64 * slabs(c) <= 1 << 23]
+    assert (4097, 1 << 24) in sizes and (8192, 1 << 24) in sizes
+    for c, n in sizes:
+        mu.muon_embed_workspace_bytes(1, c, n)  # accepted
+    out = subprocess.run([exe], input="\n".join(f"{c} {n}" for c, n in sizes), check=True, stdout=subprocess.PIPE, text=True).stdout
+    for (c, n), line in zip(sizes, out.splitlines(), strict=True):
+        vpr, per, blocks = map(int, line.split())
+        assert vpr == -(-c // 8) and blocks * 256 < 1 << 32, (c, n)
+        assert (blocks - 1) * per < n <= blocks * per and vpr * per < 1 << 31, (c, n)

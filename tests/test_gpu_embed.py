@@ -494,3 +494,23 @@ def test_live_rows_of_a_permuted_tensor_are_refused():
     want = torch.linalg.vector_norm(x.double()).item()
     assert abs(plan.norm()[0].item() - want) <= 2.0 ** -23 * want  # all of it, as before
     plan.destroy()
+
+
+def test_lookup_of_the_most_tokens_of_wide_rows():
+    """2^24 tokens of 4097 columns, where a block for each token would be more threads than a launch holds."""
+    n, cols, vocab = 1 << 24, 4097, 37
+    need = n * (2 * cols + 16) + (8 << 30)
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GB of free device memory")
+    e = torch.randn(vocab, cols, device=DEV).bfloat16()
+    tok = torch.randint(-1, vocab, (n,), device=DEV, dtype=torch.int32, generator=torch.Generator(device=DEV).manual_seed(1))
+    out = torch.empty(n, cols, dtype=torch.bfloat16, device=DEV)
+    plan = mu.EmbeddingPlan(e, n)
+    plan.lookup(tok, out)
+    rows = torch.cat([e, torch.zeros(1, cols, dtype=e.dtype, device=DEV)])  # (-1 is the last one)
+    step = 1 << 18
+    for i in range(0, n, step):
+        assert torch.equal(out[i:i + step], rows[tok[i:i + step].long()]), i
+    plan.destroy()
+    del out
+    torch.cuda.empty_cache()
