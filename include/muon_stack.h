@@ -67,9 +67,11 @@ extern "C" {
  * The matrices of a stack must be apart: blocks one behind another (stride >=
  * a matrix's span, (rows - 1) * ld + cols) or side by side in the columns of
  * one matrix (stride >= cols, (count - 1) * stride + cols <= ld).
- * Otherwise nothing written may overlap anything else of the plan, column
- * slices at one row stride being told apart by their columns
- * (MUON_E_INVALID). */
+ * Otherwise nothing written may overlap anything else of the plan
+ * (MUON_E_INVALID). Stacks may lie in one buffer in turn, matrix by matrix, and
+ * column slices at one row stride are told apart by their columns; matrices
+ * of different row strides whose rows lie between each other's count as
+ * overlapping. */
 typedef struct {
   int64_t count;
   int64_t rows;

@@ -1095,19 +1095,27 @@ struct Host {
 
 bool empty(const muon_stack& s) { return s.count == 0 || s.rows == 0 || s.cols == 0; }
 
-// Whether a stack's matrices are apart, and the place of all of them in memory.
+// Whether a stack's matrices are apart, and the place of each of them in
+// memory. Those that follow each other without a gap, in rows or in columns,
+// are one place; between others there may be matrices of another stack.
 bool apart(const muon_stack& s, int64_t ld, int64_t stride, const void* p, bool write, int64_t es,
            std::vector<muon::tensor_overlap::Interval>* iv) {
   const int64_t span = (s.rows - 1) * ld + s.cols, all = (s.count - 1) * stride + span;
   const bool blocks = s.count == 1 || stride >= span;
-  const bool side = s.count > 1 && !blocks && stride >= s.cols && (s.count - 1) * stride + s.cols <= ld;
+  const bool side = !blocks && stride >= s.cols && (s.count - 1) * stride + s.cols <= ld;
   if (!blocks && !side) return false;
-  int64_t width = all, step = 0;  // one solid run
-  if (side) width = (s.count - 1) * stride + s.cols, step = s.rows > 1 ? ld : 0;
-  else if (ld > s.cols && (s.count == 1 || stride % ld == 0) && all > s.cols) width = s.cols, step = ld;
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
   if (lo > UINTPTR_MAX - static_cast<uintptr_t>(all * es)) return false;
-  iv->push_back({lo, lo + static_cast<uintptr_t>(all * es), static_cast<uintptr_t>(width * es), static_cast<uintptr_t>(step * es), write});
+  int64_t count = s.count, rows = s.rows, cols = s.cols;
+  if (blocks && (count == 1 || stride == rows * ld)) rows *= count, count = 1;
+  else if (side && stride == cols) cols *= count, count = 1;
+  const bool solid = rows == 1 || ld == cols;  // no gaps between the rows
+  const int64_t size = (rows - 1) * ld + cols;
+  for (int64_t t = 0; t < count; ++t) {
+    const uintptr_t at = lo + static_cast<uintptr_t>(t * stride * es);
+    iv->push_back({at, at + static_cast<uintptr_t>(size * es), static_cast<uintptr_t>((solid ? size : cols) * es),
+                   static_cast<uintptr_t>((solid ? 0 : ld) * es), write});
+  }
   return true;
 }
 

@@ -460,3 +460,37 @@ def test_one_training_step_of_heads_and_embedding():
             want = w[t].numpy() * f32(1 - np.float32(f32(0.02)) * np.float32(f32(0.01))) - f32(0.02) * x
             off = np.maximum(np.abs(to_f64(w1[t]) - want) - 2.0 ** -8 * np.abs(want) - 2.0 ** -23 * (np.abs(w[t].numpy()) + np.abs(x)), 0.0)
             assert np.linalg.norm(off) <= TOL * f32(0.02) * np.linalg.norm(x)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_interleaved_stacks_in_one_plan(dtype):
+    """q, k and v of [layers, 3, rows, cols] buffers, and adapter factors one behind another, as stacks of one plan: the
+    bits of a plan each on copies, weights among them."""
+    gen = torch.Generator().manual_seed(8)
+    rand = lambda *s: torch.randn(*s, generator=gen).to(TDT[dtype]).to(DEV)  # noqa: E731
+    layers, rows, cols, r, d = 5, 40, 96, 8, 72
+    flat = [rand(layers * (r * d + d * r)) for _ in range(4)]
+    fused = [rand(layers, 3, rows, cols) for _ in range(4)]
+    views = []  # per buffer (grad, momentum, out, weight): its stacks
+    for x, f in zip(fused, flat):
+        both = f.view(layers, 2 * r * d)
+        views.append([x[:, j] for j in range(3)] + [both[:, :r * d].view(layers, r, d), both[:, r * d:].view(layers, d, r)])
+    alone = [[v.clone() for v in stacks] for stacks in views]
+    plan = mu.StackPlan(*views[:3])
+    plan.set_weights(views[3])
+    plan.step(config())
+    plan.step_apply(config(), 0.02, 0.1)
+    for i in range(5):
+        own = mu.StackPlan(*[[a[i]] for a in alone[:3]])
+        own.set_weights([alone[3][i]])
+        own.step(config())
+        own.step_apply(config(), 0.02, 0.1)
+        for a, v in zip(alone, views):
+            assert torch.equal(a[i], v[i]), i
+        own.destroy()
+    first = views[3][0]
+    for w in (first, fused[3].view(-1)[rows * cols - 1:].as_strided(first.shape, first.stride())):
+        with pytest.raises(mu.MuonError) as exc:
+            plan.set_weights([first, w, *views[3][2:]])
+        assert exc.value.code == 1                         # the same weights twice, one element into the neighbour
+    plan.destroy()

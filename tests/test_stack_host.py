@@ -123,3 +123,66 @@ def test_binding_layouts():
         mu.muon_stack_workspace_bytes([a], None, [])
     with pytest.raises(ValueError):
         mu.StackPlan([a], None, [a])                                 # host memory
+
+
+def moved(s, elems, es=2):
+    """The same stack `elems` elements further in each of its buffers."""
+    return (*s[:5], *(p + es * elems for p in s[5:]))
+
+
+def test_interleaved_stacks(lib):
+    """Stacks whose matrices lie in turn in one buffer share nothing: [layers, 3, ..] projections, adapter factors one
+    behind another, [d, heads, 3, side] columns. One element into the neighbour they do."""
+    q = stack(count=4, stride=3 * 320)                                    # blocks of 8 x 40
+    assert status(lib, [moved(q, 320 * j) for j in range(3)]) == OK
+    assert status(lib, [q, moved(q, 319)]) == INVALID and status(lib, [q, moved(q, 641)]) == INVALID
+    a, b = stack(count=5, rows=16, cols=100, ld=100, stride=16 * 100 + 64 * 16), stack(count=5, rows=64, cols=16, ld=16, stride=16 * 100 + 64 * 16)
+    assert status(lib, [a, moved(b, 1600)]) == OK
+    assert status(lib, [a, moved(b, 1599)]) == INVALID and status(lib, [a, moved(b, 1601)]) == INVALID
+    # rows with a gap: the same columns in turn, and the columns of the gap
+    c = stack(count=3, rows=4, cols=40, ld=100, stride=1200)
+    assert status(lib, [moved(c, 400 * j) for j in range(3)]) == OK
+    assert status(lib, [moved(c, 400 * j + 40 * k) for j in range(3) for k in range(2)]) == OK
+    assert status(lib, [c, moved(c, 39)]) == INVALID and status(lib, [c, moved(c, 2 * 400 + 61), moved(c, 1)]) == INVALID
+    # columns of one matrix in turn
+    w = stack(count=4, rows=50, cols=8, ld=96, stride=24)
+    assert status(lib, [moved(w, 8 * j) for j in range(3)]) == OK
+    assert status(lib, [w, moved(w, 7)]) == INVALID and status(lib, [w, moved(w, 17)]) == INVALID
+
+
+def elements(s, base):
+    count, rows, cols, ld, stride = s[:5]
+    return {base + t * stride + i * ld + j for t in range(count) for i in range(rows) for j in range(cols)}
+
+
+def test_overlaps_against_every_element(lib):
+    """Pairs of small stacks in one buffer: what shares an element is refused, and where the two have one row stride, or
+    rows without gaps, what does not is accepted."""
+    rng = torch.Generator().manual_seed(0)
+    r = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=rng))  # noqa: E731
+    seen = {True: 0, False: 0}
+    for _ in range(3000):
+        ld, dense = r(4, 12), r(0, 1)
+        two = []
+        for _ in range(2):
+            rows, count = r(1, 4), r(1, 4)
+            cols = r(1, ld)
+            own = cols if dense else ld
+            span = (rows - 1) * own + cols
+            if not dense and r(0, 1) and cols * count <= ld:
+                stride = r(cols, (ld - cols) // max(1, count - 1)) if count > 1 else 0
+            else:
+                stride = r(span, 3 * span)
+            two.append((count, rows, cols, own, stride, r(0, 60)))
+        apart = [elements(t, t[5]) for t in two]
+        if any(len(e) != t[0] * t[1] * t[2] for e, t in zip(apart, two)):
+            continue
+        share = bool(apart[0] & apart[1])
+        got = status(lib, [stack(count=t[0], rows=t[1], cols=t[2], ld=t[3], stride=t[4], grad=(2 + i) * B, momentum=None, out=B + 2 * t[5])
+                           for i, t in enumerate(two)])
+        if share:
+            assert got == INVALID, two
+        elif dense:
+            assert got == OK, two
+        seen[got == OK] += 1
+    assert min(seen.values()) > 300
