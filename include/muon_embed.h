@@ -23,8 +23,10 @@
  * a token are not decayed and their moments do not fade.
  *
  * Arithmetic: out is the float32 product, rounded once to its type. Sums are
- * float32 in an order fixed by the batch's tokens (a token's positions
- * ascending, in runs whose sums are then added); a sum is multiplied by s and
+ * taken in an order fixed by the batch's tokens: a token's positions ascending,
+ * in float32 runs of at most 64, whose sums are added in float64, so that no
+ * sum is further off than 63 float32 roundings of what it adds up, however
+ * long. It is then rounded to float32, multiplied by s and
  * rounded once to the table's type (with `accumulate` after the float32
  * addition to what grad holds).
  *

@@ -15,7 +15,7 @@
 //    tokens they hold. A wave takes the columns of a slab through one chunk and
 //    writes the sum of each token that lies within it; a token that crosses a
 //    chunk's border leaves float32 partial sums, one per chunk.
-//  - join: adds a crossing token's partial sums in order.
+//  - join: adds a crossing token's partial sums in order, in float64.
 // Equal inputs give equal bits: no sum depends on which wave comes first.
 #include <hip/hip_runtime.h>
 
@@ -669,11 +669,14 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(SumArgs A) {
 
 // A token that crosses chunks: its first part, then one part of every later
 // chunk it reaches. Block (chunk, slab); the waves take the later parts in
-// turn, and their sums are added in order. 5 to 8 us, most of it the latency of
+// turn, and their sums are added in order, in float64: a token may have 2^18
+// parts, and a float32 sum that has outgrown them rounds each the same way (2^22
+// equal rows: off by 1.5e-4, in float64 by 6e-7, which is the runs' own; whole
+// calls 55.5 and 223 us with either). 5 to 8 us, most of it the latency of
 // finding out which block has something to add and of its few loads.
 template <typename G, int MODE>
 __global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs A) {
-  __shared__ float4 red[kThreads / 64 - 1][64];
+  __shared__ double red[kThreads / 64 - 1][kVec][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t chunk = blockIdx.x / A.slabs;
   const int slab = static_cast<int>(blockIdx.x - chunk * A.slabs);
@@ -686,11 +689,14 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs A) {
   if (c0 > 0 && before == r.key) return;  // began before this chunk: another block's
   const Cols l = cols_of(slab, lane, A.cols);
   const int64_t stop = (r.end - 1) / A.chunk;  // the last chunk it reaches
-  float acc[kVec] = {};
+  double acc[kVec] = {};
   constexpr int W = kThreads / 64, U = 8;
   if (l.nc > 0) {
     if (wave == 0) {
-      muon_adam::load4<false>(A.tail + chunk * A.ld_part + l.from, acc);
+      float x[kVec];
+      muon_adam::load4<false>(A.tail + chunk * A.ld_part + l.from, x);
+#pragma unroll
+      for (int q = 0; q < kVec; ++q) acc[q] = double(x[q]);
     }
     for (int64_t j0 = chunk + 1 + wave; j0 <= stop; j0 += W * U) {
       float x[U][kVec];
@@ -700,21 +706,25 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs A) {
       for (int u = 0; u < U; ++u) {
         if (j0 + u * W > stop) break;
 #pragma unroll
-        for (int q = 0; q < kVec; ++q) acc[q] += x[u][q];
+        for (int q = 0; q < kVec; ++q) acc[q] += double(x[u][q]);
       }
     }
   }
-  if (wave > 0) red[wave - 1][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  if (wave > 0)
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) red[wave - 1][q][lane] = acc[q];
   __syncthreads();
   if (wave > 0) return;
+  float sum[kVec];
 #pragma unroll
-  for (int w = 0; w < W - 1; ++w) {
-    const float4 t = red[w][lane];
-    acc[0] += t.x, acc[1] += t.y, acc[2] += t.z, acc[3] += t.w;
+  for (int q = 0; q < kVec; ++q) {
+#pragma unroll
+    for (int w = 0; w < W - 1; ++w) acc[q] += red[w][q][lane];
+    sum[q] = static_cast<float>(acc[q]);
   }
   int64_t row = r.key;
   if (MODE == kRows) row = distinct_in(A.distinct, 0, r.key / A.range, lane) + r.slot;
-  put<G, MODE>(A, row, l, acc);
+  put<G, MODE>(A, row, l, sum);
 }
 
 // ------------------------------------------------------------ Adam on rows

@@ -514,3 +514,28 @@ def test_lookup_of_the_most_tokens_of_wide_rows():
     plan.destroy()
     del out
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("form", ["dense", "added", "rows"])
+@pytest.mark.parametrize("n", [1 << 16, 300_001, 1 << 22])
+def test_sums_of_one_frequent_token(n, form):
+    """Equal rows, whose partial sums are all rounded the same way once a float32 sum outgrows them. Runs of 64 terms leave
+    63 roundings of 2^-24 of the sum of magnitudes; adding the runs' sums in float64 (under 2^19 of them) under 2^-34 of
+    it; then the roundings to float32, of the product and of the addition."""
+    cols = 12
+    e = torch.zeros(4, cols, device=DEV)
+    row = torch.linspace(0.1, 1.2, cols, device=DEV)
+    d = row.repeat(n, 1)
+    tok = torch.full((n,), 2, dtype=torch.int32, device=DEV)
+    want = n * row.double()
+    plan = mu.EmbeddingPlan(e, n)
+    if form == "rows":
+        rows, vals, count = torch.zeros(4, dtype=torch.int32, device=DEV), torch.zeros(4, cols, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+        got = plan.gradient_rows(tok, d, rows, vals, count)[1][0]
+        assert count.item() == 1 and rows[0].item() == 2
+    else:
+        got = plan.gradient(tok, d, torch.zeros_like(e), accumulate=form == "added")[2]
+    off = ((got.double() - want).abs() / want).max().item()
+    say(f"{n} equal rows, {form}: off by {off:.1e}")
+    assert off <= (63 + 3 + 2.0 ** -10) * 2.0 ** -24
+    plan.destroy()

@@ -156,8 +156,8 @@ def elements(s, base):
 
 
 def test_overlaps_against_every_element(lib):
-    """Pairs of small stacks in one buffer: what shares an element is refused, and where the two have one row stride, or
-    rows without gaps, what does not is accepted."""
+    """Pairs of small stacks in one buffer: what shares an element is refused, and where the rows
+    have no gaps, what does not is accepted."""
     rng = torch.Generator().manual_seed(0)
     r = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=rng))  # noqa: E731
     seen = {True: 0, False: 0}
