@@ -26,15 +26,26 @@
  * After s steps A is formed anew from X: s is chosen from the polynomial so
  * that rounding errors of A grow by less than 2^15 (bf16 sets) or 2^3 (fp32
  * sets) within a run of s (five and one steps for the usual quintic, thirteen
- * and three for the cubic).
+ * and three for the cubic). What that leaves of X stands below.
  *
  * Arithmetic: buf' is the exact mu * buf + G rounded once to the set's dtype,
  * as in muon.h; everything else is fp32. The products run on the matrix
  * cores with fp32 accumulation; every operand x is taken as two fp16 numbers,
  * x 2^e = hi + lo with |x 2^e - hi - lo| <= 2^-22 |x 2^e| (2^-24 for the
  * smallest, entries being scaled to at most 2^15), and a product as hi hi +
- * hi lo + lo hi, at about fp32's accuracy for both dtypes. Sums of squares
- * are kept relative to a power of two, so no finite u overflows them.
+ * hi lo + lo hi, for both dtypes. Sums of squares are kept relative to a power
+ * of two, so no finite u overflows them.
+ *
+ * Accuracy of X before its rounding, relative to its norm, five quintic steps,
+ * measured on shapes from 2 x 50 to 128 x 2048. fp32 sets: 4e-6 on random
+ * gradients, 7e-5 on gradients of rank one. bf16 sets, whose five steps come
+ * from one A: 5e-6 on random gradients (4e-5 on square ones), up to 6e-4 where
+ * singular values span two decades, a median of up to 1e-3 where they span
+ * three to five, and of 1.8e-3 on gradients of rank one, whose other singular
+ * values are the rounding of their entries; the worst of thousands of
+ * matrices 6.3e-3, with a short side of four (2.4e-3 with one of 64). The
+ * rounding of a bf16 output is 1.7e-3, and muon_plan_step on the same gradients
+ * is off by a median of 1.0e-3 to 3.1e-3 and by 5.8e-3 at worst before it.
  *
  * Conventions are those of muon.h: pointers are device memory owned by the
  * caller, arguments are validated before any work is enqueued (nothing is

@@ -494,3 +494,52 @@ def test_interleaved_stacks_in_one_plan(dtype):
             plan.set_weights([first, w, *views[3][2:]])
         assert exc.value.code == 1                         # the same weights twice, one element into the neighbour
     plan.destroy()
+
+
+# What a bf16 set leaves in X before its rounding. One rounding of A to its two fp16 numbers is LOW (3.3e-3) of X's norm
+# where X lies in directions of singular value near zero; in the same directions and to first order the first update of A
+# adds lo lo left out of A^T Q (2^-22, two roundings of 2^-23), T's rounding (0.7 3.44 / 11.86 = 0.2 of one), lo lo left out
+# of T^T Q (0.4), and all that follows under 0.4, being of an A whose largest eigenvalue is a half, grown by 11.86 less per
+# step: 4 in all, and float32's part of the sums of A up to 1 more. RAW is all of them at their largest and aligned. They
+# are independent, so a matrix in the middle of many has less than a third of it: 3.3e-3 again.
+RAW, RAW_MEDIAN = 5 * 3.3e-3, 3.3e-3
+
+
+def raw_x(g, momentum):
+    """(X before the output's rounding, X in float64): W <- W0 - X from W0 = bf16(X) is off by bf16's rounding of the
+    difference, 2^-17 of X. A zero buffer makes u a multiple of the gradient, so both forms have the same X."""
+    x = g.double()
+    x = x / (torch.linalg.matrix_norm(x)[:, None, None] + EPS)
+    tall = x.shape[1] > x.shape[2]
+    x = x.transpose(1, 2).contiguous() if tall else x
+    for _ in range(5):
+        a = x @ x.transpose(1, 2).contiguous()
+        x = QUINTIC[0] * x + (QUINTIC[1] * a + QUINTIC[2] * (a @ a)) @ x
+    x = x.transpose(1, 2).contiguous() if tall else x
+    w0 = x.to(g.dtype)
+    w = w0.clone()
+    plan = mu.StackPlan([g], [torch.zeros_like(g)] if momentum else None, [torch.empty_like(g)])
+    plan.set_weights([w])
+    plan.step_apply(config(momentum=MU if momentum else 0.0, nesterov=bool(momentum)), 1.0, 0.0)
+    torch.cuda.synchronize()
+    plan.destroy()
+    return w0.double() - w.double(), x
+
+
+@pytest.mark.parametrize("momentum", [False, True])
+@pytest.mark.parametrize("rows,cols", [(4, 300), (8, 100), (16, 765), (40, 100), (64, 768), (768, 64), (128, 300)])
+def test_x_of_bf16_sets_before_rounding(rows, cols, momentum):
+    gen = torch.Generator().manual_seed(rows)
+    count, m = 48, min(rows, cols)
+    rand = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    left, right = torch.linalg.qr(rand(count, rows, m))[0], torch.linalg.qr(rand(count, cols, m))[0].transpose(1, 2).contiguous()
+    for name, tol, middle, g in (
+            ("flat", TOL, TOL, 0.05 * rand(count, rows, cols)),
+            ("rank one", RAW, RAW_MEDIAN, rand(count, rows, 1) @ rand(count, 1, cols)),
+            ("rank two", RAW, RAW_MEDIAN, rand(count, rows, 2) @ rand(count, 2, cols)),
+            ("three decades", RAW, RAW_MEDIAN, left @ torch.diag(torch.logspace(0, -3, m)) @ right),
+            ("five decades", RAW, RAW_MEDIAN, left @ torch.diag(torch.logspace(0, -5, m)) @ right)):
+        got, want = raw_x(g.bfloat16().to(DEV), momentum)
+        off = torch.linalg.matrix_norm(got - want) / torch.linalg.matrix_norm(want)
+        say(f"{rows} x {cols} {name}: at most {off.max():.1e}, median {off.median():.1e}")
+        assert off.max() <= tol and off.median() <= middle
