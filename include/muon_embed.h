@@ -34,7 +34,9 @@
  * caller, arguments are validated before any work is enqueued, work is
  * asynchronous on `stream`, results are deterministic (equal inputs give
  * bitwise-equal outputs), NaN and infinities propagate, no call allocates
- * except plan creation, and every call can be captured into a graph.
+ * except plan creation, and every call can be captured into a graph. Buffers
+ * that must not overlap (MUON_E_INVALID) are taken from their first element to
+ * their last, the gaps between rows included.
  */
 #ifndef MUON_EMBED_H
 #define MUON_EMBED_H

@@ -106,8 +106,10 @@ typedef struct {
 
 typedef struct muon_stack_plan_s muon_stack_plan;
 
-/* Bytes of device workspace a step on these stacks needs (host only, no
- * device calls; 0 when all are empty). */
+/* Bytes of device workspace a step on these stacks needs, whatever its
+ * configuration (host only, no device calls; 0 when all are empty). Most of it
+ * is room for every X in float32, which a configuration whose steps are one run
+ * does not touch. */
 muon_status muon_stack_workspace_bytes(const muon_stack* stacks, int32_t n, muon_dtype dtype,
                                        size_t* bytes);
 

@@ -37,7 +37,7 @@ constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortLoads = 8;      // tokens a lane has in flight
 constexpr int kQueue = 64 * (kSortLoads + 1);  // of a wave: tokens found, not yet placed
-constexpr int kMaxRange = 3000;    // (a limit, reached from a vocabulary of 96000 on) vocabulary entries of a sort block: ten counters each, 117 of the 160 KB of LDS
+constexpr int kMaxRange = 3000;    // vocabulary entries of a sort block, at most: ten counters each, 117 of the 160 KB of LDS (reached where vocab * segments exceeds 3000 * kSortBlocks)
 constexpr int kSortBlocks = 256;   // sort blocks: one per CU
 constexpr int kSegment = 4096;     // tokens of a segment of the batch, at least
 constexpr int kSlab = 64 * kVec;   // columns of a wave in the sum
@@ -196,7 +196,7 @@ struct LookArgs {
 // them: some elements are written twice, with the same value. Loads are
 // without branches, so that all of a thread's are in flight at once: a token
 // outside the vocabulary loads row 0 and stores zeros. 8192 tokens of 768 bf16
-// elements 5.4 us; 65536 of 1021 fp32 ones to bf16 (142 MB read from HBM, 134
+// elements 5.4 us; 65536 of 1021 fp32 ones to bf16 (145 MB read from HBM, 134
 // written) 55.5 us, 5.0 TB/s (with 1, 2, 4 and 8 vectors in flight 58, 55, 55.5
 // and 56.5 us).
 template <typename E, typename O, typename I>

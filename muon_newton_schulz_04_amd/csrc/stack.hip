@@ -1023,8 +1023,9 @@ __device__ __forceinline__ void gram_any(const Args& A, const Mat& M, const Part
 // ----------------------------------------------------------------- kernels
 
 // Gradient and momentum read, the momentum written, parts' Gram matrices: 576
-// bf16 matrices of 64 x 768 (170 MB and 19 MB of parts) 40 us, 4.7 TB/s; 192 of
-// 128 x 2048 (302 MB and 25 MB) 83 us, 3.9 TB/s; 48 of 64 x 768 9 us.
+// bf16 matrices of 64 x 768 (170 MB and 19 MB of parts) 41 us, 4.6 TB/s; 192 of
+// 128 x 2048 (302 MB and 25 MB) 85 us (80 to 88 by run), 3.9 TB/s; 48 of 64 x 768
+// 9 us.
 template <typename T, int MT, bool NARROW>
 __global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW)) void stack_gram_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
@@ -1038,7 +1039,7 @@ __global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW)) void stack_
 }
 
 // Five quintic steps: 48 matrices of 64 rows 14.5 us (parts 4, a step 2), 576 in
-// two or three on each CU 28 us; 192 of 128 rows 60 us, a step 11, of which
+// two or three on each CU 28 us; 192 of 128 rows 58 to 63 us, a step 11, of which
 // the matrix cores are busy for 5 and the LDS for 3.5, in turns.
 template <int MT>
 __global__ __launch_bounds__(Sq<MT>::threads) void stack_solve_kernel(Args A, int first) {
@@ -1050,9 +1051,10 @@ __global__ __launch_bounds__(Sq<MT>::threads) void stack_solve_kernel(Args A, in
 }
 
 // LAST with weights: 576 bf16 matrices of 64 x 768 (226 MB) 47 us, 4.9 TB/s; 192
-// of 128 x 2048 (403 MB) 95 us, 4.2 TB/s; 48 of 64 x 768, no weights, 8 us. With
-// 172 registers, so that two workgroups shared a CU and a third of them waited,
-// the first took 53. SOLVE: each part's workgroup solves for P itself.
+// of 128 x 2048 (403 MB) 97 us (92 to 100 by run), 4.2 TB/s; 48 of 64 x 768, no
+// weights, 8 us. With 172 registers, so that two workgroups shared a CU and a
+// third of them waited, the first took 53. SOLVE: each part's workgroup solves
+// for P itself.
 template <typename T, int MT, bool NARROW, bool GRAD, bool LAST, bool WEIGHTS, bool SOLVE>
 __global__ __launch_bounds__(Cfg<MT>::threads, per_simd(MT, NARROW || SOLVE)) void stack_apply_kernel(Args A) {
   extern __shared__ __align__(16) char lds[];
@@ -1170,8 +1172,8 @@ int64_t groups_of(int cls) { return cls == 3 ? 256 : cls == 0 ? 512 : 768; }
 // Matrices of mp = 32 that all run at once in two workgroups on each CU have
 // their P solved for by the workgroups that use it: the launch that this saves
 // costs more than one wave's solve does in each of them (96 fp32 matrices of 16
-// x 765, four runs of steps: 69 us with, 58 us without it; 288 bf16 matrices of
-// 32 x 768, which take turns: 41 us with, 47 us without).
+// x 765, four runs of steps: 58 us with, 53 us without it; 288 bf16 matrices of
+// 32 x 768, which take turns: 37 us with, 41 us without).
 constexpr int64_t kSolveThere = 512;
 
 muon_status build(const muon_stack* st, int32_t n, muon_dtype dtype, Host* H) {
