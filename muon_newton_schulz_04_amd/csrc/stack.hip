@@ -1283,8 +1283,8 @@ std::vector<char> tables(const Host& H, const std::vector<Mat>& mats) {
 // the last factor q by |b / a| of what they have become: with A rounded to 2^-23
 // a run of five quintic steps leaves 1.39 11.86^4 2^-23 = 3.3e-3 of X for each
 // such rounding that lies in directions of singular value near zero. That is
-// what bf16 sets take (a median of 1.2e-3 to 1.8e-3 on gradients of rank one,
-// 3e-6 on random ones; a bf16 output's rounding is 1.7e-3): with runs of three
+// what bf16 sets take (a median of up to 1.8e-3 on gradients of rank one, 3e-6
+// on random ones; a bf16 output's rounding is 1.7e-3): with runs of three
 // and two steps X is off by 5e-5 at most on the same gradients, and 48 matrices
 // of 64 x 768 take 45 us for 31, 576 of them 175 for 115, 192 of 128 x 2048 332 for
 // 217. fp32 sets form A anew before errors have grown by eight. The slope and
